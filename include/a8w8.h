@@ -70,7 +70,11 @@ typedef enum {
 #define A8W8_DEVERR_TOKEN 0x8u       /* token id outside [0, vocab) */
 #define A8W8_DEVERR_POS 0x10u        /* RoPE position outside the table */
 #define A8W8_DEVERR_TIMEOUT 0x20u    /* a bounded wait on an asynchronous copy gave up */
-#define A8W8_DEVERR_ROW 0x40u        /* a8w8_prefill_step: last_rows entry outside [0, M) */
+#define A8W8_DEVERR_ROW 0x40u        /* a8w8_prefill_step: last_rows entry outside [0, M);
+                                      * page operations: a row outside [0, B) */
+#define A8W8_DEVERR_PAGES 0x80u      /* page operations: no free page was left */
+#define A8W8_DEVERR_ALIAS 0x100u     /* page operations: a page or row named twice, or a
+                                      * child row in use */
 
 /* Message of the last failed call on this host thread ("" if none). */
 const char* a8w8_last_error(void);
@@ -343,6 +347,140 @@ a8w8_status a8w8_prefill_layer_i8kv(const a8w8_layer_weights* w, const a8w8_conf
                                     float* k_scale, float* v_scale, const float* rope,
                                     int max_pos, void* ws, size_t ws_bytes,
                                     const a8w8_layer_taps* taps, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* 4-bit KV cache variant                                                    */
+/* ------------------------------------------------------------------------- */
+
+/* K/V cache rows held in 4 bits, for more cached tokens per byte than the
+ * INT8 variant; the source pages have no counterpart. A row is one KV head's
+ * D values of one token (D is 64 or 128), held as
+ *   codes [num_blocks * page_size, Hkv, D / 2] uint8: element 2j in the low,
+ *     2j + 1 in the high nibble of byte j,
+ *   meta [num_blocks * page_size, Hkv, 2] BF16: the pair (s, m),
+ * and standing for code * s + m: m = min x, s = bf16_rne((max x - m) / 15),
+ * code = clamp(rne((x - m) / s), 0, 15) (differences and quotients in IEEE
+ * float32; s = 0 gives codes 0). D / 2 + 4 bytes a row. A row holding a NaN or
+ * an infinity, or whose range max x - m overflows float32, has s = m = NaN and
+ * codes 0, and reads as NaN. */
+
+/* Quantises k, v ([T, Hkv, D] BF16) row by row into the 4-bit cache at
+ * slot_mapping[t]. slot < 0 skips the token; slot >= num_blocks * page_size
+ * is skipped and flags A8W8_DEVERR_SLOT. The slots >= 0 of one call are
+ * distinct (of two tokens with one slot, either may be held, or a mixture). */
+a8w8_status paged_kv_write_i4(const a8w8_bf16* k, const a8w8_bf16* v, int T, int Hkv, int D,
+                              const int32_t* slot_mapping, uint8_t* k_codes, uint8_t* v_codes,
+                              a8w8_bf16* k_meta, a8w8_bf16* v_meta, int num_blocks, int page_size,
+                              void* stream);
+
+/* Reads the rows at slot_mapping[t] back into k, v ([T, Hkv, D] BF16):
+ * bf16_rne of the float32 value code * s + m (code * s is exact). A slot may
+ * be named any number of times; slot < 0 gives rows of zeros, and so does
+ * slot >= num_blocks * page_size, which flags A8W8_DEVERR_SLOT. */
+a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
+                             const a8w8_bf16* k_meta, const a8w8_bf16* v_meta, int num_blocks,
+                             int page_size, const int32_t* slot_mapping, int T, int Hkv, int D,
+                             a8w8_bf16* k, a8w8_bf16* v, void* stream);
+
+/* paged_decode_attention_bf16 over the 4-bit cache. Same tables, shape rules
+ * and errors, with its own workspace (a8w8_attention_i4_workspace_bytes of
+ * the same B, Hq, Hkv, D and max_blocks * page_size; its contents need no
+ * initialisation), and in float32 arithmetic where the BF16 form is in
+ * two-float: the scores are float32 sums of exact products, the softmax
+ * weights are taken to 2^-12 of themselves (or 2^-16 of their request's
+ * largest weight * s, where that is more) before the products with the codes,
+ * and out is rounded to BF16 once. A token whose block id is outside [0,
+ * num_blocks) counts as a row of zeros and flags A8W8_DEVERR_BLOCK; a NaN row
+ * makes the heads that attend to it NaN. */
+a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
+                                        const uint8_t* v_codes, const a8w8_bf16* k_meta,
+                                        const a8w8_bf16* v_meta, const int32_t* block_table,
+                                        const int32_t* ctx_lens, int B, int Hq, int Hkv, int D,
+                                        int page_size, int max_blocks, int num_blocks,
+                                        float softmax_scale, a8w8_bf16* out, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+size_t a8w8_attention_i4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_ctx);
+
+/* ------------------------------------------------------------------------- */
+/* Pages of a cache                                                          */
+/* ------------------------------------------------------------------------- */
+
+/* Page management on the device, for serving loops that share pages between
+ * sequences (several samples of one prompt, a reused prefix) and give them
+ * back while others go on; the source pages leave it to the host. It serves
+ * every cache form of this library:
+ *   - the pool: num_caches device arrays (HOST array `caches`) of num_blocks
+ *     pages of page_bytes[c] bytes each (HOST array), for instance K and V of
+ *     every layer, or codes and scales; at most 256. page_bytes[c] is a
+ *     multiple of 4 * page_size below 2^31 (of 4 where a call takes no
+ *     page_size); pages of a multiple of 16 bytes move fastest.
+ *   - block_table [B, max_blocks], ctx_lens [B]: as the decode step reads
+ *     them; a negative table entry holds no page, and a row's pages stand at
+ *     its front. A row with context 0 and a negative first entry is free.
+ *   - refcount [num_blocks]: how many table entries hold the page; a page
+ *     whose count is 0 (or less) is free.
+ * Free pages are handed out lowest first, in the order of the call's list.
+ * Lists (device) may hold negative entries, which are skipped; an entry that
+ * cannot be carried out is skipped as a whole and flagged, the others are
+ * carried out. ws: a8w8_pages_workspace_bytes(num_blocks, B, n) bytes of device
+ * memory (n = 0 for paged_compact) that need no initialisation; calls that
+ * share a workspace, or a pool, must not overlap on the GPU. num_blocks is
+ * below 2^21 and max_blocks * page_size at most 2^24. */
+size_t a8w8_pages_workspace_bytes(int num_blocks, int B, int n);
+
+/* Copies page src[i] to page dst[i] in every cache, i < n. A pair with a
+ * negative page or src == dst does nothing. A page >= num_blocks is flagged
+ * A8W8_DEVERR_BLOCK; a pair whose destination is an earlier pair's destination
+ * or another pair's source is skipped and flagged A8W8_DEVERR_ALIAS, so the
+ * result does not depend on the order of the copies. */
+a8w8_status paged_copy_pages(void* const* caches, const size_t* page_bytes, int num_caches,
+                             int num_blocks, const int32_t* src, const int32_t* dst, int n,
+                             void* stream);
+
+/* Forks row parents[i] into the free row children[i], i < n: the child gets
+ * the parent's context; the full pages are shared (refcount + 1); of a page
+ * that the context fills in part, the tokens in use are copied in every cache
+ * to a free page of the child's own, so that both can go on writing; the rest
+ * of the child's table row becomes -1. A parent with context 0 leaves the
+ * child as it is. Tables are read as they stood before the call. Skipped and
+ * flagged: a row >= B (A8W8_DEVERR_ROW); a child that is in use or that an
+ * earlier entry names (A8W8_DEVERR_ALIAS); a parent's context or block id out
+ * of range (A8W8_DEVERR_CTX, _BLOCK); the forks left when no page is free
+ * (A8W8_DEVERR_PAGES; those that need none are carried out). */
+a8w8_status paged_fork(void* const* caches, const size_t* page_bytes, int num_caches,
+                       int num_blocks, int page_size, int32_t* block_table, int32_t* ctx_lens,
+                       int32_t* refcount, int B, int max_blocks, const int32_t* parents,
+                       const int32_t* children, int n, void* ws, size_t ws_bytes, void* stream);
+
+/* Gives row rows[i] pages for tokens[i] tokens, i < n: every negative one of
+ * its first ceil(tokens[i] / page_size) entries gets a free page (refcount 1);
+ * contexts and the pages that the row holds stay. A row that the free pages
+ * do not suffice for gets none (A8W8_DEVERR_PAGES), nor do the rows behind it
+ * that need some. Skipped and flagged: a row >= B (A8W8_DEVERR_ROW) or that an
+ * earlier entry names (A8W8_DEVERR_ALIAS); tokens[i] outside [0, max_blocks *
+ * page_size] (A8W8_DEVERR_CTX). */
+a8w8_status paged_reserve(int32_t* block_table, int32_t* refcount, int B, int max_blocks,
+                          int num_blocks, int page_size, const int32_t* rows,
+                          const int32_t* tokens, int n, void* ws, size_t ws_bytes, void* stream);
+
+/* Frees the listed rows: each page of rows[i] loses one reference, the row's
+ * entries become -1 and its context 0 (a row named twice is freed once). A
+ * row >= B flags A8W8_DEVERR_ROW; an entry >= num_blocks, or whose page was
+ * free already, flags A8W8_DEVERR_BLOCK and only leaves the table. */
+a8w8_status paged_free(int32_t* block_table, int32_t* ctx_lens, int32_t* refcount, int B,
+                       int max_blocks, int num_blocks, const int32_t* rows, int n, void* stream);
+
+/* Moves the pool's live pages to its front: with L live pages, the k-th live
+ * page numbered L or more moves, in every cache, to the k-th free page below
+ * L, and the counts and every entry of block_table follow. num_live (device
+ * [1], nullable) receives L: pages L and above are then free. A table entry
+ * that holds a free page numbered L or more, or one >= num_blocks, stays as it
+ * is and flags A8W8_DEVERR_BLOCK. */
+a8w8_status paged_compact(void* const* caches, const size_t* page_bytes, int num_caches,
+                          int num_blocks, int32_t* block_table, int32_t* refcount, int B,
+                          int max_blocks, int32_t* num_live, void* ws, size_t ws_bytes,
+                          void* stream);
 
 /* ------------------------------------------------------------------------- */
 /* BF16 (unquantised) layer variant                                          */

@@ -1,0 +1,404 @@
+"""The 4-bit KV cache: quantise-on-write, read-back and decode attention.
+
+On the CPU: the float64 oracle (oracle/kv_i4.py) against hand-computed rows,
+the C oracle's BF16 attention and its own invariants, and the refusals of the
+entry points. On the GPU: written codes and pairs bit for bit, read-back bit
+for bit, and attention within bounds derived from its arithmetic.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+import w8a8_quantized_decode_gb300 as a8w8
+from gpu_util import to_dev, to_host
+from oracle import kv_i4
+
+gpu = pytest.mark.gpu
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    a8w8.build()
+    return a8w8.lib()
+
+
+def _bf(x):
+    return kv_i4.f32_to_bf16(np.asarray(x, np.float32))
+
+
+# ---------------------------------------------------------------------------
+# oracle pins (CPU)
+# ---------------------------------------------------------------------------
+
+def test_rows_by_hand():
+    codes, meta = kv_i4.quant_rows(_bf(np.arange(16)))           # s = 1, m = 0: the codes themselves
+    assert kv_i4.unpack(codes).tolist() == list(range(16))
+    assert kv_i4.bf16_to_f64(meta).tolist() == [1.0, 0.0]
+    assert codes[0] == 0x10 and codes[7] == 0xFE                 # element 2j in the low nibble
+    # ties to even: s = 1, values k + 1/2 between the ends -2 and 13
+    row = np.array([-2, 13, -1.5, -0.5, 0.5, 1.5, 2.5, 3.5], np.float32)
+    codes, meta = kv_i4.quant_rows(_bf(row))
+    assert kv_i4.bf16_to_f64(meta).tolist() == [1.0, -2.0]
+    assert kv_i4.unpack(codes).tolist() == [0, 15, 0, 2, 2, 4, 4, 6]
+    # a constant row has s = 0 and reads back exactly
+    codes, meta = kv_i4.quant_rows(_bf(np.full(8, 2.71875)))
+    assert not codes.any() and (kv_i4.dequant_rows(codes, meta) == 2.71875).all()
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_rows_that_hold_no_finite_range(bad):
+    row = np.ones(8, np.float32)
+    row[3] = bad
+    codes, meta = kv_i4.quant_rows(_bf(row))
+    assert not codes.any() and np.isnan(kv_i4.dequant_rows(codes, meta)).all()
+    row = np.array([3e38, -3e38] * 4, np.float32)                # the range overflows float32
+    assert np.isnan(kv_i4.dequant_rows(*kv_i4.quant_rows(_bf(row)))).all()
+
+
+def test_quantisation_error_is_half_a_step():
+    """|x^ - x| <= s / 2 + 15 s 2^-8 (s is a BF16 rounding of range / 15, so the top code may
+    stand up to 15 s 2^-8 off), plus the float32 roundings of the quotient."""
+    for seed, std in ((1, 1.0), (2, 1e-3), (3, 300.0)):
+        x = synth.bf16_normal(seed, (200, 128), std=std)
+        codes, meta = kv_i4.quant_rows(x)
+        s = kv_i4.bf16_to_f64(meta)[:, :1]
+        err = np.abs(kv_i4.dequant_rows(codes, meta) - kv_i4.bf16_to_f64(x))
+        assert (err <= s * (0.5 + 15 * 2.0 ** -8 + 2.0 ** -18)).all()
+        assert (kv_i4.unpack(codes).max(1) >= 14).all() and (kv_i4.unpack(codes).min(1) == 0).all()
+
+
+def test_attention_oracle_equals_the_bf16_oracle_on_exact_rows():
+    """Pairs with s = 2^e and m a small multiple of it give values that BF16 holds, so the C
+    oracle's attention over a BF16 cache of those values must agree to its one rounding."""
+    rng = np.random.default_rng(5)
+    B, Hq, Hkv, D, page = 3, 6, 2, 64, 16
+    ctx = np.array([37, 1, 0], np.int32)
+    bt, nblk = synth.paged_layout(6, np.maximum(ctx, 1), page, spare_blocks=1)
+    n = nblk * page
+    kc, vc = (rng.integers(0, 256, (n, Hkv, D // 2)).astype(np.uint8) for _ in range(2))
+    km, vm = (np.stack((_bf(2.0 ** rng.integers(-3, 1, (n, Hkv))),
+                        _bf(-rng.integers(0, 8, (n, Hkv)))), axis=-1) for _ in range(2))
+    q = synth.bf16_normal(7, (B, Hq, D))
+    out, bound = kv_i4.attention(q, kc, vc, km, vm, bt, ctx, page)
+    kb, vb = (_bf(kv_i4.dequant_rows(c, m)) for c, m in ((kc, km), (vc, vm)))
+    assert (kv_i4.bf16_to_f64(kb) == kv_i4.dequant_rows(kc, km)).all()
+    ref, rc = oracle.paged_attention(q, kb, vb, bt, ctx, page)
+    ref = kv_i4.bf16_to_f64(ref)
+    assert rc == 0 and (np.abs(out - ref) <= np.abs(out) * 2.0 ** -8 + 1e-12).all()
+    assert not out[2].any() and (bound[:2] > 0).all()
+
+
+# ---------------------------------------------------------------------------
+# refusals (CPU)
+# ---------------------------------------------------------------------------
+
+def test_write_and_read_validation(lib):
+    w = lambda k=FAKE, D=128, T=2, Hkv=8, km=FAKE, page=16: lib.paged_kv_write_i4(  # noqa: E731
+        k, FAKE, T, Hkv, D, FAKE, FAKE, FAKE, km, FAKE, 4, page, None)
+    r = lambda k=FAKE, D=128, T=2, Hkv=8, km=FAKE, page=16: lib.paged_kv_read_i4(  # noqa: E731
+        FAKE, FAKE, km, FAKE, 4, page, FAKE, T, Hkv, D, k, FAKE, None)
+    for f in (w, r):
+        assert f(D=96) == a8w8.ERR_UNSUPPORTED_SHAPE
+        assert f(T=1 << 30, Hkv=8) == a8w8.ERR_UNSUPPORTED_SHAPE
+        assert f(T=-1) == a8w8.ERR_INVALID_ARG
+        assert f(Hkv=0) == a8w8.ERR_INVALID_ARG
+        assert f(page=0) == a8w8.ERR_INVALID_ARG
+        assert f(k=None) == a8w8.ERR_INVALID_ARG
+        assert f(km=FAKE + 4) == a8w8.ERR_INVALID_ARG
+        assert f(T=0, k=None) == a8w8.OK
+
+
+def test_attention_validation(lib):
+    def f(D=128, Hq=16, Hkv=2, ws=FAKE, wsb=1 << 30, km=FAKE, B=2, page=128, max_blocks=40):
+        return lib.paged_decode_attention_i4kv(FAKE, FAKE, FAKE, km, FAKE, FAKE, FAKE, B, Hq, Hkv,
+                                               D, page, max_blocks, 100, 0.1, FAKE, ws, wsb, None)
+    assert f(D=96) == a8w8.ERR_UNSUPPORTED_SHAPE
+    assert f(Hq=18) == a8w8.ERR_UNSUPPORTED_SHAPE      # more than 8 heads a group
+    assert f(Hq=15) == a8w8.ERR_UNSUPPORTED_SHAPE
+    assert f(max_blocks=1 << 18) == a8w8.ERR_UNSUPPORTED_SHAPE
+    assert f(B=65536) == a8w8.ERR_UNSUPPORTED_SHAPE
+    assert f(km=None) == a8w8.ERR_INVALID_ARG
+    assert f(B=-1) == a8w8.ERR_INVALID_ARG
+    assert f(page=0) == a8w8.ERR_INVALID_ARG
+    assert f(B=0, km=None) == a8w8.OK
+    need = lib.a8w8_attention_i4_workspace_bytes(2, 16, 2, 128, 40 * 128)
+    if need:
+        assert f(ws=None) == a8w8.ERR_WORKSPACE
+        assert f(wsb=need - 1) == a8w8.ERR_WORKSPACE
+        assert f(ws=FAKE + 8) == a8w8.ERR_WORKSPACE
+    assert lib.a8w8_attention_i4_workspace_bytes(0, 16, 2, 128, 4096) == 0
+    assert lib.a8w8_attention_i4_workspace_bytes(1, 16, 3, 128, 4096) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(a8w8.A8W8Error, match="int32"):
+        a8w8._typed(t, torch.int32, "x")
+    with pytest.raises(a8w8.A8W8Error, match="codes"):
+        z = torch.zeros((32, 2, 32), dtype=torch.uint8)
+        m = torch.zeros((32, 2, 2), dtype=torch.bfloat16)
+        a8w8._cache_i4(z, z, m, m[:31], 2, 64, 16, "x")
+
+
+# ---------------------------------------------------------------------------
+# write and read (GPU)
+# ---------------------------------------------------------------------------
+
+def _cache(rng, n, Hkv, D, k_scale=0.35, v_scale=0.35):
+    """Random codes and pairs; a scale may be an array of one value per slot."""
+    out = []
+    for sc in (k_scale, v_scale):
+        out.append(rng.integers(0, 256, (n, Hkv, D // 2)).astype(np.uint8))
+        s = np.reshape(sc, (-1, 1)) * rng.uniform(0.7, 1.3, (n, Hkv))
+        out.append(np.stack((_bf(s), _bf(-7.5 * s * rng.uniform(0.85, 1.15, (n, Hkv)))), axis=-1))
+    kc, km, vc, vm = out
+    return kc, vc, km, vm
+
+
+@gpu
+@pytest.mark.parametrize("T,Hkv,D,page", [(1, 2, 64, 16), (7, 8, 128, 128), (5, 1, 128, 5),
+                                          (33, 3, 64, 24), (257, 5, 128, 16)])
+def test_write_and_read_exact(T, Hkv, D, page):
+    rng = np.random.default_rng(T)
+    nblk = -(-T // page) + 2
+    n = nblk * page
+    k = synth.bf16_normal(T + 1, (T, Hkv, D))
+    v = synth.bf16_normal(T + 2, (T, Hkv, D), std=3.0)
+    slots = rng.permutation(n)[:T].astype(np.int32)
+    if T > 4:
+        slots[1] = -1
+        k[0, 0] = 0                                        # constant rows: s = 0
+        v[2, 0] = _bf(np.full(D, -1.75))
+        k[3, 0] = _bf(np.where(np.arange(D) % 3 == 0, 1e-39, 0))       # subnormal range
+        v[3, 0] = _bf(np.linspace(-3e38, 2.9e37, D))       # range near the end of float32
+        k[4, 0] = _bf(rng.normal(size=D) * 2.0 ** -120)    # quotients by the division
+        v[4, 0, 1] = _bf(np.nan)
+    host = list(_cache(rng, n, Hkv, D))
+    dev = [to_dev(a) for a in host]
+    a8w8.read_device_errors()
+    a8w8.paged_kv_write_i4(to_dev(k), to_dev(v), to_dev(slots), *dev, page)
+    want = [a.copy() for a in host]
+    assert kv_i4.kv_write(k, v, slots, *want) == 0
+    got = [to_host(d) for d in dev]
+    for g, w in zip(got[:2], want[:2]):
+        assert np.array_equal(g, w)
+    for g, w in zip(got[2:], want[2:]):      # as values: a minimum of zero may carry either sign
+        assert np.array_equal(kv_i4.bf16_to_f64(g), kv_i4.bf16_to_f64(w), equal_nan=True)
+    # read back, a slot twice and a padded one
+    at = np.concatenate((slots, slots[:1], [-1])).astype(np.int32)
+    gk, gv = (to_host(x) for x in a8w8.paged_kv_read_i4(*dev, to_dev(at), page))
+    for g, c, m in ((gk, got[0], got[2]), (gv, got[1], got[3])):
+        with np.errstate(over="ignore"):
+            x = kv_i4.dequant_rows(c[np.maximum(at, 0)], m[np.maximum(at, 0)]).astype(np.float32)
+        x[at < 0] = 0
+        assert np.array_equal(kv_i4.bf16_to_f64(g), kv_i4.bf16_to_f64(_bf(x)), equal_nan=True)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+def test_slots_out_of_range_are_flagged_and_skipped():
+    Hkv, D, page, nblk = 2, 64, 16, 2
+    k = synth.bf16_normal(5, (3, Hkv, D))
+    host = list(_cache(np.random.default_rng(1), nblk * page, Hkv, D))
+    dev = [to_dev(a) for a in host]
+    slots = np.array([nblk * page, 4, 2 ** 31 - 1], np.int32)
+    a8w8.read_device_errors()
+    a8w8.paged_kv_write_i4(to_dev(k), to_dev(k), to_dev(slots), *dev, page)
+    assert a8w8.read_device_errors() == a8w8.DEVERR_SLOT
+    want = [a.copy() for a in host]
+    assert kv_i4.kv_write(k, k, slots, *want) == 2
+    for d, w in zip(dev, want):
+        assert np.array_equal(to_host(d), w)
+    gk, gv = a8w8.paged_kv_read_i4(*dev, to_dev(slots), page)
+    assert a8w8.read_device_errors() == a8w8.DEVERR_SLOT
+    assert not to_host(gk)[[0, 2]].any() and to_host(gk)[1].any()
+    # no tokens: nothing happens
+    a8w8.paged_kv_write_i4(to_dev(k[:0]), to_dev(k[:0]), to_dev(slots[:0]), *dev, page)
+    assert a8w8.paged_kv_read_i4(*dev, to_dev(slots[:0]), page)[0].shape == (0, Hkv, D)
+    assert a8w8.read_device_errors() == 0
+
+
+# ---------------------------------------------------------------------------
+# attention (GPU)
+# ---------------------------------------------------------------------------
+
+def _check(got, want, bound):
+    """Within the derived bound plus the BF16 rounding of the result (half a step: 2^-8)."""
+    g = kv_i4.bf16_to_f64(to_host(got))
+    tol = bound + (np.abs(want) + bound) * 2.0 ** -8
+    assert np.array_equal(np.isnan(g), np.isnan(want))
+    ok = np.isnan(want) | (np.abs(g - want) <= tol)
+    worst = np.nanmax(np.abs(g - want) / np.maximum(tol, 1e-300))
+    assert ok.all(), f"{(~ok).sum()} of {ok.size} elements off, worst {worst:.3g} of the bound"
+    # the error as a whole is that of the one rounding (2^-8 / sqrt(3) at most, relative)
+    f = ~np.isnan(want)
+    if np.linalg.norm(want[f]) > 0:
+        rel = np.linalg.norm((g - want)[f]) / np.linalg.norm(want[f])
+        assert rel <= 2.0 ** -8 / np.sqrt(3) + np.linalg.norm(bound[f]) / np.linalg.norm(want[f])
+
+
+def _case(seed, ctx, Hq, Hkv, D, page, gain=1.5, **scales):
+    rng = np.random.default_rng(seed)
+    ctx = np.asarray(ctx, np.int32)
+    bt, nblk = synth.paged_layout(seed, np.maximum(ctx, 1), page, spare_blocks=2)
+    cache = _cache(rng, nblk * page, Hkv, D, **scales)
+    q = synth.bf16_normal(seed + 1, (len(ctx), Hq, D), std=gain)
+    return q, cache, bt, ctx
+
+
+SHAPES = [
+    # contexts, Hq, Hkv, D, page
+    ([255], 40, 8, 128, 128),
+    ([1], 8, 8, 128, 128),
+    ([16, 17, 15, 31, 32, 33, 63, 64, 65, 0], 4, 2, 64, 16),
+    ([1, 2, 3, 5, 7, 8, 9], 6, 2, 128, 5),
+    ([4096, 300, 0, 2049], 40, 8, 128, 128),
+    ([777, 1300], 8, 1, 128, 48),
+    ([129, 1, 3000], 7, 1, 64, 24),
+    ([500, 501], 12, 4, 64, 1),
+    (list(range(0, 1200, 37)), 10, 5, 128, 32),
+    ([128, 256, 384, 512] * 5, 16, 2, 128, 64),
+]
+
+
+@gpu
+@pytest.mark.parametrize("ctx,Hq,Hkv,D,page", SHAPES)
+def test_attention(ctx, Hq, Hkv, D, page):
+    q, cache, bt, ctx = _case(len(ctx) * 7 + Hq, ctx, Hq, Hkv, D, page)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
+    a8w8.read_device_errors()
+    dev = [to_dev(a) for a in (q, *cache, bt, ctx)]
+    got = a8w8.paged_decode_attention_i4kv(*dev, page)
+    _check(got, want, bound)
+    assert not to_host(got)[ctx == 0].any()
+    assert a8w8.read_device_errors() == 0
+    again = a8w8.paged_decode_attention_i4kv(*dev, page)
+    assert np.array_equal(to_host(got), to_host(again))       # the same bits every time
+
+
+@gpu
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_attention_groups(G):
+    q, cache, bt, ctx = _case(G, [70, 200, 3], 2 * G, 2, 128, 16)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, 16)
+    _check(a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], 16), want,
+           bound)
+
+
+@gpu
+@pytest.mark.parametrize("what", ["peaked", "tiny v", "mixed v", "zero s", "huge v", "rising",
+                                  "scale 0", "negative scale"])
+def test_attention_ranges(what):
+    """Weights, scales and maxima over wide ranges: one token that takes all, V rows of tiny,
+    mixed (10 decades) or zero s, scores that rise along the context."""
+    n, page = 600, 16
+    rng = np.random.default_rng(3)
+    gain = 30.0 if what == "peaked" else 1.5
+    sc = {"scale 0": 0.0, "negative scale": -0.2}.get(what)
+    v_scale = {"tiny v": 1e-9, "huge v": 1e30}.get(what, 0.35)
+    q, cache, bt, ctx = _case(9, [n, 1, 77], 10, 2, 128, page, gain=gain, v_scale=v_scale)
+    kc, vc, km, vm = cache
+    if what == "mixed v":
+        s = kv_i4.bf16_to_f64(vm) * (10.0 ** rng.uniform(-5, 5, vm.shape[:2]))[..., None]
+        vm = _bf(s)
+    if what == "zero s":
+        vm[::2, :, 0] = 0                                  # constant rows, every other slot
+        km[1::3, :, 0] = 0
+    if what == "rising":
+        for t in range(n):                                 # K grows with the position
+            slot = bt[0][t // page] * page + t % page
+            km[slot] = _bf(kv_i4.bf16_to_f64(km[slot]) * (t / 60.0))
+    cache = (kc, vc, km, vm)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page, scale=sc)
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page,
+                                           softmax_scale=sc)
+    _check(got, want, bound)
+
+
+@gpu
+def test_attention_bad_tables_and_nan_rows():
+    page, Hq, Hkv, D = 16, 4, 2, 64
+    q, cache, bt, ctx = _case(4, [100, 40, 90, 33], Hq, Hkv, D, page)
+    bt[0, 2], bt[1, 0] = 10 ** 6, -5                       # rows of zeros
+    ctx[2] = bt.shape[1] * page + 1                        # out of range: no tokens
+    cache[2][bt[3, 1] * page + 3, 1] = _bf(np.nan)         # head 1 of request 3
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
+    a8w8.read_device_errors()
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page)
+    assert a8w8.read_device_errors() == a8w8.DEVERR_BLOCK | a8w8.DEVERR_CTX
+    _check(got, want, bound)
+    assert np.isnan(want[3, 2:]).all() and not np.isnan(want[3, :2]).any()
+    assert not to_host(got)[2].any()
+    # past the context nothing counts: a bad id, a NaN row
+    q, cache, bt, ctx = _case(5, [17, 30], Hq, Hkv, D, page)
+    cache[2][bt[0, 1] * page + 1:bt[0, 1] * page + page] = _bf(np.nan)
+    cache[3][bt[1, 1] * page + 14:bt[1, 1] * page + page] = _bf(np.nan)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
+    _check(a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page), want,
+           bound)
+    assert a8w8.read_device_errors() == 0 and not np.isnan(want).any()
+
+
+@gpu
+def test_attention_captured_on_another_stream():
+    """A captured call replays on new queries, tables and contexts; the workspace starts with
+    arbitrary contents."""
+    import torch
+    page, Hq, Hkv, D = 32, 10, 2, 128
+    q, cache, bt, ctx = _case(6, [900, 1, 64, 333], Hq, Hkv, D, page)
+    dev = [to_dev(a) for a in (q, *cache, bt, ctx)]
+    need = max(a8w8.attention_i4_workspace_bytes(4, Hq, Hkv, D, bt.shape[1] * page), 16)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(dev[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a8w8.paged_decode_attention_i4kv(*dev, page, ws=ws, out=out)
+    side.synchronize()
+    first = to_host(out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a8w8.paged_decode_attention_i4kv(*dev, page, ws=ws, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(first, to_host(out))
+    q2 = synth.bf16_normal(99, q.shape)
+    ctx2 = np.array([17, 0, 50, 900 if bt.shape[1] * page >= 900 else 1], np.int32)
+    bt2 = bt[[3, 2, 1, 0]].copy()
+    dev[0].copy_(to_dev(q2))
+    dev[5].copy_(to_dev(bt2))
+    dev[6].copy_(to_dev(ctx2))
+    g.replay()
+    torch.cuda.synchronize()
+    want, bound = kv_i4.attention(q2, *cache, bt2, ctx2, page)
+    _check(out, want, bound)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """Pages whose codes lie more than 4 GiB into the cache (write, read, attention)."""
+    import torch
+    Hkv, D, page = 8, 128, 128
+    nblk = (1 << 32) // (page * Hkv * D // 2) + 40
+    dev = [torch.zeros((nblk * page, Hkv, D // 2), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    dev += [torch.zeros((nblk * page, Hkv, 2), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    T = 300
+    k, v = synth.bf16_normal(1, (T, Hkv, D)), synth.bf16_normal(2, (T, Hkv, D))
+    bt = np.array([[nblk - 1, 3, nblk - 7]], np.int32)
+    t = np.arange(T)
+    slots = (bt[0][t // page] * page + t % page).astype(np.int32)
+    a8w8.paged_kv_write_i4(to_dev(k), to_dev(v), to_dev(slots), *dev, page)
+    q = synth.bf16_normal(3, (1, 40, D))
+    got = a8w8.paged_decode_attention_i4kv(to_dev(q), *dev, to_dev(bt), to_dev(np.array([T], np.int32)),
+                                           page)
+    small = [np.zeros((3 * page, *d.shape[1:]), np.uint8 if i < 2 else np.uint16)
+             for i, d in enumerate(dev)]
+    kv_i4.kv_write(k, v, t.astype(np.int32), *small)
+    want, bound = kv_i4.attention(q, *small, np.array([[0, 1, 2]]), [T], page)
+    _check(got, want, bound)
+    gk, _ = a8w8.paged_kv_read_i4(*dev, to_dev(slots), page)
+    x = kv_i4.dequant_rows(small[0][:T], small[2][:T]).astype(np.float32)
+    assert np.array_equal(to_host(gk), _bf(x))

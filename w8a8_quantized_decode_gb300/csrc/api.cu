@@ -229,6 +229,73 @@ a8w8_status check_ptrs(std::initializer_list<const void*> ptrs, const char* what
     return A8W8_OK;
 }
 
+KvI4 kv_i4(const uint8_t* k_codes, const uint8_t* v_codes, const a8w8_bf16* k_meta,
+           const a8w8_bf16* v_meta) {
+    KvI4 c;
+    c.k_codes = const_cast<uint8_t*>(k_codes);
+    c.v_codes = const_cast<uint8_t*>(v_codes);
+    c.k_meta = const_cast<bf16*>(reinterpret_cast<const bf16*>(k_meta));
+    c.v_meta = const_cast<bf16*>(reinterpret_cast<const bf16*>(v_meta));
+    return c;
+}
+
+a8w8_status check_rows_i4(int T, int Hkv, int D, const char* what) {
+    if (D != 64 && D != 128)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %d not supported", what, D);
+    if ((long long)T * Hkv > (1LL << 31))
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^31 rows", what);
+    return A8W8_OK;
+}
+
+// Page operations: the sizes shared by all of them.
+constexpr int kMaxPages = (1 << 21) - 1;   // ranks of 1024 rows' needs add up in 32 bits
+
+a8w8_status check_pages(int num_blocks, int B, int max_blocks, int page_size, const char* what) {
+    if (num_blocks <= 0 || B <= 0 || max_blocks <= 0 || page_size <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "%s: bad size", what);
+    if (num_blocks > kMaxPages)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: more than %d pages", what, kMaxPages);
+    if ((long long)max_blocks * page_size > (1 << 24))
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: context longer than 2^24 tokens", what);
+    return A8W8_OK;
+}
+
+// The pool's caches from the caller's HOST arrays; every cache's page is a
+// whole number of 4-byte words per token.
+a8w8_status cache_list(CacheList& c, void* const* caches, const size_t* page_bytes, int num_caches,
+                       int num_blocks, int page_size, const char* what) {
+    if (num_caches <= 0 || num_blocks <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "%s: bad size", what);
+    if (num_caches > kMaxCaches)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: more than %d caches", what, kMaxCaches);
+    if (num_blocks > kMaxPages)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: more than %d pages", what, kMaxPages);
+    if (!caches || !page_bytes) return fail(A8W8_ERR_INVALID_ARG, "%s: cache arrays are NULL", what);
+    for (int i = 0; i < num_caches; ++i) {
+        a8w8_status s = check_ptrs({caches[i]}, what);
+        if (s != A8W8_OK) return s;
+        if (page_bytes[i] == 0 || page_bytes[i] % (4 * (size_t)page_size) ||
+            page_bytes[i] >= (1u << 31))
+            return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
+                        "%s: %zu bytes per page: 4-byte words per token, below 2^31 bytes", what,
+                        page_bytes[i]);
+        c.base[i] = static_cast<unsigned char*>(caches[i]);
+        c.page_bytes[i] = (unsigned)page_bytes[i];
+    }
+    c.num_caches = num_caches;
+    c.num_blocks = num_blocks;
+    page_units(c);
+    return A8W8_OK;
+}
+
+a8w8_status check_pages_ws(int num_blocks, int B, int n, const void* ws, size_t ws_bytes,
+                           const char* what) {
+    const size_t need = pages_workspace_bytes(num_blocks, B, n);
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(A8W8_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", what, need);
+    return A8W8_OK;
+}
+
 a8w8_status check_layer_weights(const a8w8_layer_weights* w) {
     if (!w) return fail(A8W8_ERR_INVALID_ARG, "layer weights are NULL");
     return check_ptrs({w->input_norm_w, w->w_qkv, w->s_qkv, w->q_norm_w, w->k_norm_w, w->w_o, w->s_o,
@@ -896,6 +963,185 @@ a8w8_status paged_decode_attention_i8kv(const a8w8_bf16* q, const int8_t* k_code
     ai.v_scale = const_cast<float*>(v_scale);
     cudaError_t e = launch_attention_i8(ai, make_launch(stream, false));
     return e == cudaSuccess ? A8W8_OK : cuda_fail(e, "paged_decode_attention_i8kv");
+}
+
+a8w8_status paged_kv_write_i4(const a8w8_bf16* k, const a8w8_bf16* v, int T, int Hkv, int D,
+                              const int32_t* slot_mapping, uint8_t* k_codes, uint8_t* v_codes,
+                              a8w8_bf16* k_meta, a8w8_bf16* v_meta, int num_blocks, int page_size,
+                              void* stream) {
+    if (T < 0 || Hkv <= 0 || num_blocks < 0 || page_size <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "paged_kv_write_i4: bad size");
+    if (T == 0) return A8W8_OK;
+    a8w8_status s = check_rows_i4(T, Hkv, D, "paged_kv_write_i4");
+    if (s != A8W8_OK) return s;
+    if ((s = check_ptrs({k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta},
+                        "paged_kv_write_i4")) != A8W8_OK)
+        return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_kv_write_i4(
+        reinterpret_cast<const bf16*>(k), reinterpret_cast<const bf16*>(v), T, Hkv, D, slot_mapping,
+        kv_i4(k_codes, v_codes, k_meta, v_meta), (long)num_blocks * page_size, device_error_word(),
+        L);
+    return e == cudaSuccess ? A8W8_OK : cuda_fail(e, "paged_kv_write_i4");
+}
+
+a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
+                             const a8w8_bf16* k_meta, const a8w8_bf16* v_meta, int num_blocks,
+                             int page_size, const int32_t* slot_mapping, int T, int Hkv, int D,
+                             a8w8_bf16* k, a8w8_bf16* v, void* stream) {
+    if (T < 0 || Hkv <= 0 || num_blocks < 0 || page_size <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "paged_kv_read_i4: bad size");
+    if (T == 0) return A8W8_OK;
+    a8w8_status s = check_rows_i4(T, Hkv, D, "paged_kv_read_i4");
+    if (s != A8W8_OK) return s;
+    if ((s = check_ptrs({k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta},
+                        "paged_kv_read_i4")) != A8W8_OK)
+        return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_kv_read_i4(kv_i4(k_codes, v_codes, k_meta, v_meta),
+                                      (long)num_blocks * page_size, slot_mapping, T, Hkv, D,
+                                      reinterpret_cast<bf16*>(k), reinterpret_cast<bf16*>(v),
+                                      device_error_word(), L);
+    return e == cudaSuccess ? A8W8_OK : cuda_fail(e, "paged_kv_read_i4");
+}
+
+size_t a8w8_attention_i4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_ctx) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_ctx <= 0) return 0;
+    return attn_i4_part_bytes(B, Hq, Hkv, D, max_ctx);
+}
+
+a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
+                                        const uint8_t* v_codes, const a8w8_bf16* k_meta,
+                                        const a8w8_bf16* v_meta, const int32_t* block_table,
+                                        const int32_t* ctx_lens, int B, int Hq, int Hkv, int D,
+                                        int page_size, int max_blocks, int num_blocks,
+                                        float softmax_scale, a8w8_bf16* out, void* ws,
+                                        size_t ws_bytes, void* stream) {
+    if (B < 0 || Hq <= 0 || Hkv <= 0 || page_size <= 0 || max_blocks <= 0 || num_blocks <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "paged_decode_attention_i4kv: bad size");
+    if (B == 0) return A8W8_OK;
+    if (D != 64 && D != 128) return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "head_dim %d not supported", D);
+    if (Hq % Hkv || Hq / Hkv > 8) return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "Hq/Hkv must be an integer <= 8");
+    if ((long long)max_blocks * page_size > (1 << 24))
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "context longer than 2^24 tokens");
+    if (B > 65535 || Hq > 65535)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "more than 65535 requests or query heads");
+    a8w8_status s = check_ptrs({q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, out},
+                               "paged_decode_attention_i4kv");
+    if (s != A8W8_OK) return s;
+    const size_t need = attn_i4_part_bytes(B, Hq, Hkv, D, max_blocks * page_size);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
+        return fail(A8W8_ERR_WORKSPACE, "attention workspace needs %zu bytes", need);
+    AttnI4Params a = {};
+    a.q = reinterpret_cast<const bf16*>(q);
+    a.c = kv_i4(k_codes, v_codes, k_meta, v_meta);
+    a.block_table = block_table;
+    a.ctx_lens = ctx_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.page = page_size;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.scale = softmax_scale;
+    a.out = reinterpret_cast<bf16*>(out);
+    a.part = static_cast<float*>(ws);
+    a.err = device_error_word();
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_attention_i4(a, L);
+    return e == cudaSuccess ? A8W8_OK : cuda_fail(e, "paged_decode_attention_i4kv");
+}
+
+size_t a8w8_pages_workspace_bytes(int num_blocks, int B, int n) {
+    if (num_blocks <= 0 || B <= 0 || n < 0) return 0;
+    return pages_workspace_bytes(num_blocks, B, n);
+}
+
+a8w8_status paged_copy_pages(void* const* caches, const size_t* page_bytes, int num_caches,
+                             int num_blocks, const int32_t* src, const int32_t* dst, int n,
+                             void* stream) {
+    CacheList c;
+    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_copy_pages: negative count");
+    a8w8_status s = cache_list(c, caches, page_bytes, num_caches, num_blocks, 1, "paged_copy_pages");
+    if (s != A8W8_OK || n == 0) return s;
+    if ((s = check_ptrs({src, dst}, "paged_copy_pages")) != A8W8_OK) return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    CUDA_TRY(launch_copy_pages(c, src, dst, n, device_error_word(), L), "paged_copy_pages");
+    return A8W8_OK;
+}
+
+a8w8_status paged_fork(void* const* caches, const size_t* page_bytes, int num_caches,
+                       int num_blocks, int page_size, int32_t* block_table, int32_t* ctx_lens,
+                       int32_t* refcount, int B, int max_blocks, const int32_t* parents,
+                       const int32_t* children, int n, void* ws, size_t ws_bytes, void* stream) {
+    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_fork: negative count");
+    a8w8_status s = check_pages(num_blocks, B, max_blocks, page_size, "paged_fork");
+    if (s != A8W8_OK) return s;
+    CacheList c;
+    s = cache_list(c, caches, page_bytes, num_caches, num_blocks, page_size, "paged_fork");
+    if (s != A8W8_OK || n == 0) return s;
+    if ((s = check_ptrs({block_table, ctx_lens, refcount, parents, children}, "paged_fork")) != A8W8_OK)
+        return s;
+    if ((s = check_pages_ws(num_blocks, B, n, ws, ws_bytes, "paged_fork")) != A8W8_OK) return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    const PageTables t = {block_table, ctx_lens, refcount, B, max_blocks, page_size};
+    CUDA_TRY(launch_fork(c, t, parents, children, n, ws, device_error_word(), L), "paged_fork");
+    return A8W8_OK;
+}
+
+a8w8_status paged_reserve(int32_t* block_table, int32_t* refcount, int B, int max_blocks,
+                          int num_blocks, int page_size, const int32_t* rows,
+                          const int32_t* tokens, int n, void* ws, size_t ws_bytes, void* stream) {
+    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_reserve: negative count");
+    a8w8_status s = check_pages(num_blocks, B, max_blocks, page_size, "paged_reserve");
+    if (s != A8W8_OK || n == 0) return s;
+    if ((s = check_ptrs({block_table, refcount, rows, tokens}, "paged_reserve")) != A8W8_OK) return s;
+    if ((s = check_pages_ws(num_blocks, B, n, ws, ws_bytes, "paged_reserve")) != A8W8_OK) return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    const PageTables t = {block_table, nullptr, refcount, B, max_blocks, page_size};
+    CUDA_TRY(launch_reserve(t, num_blocks, rows, tokens, n, ws, device_error_word(), L),
+             "paged_reserve");
+    return A8W8_OK;
+}
+
+a8w8_status paged_free(int32_t* block_table, int32_t* ctx_lens, int32_t* refcount, int B,
+                       int max_blocks, int num_blocks, const int32_t* rows, int n, void* stream) {
+    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_free: negative count");
+    a8w8_status s = check_pages(num_blocks, B, max_blocks, 1, "paged_free");
+    if (s != A8W8_OK || n == 0) return s;
+    if ((s = check_ptrs({block_table, ctx_lens, refcount, rows}, "paged_free")) != A8W8_OK) return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    const PageTables t = {block_table, ctx_lens, refcount, B, max_blocks, 1};
+    CUDA_TRY(launch_free(t, num_blocks, rows, n, device_error_word(), L), "paged_free");
+    return A8W8_OK;
+}
+
+a8w8_status paged_compact(void* const* caches, const size_t* page_bytes, int num_caches,
+                          int num_blocks, int32_t* block_table, int32_t* refcount, int B,
+                          int max_blocks, int32_t* num_live, void* ws, size_t ws_bytes,
+                          void* stream) {
+    a8w8_status s = check_pages(num_blocks, B, max_blocks, 1, "paged_compact");
+    if (s != A8W8_OK) return s;
+    CacheList c;
+    s = cache_list(c, caches, page_bytes, num_caches, num_blocks, 1, "paged_compact");
+    if (s != A8W8_OK) return s;
+    if ((s = check_ptrs({block_table, refcount}, "paged_compact")) != A8W8_OK) return s;
+    if (num_live && (reinterpret_cast<uintptr_t>(num_live) & 3))
+        return fail(A8W8_ERR_INVALID_ARG, "paged_compact: num_live not 4-byte aligned");
+    if ((s = check_pages_ws(num_blocks, B, 0, ws, ws_bytes, "paged_compact")) != A8W8_OK) return s;
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    const PageTables t = {block_table, nullptr, refcount, B, max_blocks, 1};
+    CUDA_TRY(launch_compact(c, t, num_live, ws, device_error_word(), L), "paged_compact");
+    return A8W8_OK;
 }
 
 }  // extern "C"

@@ -173,6 +173,64 @@ cudaError_t launch_kv_write_i8(const bf16* k, const bf16* v, int T, int Hkv, int
                                const int32_t* slot_mapping, int8_t* k_codes, int8_t* v_codes,
                                float* k_scale, float* v_scale, long num_slots, unsigned* err,
                                const Launch& L);
+
+// 4-bit KV cache (kv_i4.cu, attn_i4.cu): codes [num_blocks*page, Hkv, D/2],
+// two to a byte, and (s, m) pairs [num_blocks*page, Hkv, 2] BF16.
+struct KvI4 {
+    uint8_t* k_codes;
+    uint8_t* v_codes;
+    bf16* k_meta;
+    bf16* v_meta;
+};
+cudaError_t launch_kv_write_i4(const bf16* k, const bf16* v, int T, int Hkv, int D,
+                               const int32_t* slot_mapping, const KvI4& c, long num_slots,
+                               unsigned* err, const Launch& L);
+cudaError_t launch_kv_read_i4(const KvI4& c, long num_slots, const int32_t* slot_mapping, int T,
+                              int Hkv, int D, bf16* k, bf16* v, unsigned* err, const Launch& L);
+struct AttnI4Params {
+    const bf16* q;          // [B, Hq, D]
+    KvI4 c;
+    const int32_t* block_table;   // [B, max_blocks]
+    const int32_t* ctx_lens;      // [B]
+    int B, Hq, Hkv, D, page, max_blocks, num_blocks;
+    float scale;
+    bf16* out;              // [B, Hq, D]
+    float* part;            // attn_i4_part_bytes
+    unsigned* err;
+};
+size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx);
+cudaError_t launch_attention_i4(const AttnI4Params& p, const Launch& L);
+
+// Pages of a cache (pages.cu). A pool is num_caches device arrays of
+// num_blocks pages each (page_bytes[c] bytes, a multiple of 4).
+constexpr int kMaxCaches = 256;
+struct CacheList {
+    unsigned char* base[kMaxCaches];
+    unsigned page_bytes[kMaxCaches];
+    unsigned first_unit[kMaxCaches + 1];   // copy units of the caches before this one
+    int num_caches;
+    int num_blocks;
+};
+// Fills first_unit from page_bytes.
+void page_units(CacheList& c);
+struct PageTables {
+    int32_t* block_table;   // [B, max_blocks], a negative entry holds no page
+    int32_t* ctx_lens;      // [B]
+    int32_t* refcount;      // [num_blocks]
+    int B, max_blocks, page;
+};
+size_t pages_workspace_bytes(int num_blocks, int B, int n);
+cudaError_t launch_copy_pages(const CacheList& c, const int32_t* src, const int32_t* dst, int n,
+                              unsigned* err, const Launch& L);
+cudaError_t launch_fork(const CacheList& c, const PageTables& t, const int32_t* parents,
+                        const int32_t* children, int n, void* ws, unsigned* err, const Launch& L);
+cudaError_t launch_reserve(const PageTables& t, int num_blocks, const int32_t* rows,
+                           const int32_t* tokens, int n, void* ws, unsigned* err, const Launch& L);
+cudaError_t launch_free(const PageTables& t, int num_blocks, const int32_t* rows, int n,
+                        unsigned* err, const Launch& L);
+cudaError_t launch_compact(const CacheList& c, const PageTables& t, int32_t* num_live, void* ws,
+                           unsigned* err, const Launch& L);
+
 // BF16 (unquantised) layer (gemv_bf16.cu): y[m][n] = bf16(sum_k x[m][k]
 // W[n][k] (+ residual[m][n])), or with `swiglu` act[m][n] = bf16(silu(g) u)
 // from the gate row n and the up row N + n of W [2N, K]. K, ldx multiples

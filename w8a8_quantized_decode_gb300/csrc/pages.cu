@@ -1,0 +1,614 @@
+// pages.cu -- the pages of a paged cache: copying, forking, reserving, freeing
+// and compacting them on the device.
+//
+// A pool is a set of caches (K and V codes, scales, ... of every layer) that
+// share one page numbering, a block table [B, max_blocks] whose negative
+// entries hold no page, the rows' context lengths, and a reference count per
+// page (0 or less = free). Page numbers are handed out lowest first and in the
+// order of the request lists, so a call's result is a function of its inputs.
+//
+// The data moves are bound by HBM (each byte read and written once); the
+// bookkeeping is a few passes over the counts and tables. fork and compact run
+// a one-CTA plan that decides every move (the decisions are ordered: ranks
+// among the free pages), then one kernel that carries the moves out over all
+// SMs. The plan starts the second kernel early by programmatic dependent
+// launch, so that only its wait remains between them.
+#include <algorithm>
+
+#include "kernels.cuh"
+
+namespace a8w8 {
+
+namespace {
+
+constexpr int kCopyThreads = 256;
+constexpr unsigned kUnitBytes = 16384;   // a copy unit: 4 vectors of 16 bytes per thread
+constexpr int kCopyCtasPerSm = 4;
+constexpr int kPlanThreads = 1024;
+constexpr unsigned kErrBlock = 0x2u, kErrCtx = 0x4u, kErrRow = 0x40u, kErrPages = 0x80u,
+                   kErrAlias = 0x100u;
+
+// Copies n bytes (a multiple of 4) with the CTA's threads: 16-byte vectors,
+// four per thread in flight, where both addresses allow it, and 4-byte words
+// for the rest.
+__device__ __forceinline__ void copy_unit(unsigned char* dst, const unsigned char* src,
+                                          unsigned n) {
+    unsigned done = 0;
+    if (((reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(src)) & 15) == 0) {
+        const unsigned nv = n / 16;
+        const int4* s = reinterpret_cast<const int4*>(src);
+        int4* d = reinterpret_cast<int4*>(dst);
+        for (unsigned i = threadIdx.x; i < nv; i += 4 * kCopyThreads) {
+            int4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * kCopyThreads < nv) v[k] = __ldcs(s + i + k * kCopyThreads);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k * kCopyThreads < nv) __stcs(d + i + k * kCopyThreads, v[k]);
+        }
+        done = nv * 16;
+    }
+    for (unsigned i = done / 4 + threadIdx.x; i < n / 4; i += kCopyThreads)
+        reinterpret_cast<unsigned*>(dst)[i] = __ldcs(reinterpret_cast<const unsigned*>(src) + i);
+}
+
+// The cache that unit u of a page belongs to (units of one page are numbered
+// through all caches).
+__device__ __forceinline__ int unit_cache(const CacheList& c, unsigned u) {
+    int lo = 0, hi = c.num_caches - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (c.first_unit[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Copies unit u of page `from` to page `to`, of the first tokens / page_size
+// of the page when `tokens` is below page_size.
+__device__ __forceinline__ void copy_page_unit(const CacheList& c, unsigned u, int from, int to,
+                                               int tokens, int page_size) {
+    const int k = unit_cache(c, u);
+    const unsigned pb = c.page_bytes[k];
+    const unsigned used = tokens >= page_size ? pb : pb / (unsigned)page_size * (unsigned)tokens;
+    const unsigned off = (u - c.first_unit[k]) * kUnitBytes;
+    if (off >= used) return;
+    copy_unit(c.base[k] + (size_t)to * pb + off, c.base[k] + (size_t)from * pb + off,
+              min(kUnitBytes, used - off));
+}
+
+// Exclusive prefix sum of v over the CTA's kPlanThreads threads; the total in
+// `total`. `s` is 32 ints of shared memory. All threads call it.
+__device__ __forceinline__ int block_exclusive(int v, int* s, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = s[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        s[lane] = w;
+    }
+    __syncthreads();
+    const int before = warp ? s[warp - 1] : 0;
+    total = s[31];
+    __syncthreads();   // s may be written again
+    return before + x - v;
+}
+
+// Which of pages [4 i, 4 i + 4) are free, as four bits (pages at or past n are
+// not).
+__device__ __forceinline__ unsigned free_mask(const int32_t* refcount, int i, int n) {
+    unsigned f = 0;
+    if (4 * i + 3 < n) {
+        const int4 r = ld_cg_v4(refcount + 4 * (size_t)i);
+        f = (r.x <= 0) | (r.y <= 0) << 1 | (r.z <= 0) << 2 | (r.w <= 0) << 3;
+    } else {
+        for (int k = 0; k < 4; ++k)
+            if (4 * i + k < n && __ldcg(refcount + 4 * (size_t)i + k) <= 0) f |= 1u << k;
+    }
+    return f;
+}
+
+// put(rank, page) for the lowest `want` free pages, rank counted from 0;
+// returns how many there are (at most `want`). All threads call it.
+template <typename Put>
+__device__ __forceinline__ int lowest_free(const int32_t* refcount, int n, int want, int* s,
+                                           Put put) {
+    int found = 0;
+    const int quads = n / 4 + (n % 4 != 0);
+    for (int q0 = 0; q0 < quads && found < want; q0 += kPlanThreads) {
+        const int q = q0 + (int)threadIdx.x;
+        const unsigned f = q < quads ? free_mask(refcount, q, n) : 0u;
+        int total;
+        int rank = found + block_exclusive(__popc(f), s, total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (f >> k & 1u) {
+                if (rank < want) put(rank, 4 * q + k);
+                ++rank;
+            }
+        found += total;
+    }
+    return min(found, want);
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+// ---------------------------------------------------------------------------
+// copy
+// ---------------------------------------------------------------------------
+
+constexpr int kPairBatch = 64;
+
+// Each CTA takes a contiguous range of (pair, unit), so that it checks few
+// pairs. A pair is carried out unless its destination is the destination of an
+// earlier pair or the source of another one; a pair counts if both pages are
+// in range and differ.
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_pages_kernel(const __grid_constant__ CacheList c, const int32_t* __restrict__ src,
+                      const int32_t* __restrict__ dst, int n, unsigned* err) {
+    __shared__ int sfrom[kPairBatch], sto[kPairBatch], sbad[kPairBatch];
+    pdl_wait();
+    pdl_trigger();
+    const unsigned U = c.first_unit[c.num_caches];
+    const long total = (long)n * U;
+    const long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (u0 >= u1) return;
+    const int p1 = (int)((u1 - 1) / U) + 1;
+    for (int p0 = (int)(u0 / U); p0 < p1; p0 += kPairBatch) {
+        const int np = min(kPairBatch, p1 - p0);
+        if ((int)threadIdx.x < np) {
+            const int f = src[p0 + threadIdx.x], t = dst[p0 + threadIdx.x];
+            const bool ok = f >= 0 && t >= 0 && f < c.num_blocks && t < c.num_blocks;
+            if (!ok && f >= 0 && t >= 0) set_error(err, kErrBlock);
+            sfrom[threadIdx.x] = f;
+            sto[threadIdx.x] = t;
+            sbad[threadIdx.x] = !ok || f == t;
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += kCopyThreads) {
+            const int f = src[j], t = dst[j];
+            if (f < 0 || t < 0 || f >= c.num_blocks || t >= c.num_blocks || f == t) continue;
+            for (int i = 0; i < np; ++i) {
+                if (sbad[i] == 1) continue;
+                if (f == sto[i] || (t == sto[i] && j < p0 + i)) sbad[i] = 2;
+            }
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < np && sbad[threadIdx.x] == 2) set_error(err, kErrAlias);
+        const long a = max(u0, (long)p0 * U), b = min(u1, (long)(p0 + np) * U);
+        for (long u = a; u < b; ++u) {
+            const int i = (int)(u / U) - p0;
+            if (sbad[i]) continue;
+            copy_page_unit(c, (unsigned)(u - (long)(p0 + i) * U), sfrom[i], sto[i], 1, 1);
+        }
+        __syncthreads();   // the batch is read until here
+    }
+}
+
+// ---------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------
+
+struct ForkPlan {
+    int state;      // 0: nothing to do, 1: carried out
+    int fresh;      // the page that takes the partial page's copy, or -1
+    int full;       // shared pages
+    int part;       // tokens of the partial page
+};
+
+__global__ void __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ parents,
+                     const int32_t* __restrict__ children, int n, ForkPlan* plan, int* need,
+                     int* first, unsigned* err) {
+    __shared__ int s[32];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = threadIdx.x; r < t.B; r += kPlanThreads) first[r] = 0x7fffffff;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        const int c = children[i];
+        if (parents[i] >= 0 && parents[i] < t.B && c >= 0 && c < t.B) atomicMin(first + c, i);
+    }
+    __syncthreads();
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        const int p = parents[i], c = children[i];
+        ForkPlan f = {0, -1, 0, 0};
+        if (p >= 0 && c >= 0) {
+            unsigned bad = p >= t.B || c >= t.B ? kErrRow : 0u;
+            int ctx = 0;
+            if (!bad) {
+                ctx = __ldcg(t.ctx_lens + p);
+                if (__ldcg(first + c) != i || __ldcg(t.ctx_lens + c) != 0 ||
+                    __ldcg(t.block_table + (size_t)c * t.max_blocks) >= 0)
+                    bad |= kErrAlias;
+                if (ctx < 0 || ctx > t.max_blocks * t.page) bad |= kErrCtx;
+            }
+            if (!bad) {
+                f.full = ctx / t.page;
+                f.part = ctx % t.page;
+                const int used = f.full + (f.part > 0);
+                bool out = false;
+                for (int j = lane; j < used; j += 32) {
+                    const int e = __ldcg(t.block_table + (size_t)p * t.max_blocks + j);
+                    out |= e < 0 || e >= num_blocks;
+                }
+                if (__any_sync(0xffffffffu, out)) bad |= kErrBlock;
+            }
+            if (bad && lane == 0) set_error(err, bad);
+            f.state = !bad && ctx > 0;
+        }
+        if (lane == 0) plan[i] = f;
+    }
+    __syncthreads();
+    // ranks of the partial pages in list order, then the lowest free pages
+    int want = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        const bool w = i < n && plan[i].state && plan[i].part > 0;
+        int total;
+        const int rank = want + block_exclusive(w, s, total);
+        if (w) need[rank] = i;
+        want += total;
+    }
+    __syncthreads();
+    const int found = lowest_free(t.refcount, num_blocks, want, s,
+                                  [&](int rank, int page) { plan[need[rank]].fresh = page; });
+    __syncthreads();
+    for (int k = found + (int)threadIdx.x; k < want; k += kPlanThreads) {
+        plan[need[k]].state = 0;
+        if (k == found) set_error(err, kErrPages);
+    }
+}
+
+// Units of all forks dealt out in turn (forks differ in how much of their
+// last page is used); the tables and counts of fork i by CTA i mod grid.
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_apply_kernel(const __grid_constant__ CacheList c, const PageTables t,
+                      const int32_t* __restrict__ parents, const int32_t* __restrict__ children,
+                      int n, const ForkPlan* plan) {
+    pdl_wait();
+    pdl_trigger();
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const ForkPlan f = plan[i];
+        if (!f.state) continue;
+        const int32_t* from = t.block_table + (size_t)parents[i] * t.max_blocks;
+        int32_t* to = t.block_table + (size_t)children[i] * t.max_blocks;
+        for (int j = threadIdx.x; j < t.max_blocks; j += kCopyThreads) {
+            int e = -1;
+            if (j < f.full) {
+                e = from[j];
+                atomicAdd(t.refcount + e, 1);
+            } else if (j == f.full && f.part > 0) {
+                e = f.fresh;
+                t.refcount[e] = 1;
+            }
+            to[j] = e;
+        }
+        if (threadIdx.x == 0) t.ctx_lens[children[i]] = f.full * t.page + f.part;
+    }
+    const unsigned U = c.first_unit[c.num_caches];
+    const long total = (long)n * U;
+    for (long u = blockIdx.x; u < total; u += gridDim.x) {
+        const int i = (int)(u / U);
+        const ForkPlan f = plan[i];
+        if (!f.state || f.part == 0) continue;
+        const int src = t.block_table[(size_t)parents[i] * t.max_blocks + f.full];
+        copy_page_unit(c, (unsigned)(u - (long)i * U), src, f.fresh, f.part, t.page);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// reserve
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kPlanThreads)
+    reserve_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ rows,
+                   const int32_t* __restrict__ tokens, int n, int* need, int* first, int* fresh,
+                   unsigned* err) {
+    __shared__ int s[32];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = threadIdx.x; r < t.B; r += kPlanThreads) first[r] = 0x7fffffff;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlanThreads)
+        if (rows[i] >= 0 && rows[i] < t.B) atomicMin(first + rows[i], i);
+    __syncthreads();
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        const int r = rows[i], tok = tokens[i];
+        int count = 0;
+        if (r >= 0) {
+            unsigned bad = r >= t.B ? kErrRow : 0u;
+            if (!bad && __ldcg(first + r) != i) bad = kErrAlias;
+            if (!bad && (tok < 0 || tok > t.max_blocks * t.page)) bad = kErrCtx;
+            if (!bad) {
+                const int entries = ceil_div(tok, t.page);
+                for (int j = lane; j < entries; j += 32)
+                    count += __ldcg(t.block_table + (size_t)r * t.max_blocks + j) < 0;
+                count = warp_sum_i(count);
+            } else if (lane == 0) {
+                set_error(err, bad);
+            }
+        }
+        if (lane == 0) need[i] = count;
+    }
+    __syncthreads();
+    // need[i] becomes the row's first rank; a row is served if its last rank
+    // is below the number of free pages
+    long want = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        // one row needs at most max_blocks pages and a pool has fewer than
+        // 2^31: a rank past the pool is held at its size
+        const int v = i < n ? min(need[i], num_blocks) : 0;
+        int total;
+        const long rank = want + (unsigned)block_exclusive(v, s, total);
+        if (i < n) need[i] = v == 0 ? -1 : (int)min(rank, (long)num_blocks);
+        want = min(want + (unsigned)total, (long)num_blocks + 1);
+    }
+    __syncthreads();
+    const int found = lowest_free(t.refcount, num_blocks, (int)min(want, (long)num_blocks), s,
+                                  [&](int rank, int page) { fresh[rank] = page; });
+    __syncthreads();
+    for (int i = warp; i < n; i += kPlanThreads / 32) {
+        const int base = need[i];
+        if (base < 0) continue;
+        int32_t* row = t.block_table + (size_t)rows[i] * t.max_blocks;
+        const int entries = ceil_div(tokens[i], t.page);
+        int count = 0;
+        for (int j = lane; j < entries; j += 32) count += row[j] < 0;
+        count = warp_sum_i(count);
+        if (count > found - base) {
+            if (lane == 0) set_error(err, kErrPages);
+            continue;
+        }
+        int at = base;
+        for (int j0 = 0; j0 < entries; j0 += 32) {
+            const int j = j0 + lane;
+            const bool empty = j < entries && row[j] < 0;
+            const unsigned m = __ballot_sync(0xffffffffu, empty);
+            if (empty) {
+                const int page = fresh[at + __popc(m & ((1u << lane) - 1u))];
+                row[j] = page;
+                t.refcount[page] = 1;
+            }
+            at += __popc(m);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// free
+// ---------------------------------------------------------------------------
+
+// One warp per listed row. Each entry is taken by an atomic exchange, so a row
+// named twice gives its pages back once.
+__global__ void __launch_bounds__(kCopyThreads)
+    free_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ rows, int n,
+                unsigned* err) {
+    pdl_wait();
+    pdl_trigger();
+    const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (i >= n) return;
+    const int r = rows[i];
+    if (r < 0) return;
+    if (r >= t.B) {
+        if (lane == 0) set_error(err, kErrRow);
+        return;
+    }
+    int32_t* row = t.block_table + (size_t)r * t.max_blocks;
+    for (int j = lane; j < t.max_blocks; j += 32) {
+        if (__ldcg(row + j) < 0) continue;
+        const int e = atomicExch(row + j, -1);
+        if (e < 0) continue;
+        if (e >= num_blocks) {
+            set_error(err, kErrBlock);
+        } else if (atomicSub(t.refcount + e, 1) <= 0) {
+            atomicAdd(t.refcount + e, 1);   // the page was free already
+            set_error(err, kErrBlock);
+        }
+    }
+    if (lane == 0) t.ctx_lens[r] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------
+
+// head[0] = live pages, head[1] = moves; move k takes page from[k] (the k-th
+// live page at or past head[0]) to page to[k] (the k-th free page below it);
+// remap[p - head[0]] for p >= head[0]: the page's new number, -1 if free.
+__global__ void __launch_bounds__(kPlanThreads)
+    compact_plan_kernel(const int32_t* __restrict__ refcount, int num_blocks, int* head, int* from,
+                        int* to, int* remap, int32_t* num_live) {
+    __shared__ int s[32];
+    pdl_wait();
+    pdl_trigger();
+    const int quads = num_blocks / 4 + (num_blocks % 4 != 0);
+    int free_pages = 0;
+    for (int q = threadIdx.x; q < quads; q += kPlanThreads)
+        free_pages += __popc(free_mask(refcount, q, num_blocks));
+    int total;
+    block_exclusive(free_pages, s, total);
+    const int live = num_blocks - total;
+    const int holes = lowest_free(refcount, live, num_blocks, s,
+                                  [&](int rank, int page) { to[rank] = page; });
+    __syncthreads();
+    int moved = 0;
+    for (int q0 = live / 4; q0 < quads; q0 += kPlanThreads) {
+        const int q = q0 + (int)threadIdx.x;
+        unsigned used = 0;
+        if (q < quads) {
+            used = ~free_mask(refcount, q, num_blocks) & 15u;
+            for (int k = 0; k < 4; ++k)
+                if (4 * q + k < live || 4 * q + k >= num_blocks) used &= ~(1u << k);
+        }
+        int rank = moved + block_exclusive(__popc(used), s, total);
+        for (int k = 0; k < 4; ++k) {
+            const int p = 4 * q + k;
+            if (q >= quads || p < live || p >= num_blocks) continue;
+            int r = -1;
+            if (used >> k & 1u) {
+                r = to[rank];
+                from[rank++] = p;
+            }
+            remap[p - live] = r;
+        }
+        moved += total;
+    }
+    if (threadIdx.x == 0) {
+        head[0] = live;
+        head[1] = holes;
+        if (num_live) *num_live = live;
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_apply_kernel(const __grid_constant__ CacheList c, const PageTables t, const int* head,
+                         const int* from, const int* to, const int* remap, unsigned* err) {
+    pdl_wait();
+    pdl_trigger();
+    const int live = head[0], moves = head[1];
+    const long tid = (long)blockIdx.x * kCopyThreads + threadIdx.x;
+    const long stride = (long)gridDim.x * kCopyThreads;
+    for (long i = tid; i < (long)t.B * t.max_blocks; i += stride) {
+        const int e = t.block_table[i];
+        if (e < live) continue;
+        const int r = e < c.num_blocks ? remap[e - live] : -1;
+        if (r < 0) set_error(err, kErrBlock);   // left as it is
+        else t.block_table[i] = r;
+    }
+    for (long k = tid; k < moves; k += stride) {
+        t.refcount[to[k]] = t.refcount[from[k]];
+        t.refcount[from[k]] = 0;
+    }
+    const unsigned U = c.first_unit[c.num_caches];
+    const long total = (long)moves * U;
+    for (long u = blockIdx.x; u < total; u += gridDim.x) {
+        const int k = (int)(u / U);
+        copy_page_unit(c, (unsigned)(u - (long)k * U), from[k], to[k], 1, 1);
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+template <typename Kern, typename... Args>
+cudaError_t launch_pages(Kern kern, int grid, int block, const Launch& L, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// CTAs for `units` copy units of kUnitBytes at most.
+int copy_grid(long units, const Launch& L) {
+    return (int)std::max(1L, std::min(units, (long)L.num_sms * kCopyCtasPerSm));
+}
+
+constexpr size_t kPart = 256;
+size_t up(size_t x) { return (x + kPart - 1) / kPart * kPart; }
+
+// The workspace: plans [n], need [n], first [B], then three lists of
+// num_blocks page numbers, and a head.
+struct PageWs {
+    size_t plan, need, first, list, total;
+};
+PageWs page_ws(int num_blocks, int B, int n) {
+    PageWs w;
+    w.plan = kPart;
+    w.need = w.plan + up((size_t)n * sizeof(ForkPlan));
+    w.first = w.need + up((size_t)n * 4);
+    w.list = w.first + up((size_t)B * 4);
+    w.total = w.list + 3 * up((size_t)num_blocks * 4);
+    return w;
+}
+
+}  // namespace
+
+void page_units(CacheList& c) {
+    unsigned u = 0;
+    for (int k = 0; k < c.num_caches; ++k) {
+        c.first_unit[k] = u;
+        u += (c.page_bytes[k] + kUnitBytes - 1) / kUnitBytes;
+    }
+    c.first_unit[c.num_caches] = u;
+}
+
+size_t pages_workspace_bytes(int num_blocks, int B, int n) {
+    return page_ws(num_blocks, B, n).total;
+}
+
+cudaError_t launch_copy_pages(const CacheList& c, const int32_t* src, const int32_t* dst, int n,
+                              unsigned* err, const Launch& L) {
+    const long units = (long)n * c.first_unit[c.num_caches];
+    return launch_pages(copy_pages_kernel, copy_grid(units, L), kCopyThreads, L, c, src, dst, n,
+                        err);
+}
+
+cudaError_t launch_fork(const CacheList& c, const PageTables& t, const int32_t* parents,
+                        const int32_t* children, int n, void* ws, unsigned* err, const Launch& L) {
+    const PageWs w = page_ws(c.num_blocks, t.B, n);
+    unsigned char* p = static_cast<unsigned char*>(ws);
+    ForkPlan* plan = reinterpret_cast<ForkPlan*>(p + w.plan);
+    cudaError_t e = launch_pages(fork_plan_kernel, 1, kPlanThreads, L, t, c.num_blocks, parents,
+                                 children, n, plan, reinterpret_cast<int*>(p + w.need),
+                                 reinterpret_cast<int*>(p + w.first), err);
+    if (e != cudaSuccess) return e;
+    const long units = (long)n * c.first_unit[c.num_caches];
+    return launch_pages(fork_apply_kernel, copy_grid(units, L), kCopyThreads, L, c, t, parents,
+                        children, n, (const ForkPlan*)plan);
+}
+
+cudaError_t launch_reserve(const PageTables& t, int num_blocks, const int32_t* rows,
+                           const int32_t* tokens, int n, void* ws, unsigned* err, const Launch& L) {
+    const PageWs w = page_ws(num_blocks, t.B, n);
+    unsigned char* p = static_cast<unsigned char*>(ws);
+    return launch_pages(reserve_kernel, 1, kPlanThreads, L, t, num_blocks, rows, tokens, n,
+                        reinterpret_cast<int*>(p + w.need), reinterpret_cast<int*>(p + w.first),
+                        reinterpret_cast<int*>(p + w.list), err);
+}
+
+cudaError_t launch_free(const PageTables& t, int num_blocks, const int32_t* rows, int n,
+                        unsigned* err, const Launch& L) {
+    const int warps = kCopyThreads / 32;
+    return launch_pages(free_kernel, n / warps + (n % warps != 0), kCopyThreads, L, t, num_blocks,
+                        rows, n, err);
+}
+
+cudaError_t launch_compact(const CacheList& c, const PageTables& t, int32_t* num_live, void* ws,
+                           unsigned* err, const Launch& L) {
+    const PageWs w = page_ws(c.num_blocks, t.B, 0);
+    unsigned char* p = static_cast<unsigned char*>(ws);
+    const size_t list = up((size_t)c.num_blocks * 4);
+    int* head = reinterpret_cast<int*>(p);
+    int* from = reinterpret_cast<int*>(p + w.list);
+    int* to = reinterpret_cast<int*>(p + w.list + list);
+    int* remap = reinterpret_cast<int*>(p + w.list + 2 * list);
+    cudaError_t e = launch_pages(compact_plan_kernel, 1, kPlanThreads, L,
+                                 (const int32_t*)t.refcount, c.num_blocks, head, from, to, remap,
+                                 num_live);
+    if (e != cudaSuccess) return e;
+    return launch_pages(compact_apply_kernel, L.num_sms * kCopyCtasPerSm, kCopyThreads, L, c, t,
+                        (const int*)head, (const int*)from, (const int*)to, (const int*)remap, err);
+}
+
+}  // namespace a8w8
