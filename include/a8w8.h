@@ -387,11 +387,13 @@ a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
  * the same B, Hq, Hkv, D and max_blocks * page_size; its contents need no
  * initialisation), and in float32 arithmetic where the BF16 form is in
  * two-float: the scores are float32 sums of exact products, the softmax
- * weights are taken to 2^-12 of themselves (or 2^-16 of their request's
- * largest weight * s, where that is more) before the products with the codes,
- * and out is rounded to BF16 once. A token whose block id is outside [0,
- * num_blocks) counts as a row of zeros and flags A8W8_DEVERR_BLOCK; a NaN row
- * makes the heads that attend to it NaN. */
+ * weights times s are rounded to FP16 (2^-11 relative) before the products
+ * with the codes, all sums are float32, and out is rounded to BF16 once. A
+ * token whose block id is outside [0, num_blocks) counts as a row of zeros and
+ * flags A8W8_DEVERR_BLOCK; a NaN row makes the heads that attend to it NaN,
+ * and so does a query head with a NaN, an infinity or a value of 2^118 or
+ * more. B is at most 65535, B * Hq at most 2^24, num_blocks * page_size below
+ * 2^31. */
 a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
                                         const uint8_t* v_codes, const a8w8_bf16* k_meta,
                                         const a8w8_bf16* v_meta, const int32_t* block_table,

@@ -69,12 +69,14 @@ def kv_write(k, v, slots, k_codes, v_codes, k_meta, v_meta) -> int:
 
 def attention(q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, page, scale=None):
     """Decode attention [B, Hq, D] in float64, and an elementwise bound on how far a float32
-    evaluation that takes the weights p s to 2^-11 (and 2^-17 of the largest) may be from it:
+    evaluation that takes the weights p s to FP16 may be from it:
 
       scores: at most (D + 16) roundings of 2^-24 of sum |q| |c s| + |m| sum |q| (the codes' and
-        the minimum's part apart, as they are added), and 2^-21 of max |q| for the parts that q
-        is split into; d(exp) = exp d(score), and 2^-21 for the exponential itself;
-      weights: 2^-11 relative to p s, times the code; 2^-17 of the largest p s per token;
+        the minimum's part apart, as they are added), and 2^-34 of max |q| where q's smallest
+        parts leave FP16's range; d(exp) = exp d(score), and 2^-21 for the exponential itself;
+      weights: 2^-11 relative to p s, times the code; 2^-34 of the largest p s per token (below
+        FP16's range);
+      sums: 2^-20 of their absolute terms;
       a bad block id counts as rows of zeros."""
     q = bf16_to_f64(q)
     B, Hq, D = q.shape
@@ -106,11 +108,11 @@ def attention(q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, page, 
                     a = np.abs(x)
                     mag = (kc @ a) * np.abs(km[:, 0]) + np.abs(km[:, 1]) * a.sum()
                     ds = abs(scale) * ((D + 16) * 2.0 ** -24 * mag
-                                       + 2.0 ** -21 * a.max() * kc.sum(1) * np.abs(km[:, 0]))
+                                       + 2.0 ** -34 * a.max() * kc.sum(1) * np.abs(km[:, 0]))
                     dp = p * (np.expm1(np.minimum(ds, 50.0)) + 2.0 ** -21)
                     w = p * np.abs(vm[:, 0])
                     bound[b, h * G + g] = (dp @ np.abs(V) + dp.sum() * np.abs(o)
-                                           + 2.0 ** -11 * (w @ vc) + 2.0 ** -17 * w.max() * vc.sum(0)
+                                           + 2.0 ** -11 * (w @ vc) + 2.0 ** -34 * w.max() * vc.sum(0)
                                            + 2.0 ** -20 * (p @ (np.abs(vm[:, :1]) * vc
                                                                 + np.abs(vm[:, 1:]))))
                 out[b, h * G + g] = o

@@ -8,35 +8,38 @@
 // everything else is one number per (token, head).
 //
 // What bounds it: D + 8 bytes per (token, KV head) from HBM. At the measured
-// copy rate an SM receives 16 tokens' rows (2.2 KB at D = 128) in about 95
-// cycles, in which it can issue 380 warp instructions; unpacking 4096 codes to
-// 16-bit floats alone would take half of them. An integer 0..15 in a byte is,
-// read as e4m3, exactly c 2^-9 (c < 8 is a subnormal, 8..15 the first binade),
-// so a word of eight codes becomes two operand registers of mma.sync
-// m16n8k32 e4m3 with two masks and a shift, and no conversion. The other
-// operand is split into e4m3 parts whose products with the codes are exact
-// and summed in float32 by the tensor cores (measured on this GPU: 2100
-// TFLOP/s against 600 for bf16 m16n8k16, sums exact to float32 rounding):
-//   * q, scaled by a power of two to a maximum in [128, 256): two parts of
-//     four significant bits hold the eight of a BF16, down to 2^-21 of the
-//     head's largest |q|. Query heads are rows 0..7 of the A operand, their
-//     low parts (times 2^5) rows 8..15: one instruction does both.
-//   * the weights p_t s_t: rounded to FP16 (2^-11 relative; beside the BF16
-//     result's 2^-8 this is what keeps them out of its error) and split into
-//     three parts of one common scale, so that all add into one accumulator;
-//     ref keeps the largest between 128 and 448, and the last bit of e4m3
-//     stands 2^-17 below that.
-// The score accumulator holds (head, token) pairs in the same lanes that the
-// weights' operand needs them in (tokens are permuted alike for K and V), so
-// nothing is exchanged between the two products. For V the contraction runs
-// over tokens: a lane reads 8 tokens' bytes for its 16 dimensions and
-// transposes 4 x 4 bytes with eight permutes.
+// copy rate an SM receives 32 tokens' rows (4.4 KB at D = 128) in about 190
+// cycles, in which it issues at most 760 warp instructions, 380 of them on the
+// integer pipe, for 8192 codes. So the two products run on the tensor cores
+// (mma.sync m16n8k16 f16, 600 TFLOP/s here: 64 of the 190 cycles) and codes
+// become operands without a conversion: an integer 0..15 in the lowest
+// mantissa bits of an FP16 is the subnormal c 2^-24, in the next four bits c
+// 2^-20, both exact, so a word of eight codes is four operand registers after
+// four masks and a shift. (mma.sync on e4m3 bytes, where a nibble is exact
+// too, compiles to conversions and f16 instructions on sm_103a: 1131
+// instructions per tile and head against 440 here, 221 us against XXX at batch
+// 64.) The power of two is taken back in the other operand or the result:
+//   * q, scaled per head by a power of two to a maximum in [2^10, 2^11) (times
+//     16 beside the low nibbles): the eight significant bits of a BF16 are
+//     exact in FP16 down to 2^-35 of the head's largest |q|. Tokens are the
+//     rows, query heads the columns, so a group of up to 8 heads costs one
+//     instruction per 16 tokens and 16 dimensions.
+//   * the weights p_t s_t, rounded to FP16: 2^-11 relative, beside the 2^-8 of
+//     the BF16 result. ref keeps the largest between 2^10 and 2^15, so that
+//     what FP16 cannot hold lies 2^-35 below it. One 8 x 8 transpose
+//     (movmatrix) per 8 tokens takes them from the score's layout into the
+//     operand's.
+// For V the contraction runs over tokens: a lane reads four tokens' bytes for
+// its 16 dimensions per 16 tokens and pairs the halves of two words by one
+// permute each.
 //
 // Work is cut into tiles of 32 tokens of one (request, KV head), numbered
 // through all requests; a CTA takes an equal run of them, whatever the
 // contexts, and its four warps take the run's tiles in turn, each with a
 // private cp.async ring (no CTA barrier inside a run). Runs that end inside a
 // (request, KV head) leave their (ref, sum, o) to a second kernel.
+#include <algorithm>
+
 #include "kernels.cuh"
 
 namespace a8w8 {
@@ -60,57 +63,32 @@ constexpr int smem_bytes(int D) {
     return ring > merge_bytes(D) ? ring : merge_bytes(D);
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], unsigned a0, unsigned a1, unsigned a2,
-                                         unsigned a3, unsigned b0, unsigned b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], unsigned a0, unsigned a1, unsigned a2,
+                                        unsigned a3, unsigned b0, unsigned b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Two floats as e4m3 bytes (a in the low byte), and two e4m3 bytes as FP16.
-__device__ __forceinline__ unsigned short e4m3_of(float a, float b) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-}
-__device__ __forceinline__ unsigned short e4m3_of_h2(unsigned h) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
-__device__ __forceinline__ unsigned h2_of_e4m3(unsigned short e) {
-    unsigned r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(e));
-    return r;
-}
-__device__ __forceinline__ unsigned h2_of(float a, float b) {
+__device__ __forceinline__ unsigned h2_of(float a, float b) {   // a in the low half
     unsigned r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ unsigned h2_sub(unsigned a, unsigned b) {
+// 8 x 8 halves, row lane / 4, columns 2 (lane % 4) and the next: transposed.
+__device__ __forceinline__ unsigned transpose8(unsigned v) {
     unsigned r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ float2 h2_floats(unsigned h) {
-    float2 f;
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
-        : "=f"(f.x), "=f"(f.y)
-        : "r"(h));
-    return f;
-}
-__device__ __forceinline__ unsigned join16(unsigned short lo, unsigned short hi) {
-    return (unsigned)lo | (unsigned)hi << 16;
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void cp16z(unsigned s, const void* g, unsigned n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
+__device__ __forceinline__ void cp16(unsigned s, const void* g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(g) : "memory");
 }
 __device__ __forceinline__ void cp4z(unsigned s, const void* g, unsigned n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
@@ -157,11 +135,13 @@ __device__ __forceinline__ long cta_exclusive(long v, long* s, long& total) {
     return before + x - v;
 }
 
-// The runs: CTA c of E takes tiles [c T / E, (c + 1) T / E) of T = Hkv sum_b
-// tiles(b), request after request, KV heads inside a request.
-__device__ __forceinline__ long run_ctas(long T, int grid) {
+// The runs: run r of E takes tiles [r T / E, (r + 1) T / E) of T = sum_b
+// tiles(b), request after request; the CTAs of a run's KV heads stand side by
+// side (CTA r Hkv + h), so that the sectors that hold several heads' (s, m)
+// words and the lines that hold their codes are read together.
+__device__ __forceinline__ long run_count(long T, int runs) {
     const long e = (T + kMinTiles - 1) / kMinTiles;
-    return e < grid ? e : grid;
+    return e < runs ? e : runs;
 }
 
 struct PartView {
@@ -200,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     // ---- where the run begins -------------------------------------------------
     long x0, x1;                   // the run's tiles
-    int b, h, j, tokens;           // its first tile: request, KV head, tile
+    int b, h, j, tokens;           // its first tile: request, KV head, tile of the request
     if (whole) {
         b = blockIdx.x / p.Hkv;
         h = blockIdx.x - b * p.Hkv;
@@ -228,29 +208,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             mine += tiles_of(tokens_of(p, i));
         }
-        long total;
-        const long before = cta_exclusive<kThreads>(mine, s_scan, total);
-        const long T = total * p.Hkv, E = run_ctas(T, gridDim.x);
-        if (blockIdx.x >= E) return;
-        x0 = T * blockIdx.x / E;
-        x1 = T * (blockIdx.x + 1) / E;
-        if (mine > 0 && x0 >= before * p.Hkv && x0 < (before + mine) * p.Hkv) {
+        long T;
+        const long before = cta_exclusive<kThreads>(mine, s_scan, T);
+        const long E = run_count(T, gridDim.x / p.Hkv);
+        const long r = blockIdx.x / p.Hkv;
+        h = blockIdx.x - (int)r * p.Hkv;
+        if (r >= E) return;
+        x0 = T * r / E;
+        x1 = T * (r + 1) / E;
+        if (mine > 0 && x0 >= before && x0 < before + mine) {
             long at = before;
             int i = b0;
             for (;; ++i) {
                 const int n = tiles_of(tokens_of(p, i));
-                if (x0 < (at + n) * p.Hkv) break;
+                if (x0 < at + n) break;
                 at += n;
             }
             s_b = i;
-            s_first = at * p.Hkv;
+            s_first = at;
         }
         __syncthreads();
         b = s_b;
         tokens = tokens_of(p, b);
-        const long in = x0 - s_first;
-        h = (int)(in / tiles_of(tokens));
-        j = (int)(in - (long)h * tiles_of(tokens));
+        j = (int)(x0 - s_first);
     }
 
     // ---- lane constants -----------------------------------------------------
@@ -269,52 +249,71 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // the column that token `lane` stands in, for the (s, m) words
     const int mcol = (lane & ~7) + (lane & 6) + ((lane & 1) ^ ((lane >> 2) & 1));
 
+    const unsigned rstride = (unsigned)p.Hkv * RB, mstride = (unsigned)p.Hkv * 4;
+    const unsigned char* kc = p.c.k_codes + h * RB + cchunk * 16;
+    const unsigned char* vc = p.c.v_codes + h * RB + cchunk * 16;
+    const unsigned char* km = reinterpret_cast<const unsigned char*>(p.c.k_meta) + h * 4;
+    const unsigned char* vm = reinterpret_cast<const unsigned char*>(p.c.v_meta) + h * 4;
+
     bool first = true;                          // the run's first segment
     while (x0 < x1) {
         const int n_all = tiles_of(tokens);
         const int j1 = (int)min((long)n_all, j + (x1 - x0));
         const int32_t* table = p.block_table + (size_t)b * p.max_blocks;
 
-        // Copies tile i of the segment's request into ring stage st: a token's
-        // row number once per lane, handed to the lanes that copy its chunks.
-        auto fetch = [&](int i, int st) {
+        // The page and the place in it of token `lane` of tile i, looked up one
+        // tile before the copies that need it.
+        int blk = -1, in_page = 0;
+        auto lookup = [&](int i) {
             const unsigned tok = (unsigned)i * kTile + lane;
-            int slot = -1;
+            blk = -1;
             if (i < j1 && (int)tok < tokens) {
                 unsigned q = __umulhi(tok, page_inv), r = tok - q * p.page;
                 if (r >= (unsigned)p.page) {
                     ++q;
                     r -= p.page;
                 }
-                const int blk = __ldg(table + q);
-                if (blk >= 0 && blk < p.num_blocks) slot = blk * p.page + (int)r;
-                else set_error(p.err, 0x2u);
+                blk = __ldg(table + q);
+                in_page = (int)r;
+                if (blk < 0 || blk >= p.num_blocks) {
+                    blk = -1;
+                    set_error(p.err, 0x2u);
+                }
             }
+        };
+        // Copies tile i into ring stage st. A token without a row (past the
+        // context, or a bad page) gets s = m = 0 and the codes of row 0, which
+        // count nothing then.
+        auto fetch = [&](int i, int st) {
             if (i < j1) {                        // warp-uniform
+                const bool ok = blk >= 0;
+                const unsigned slot = ok ? (unsigned)(blk * p.page + in_page) : 0u;
                 const unsigned base = ring + st * stage_bytes(D);
 #pragma unroll
                 for (int k = 0; k < kTile / RPI; ++k) {
-                    const int sl = __shfl_sync(0xffffffffu, slot, k * RPI + crow);
-                    const size_t off = sl < 0 ? 0 : ((size_t)sl * p.Hkv + h) * RB + cchunk * 16;
-                    const unsigned n = sl < 0 ? 0u : 16u;
+                    const unsigned sl = __shfl_sync(0xffffffffu, slot, k * RPI + crow);
                     const unsigned d = base + k * RPI * RB + coff;
-                    cp16z(d, p.c.k_codes + off, n);
-                    cp16z(d + code_bytes(D), p.c.v_codes + off, n);
+                    cp16(d, kc + (size_t)sl * rstride);
+                    cp16(d + code_bytes(D), vc + (size_t)sl * rstride);
                 }
-                const size_t row = slot < 0 ? 0 : (size_t)slot * p.Hkv + h;
-                const unsigned n = slot < 0 ? 0u : 4u;
                 const unsigned d = base + 2 * code_bytes(D) + mcol * 8;
-                cp4z(d, p.c.k_meta + 2 * row, n);
-                cp4z(d + 4, p.c.v_meta + 2 * row, n);
+                cp4z(d, km + (size_t)slot * mstride, ok ? 4u : 0u);
+                cp4z(d + 4, vm + (size_t)slot * mstride, ok ? 4u : 0u);
             }
             cp_async_commit();
         };
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) fetch(j + warp + s * kWarps, s);
+        for (int s = 0; s < kStages; ++s) {
+            lookup(j + warp + s * kWarps);
+            fetch(j + warp + s * kWarps, s);
+        }
+        lookup(j + warp + kStages * kWarps);
 
-        // ---- the query heads' parts ---------------------------------------------
-        unsigned qa[KW][4];
-        float ch, qsum;                         // score factors of head g
+        // ---- the query heads ------------------------------------------------------
+        // head g's dimensions of chunk t: for word w, elements (0, 4) and (2, 6)
+        // times 16 meet the low nibbles of the masks, (1, 5) and (3, 7) the high
+        unsigned qb[KW][4];
+        float ch0, ch1, qs0, qs1;               // score factors of heads 2 t, 2 t + 1
         {
             const bf16* q = p.q + ((size_t)b * p.Hq + (size_t)h * G + (g < G ? g : 0)) * D + t * (D / 4);
             float sum = 0.0f, top = 0.0f;
@@ -335,40 +334,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
-            // 2^e takes the largest |q| into [128, 256)
-            const int e = max(-111, min(110, 134 - (int)(__float_as_uint(top) >> 23)));
+            // 2^e takes the largest |q| into [2^10, 2^11)
+            const int e = max(-107, min(126, 137 - (int)(__float_as_uint(top) >> 23)));
             const float up = __uint_as_float((unsigned)(127 + e) << 23);
             const float sc = p.scale * 1.4426950408889634f;
-            ch = __uint_as_float((unsigned)(127 + 9 - e) << 23) * sc;
-            qsum = sum * sc;
-            // a NaN shows in the sum; above 2^118 the parts would saturate
+            float ch = __uint_as_float((unsigned)(127 + 20 - e) << 23) * sc;
+            // a NaN shows in the sum; from 2^118 on FP16 would overflow
             if (!(fabsf(sum) <= 3e38f) || top >= 3.3e35f) ch = __uint_as_float(0x7FC00000u);
+            const float qs = sum * sc;
+            ch0 = __shfl_sync(0xffffffffu, ch, 8 * t);
+            ch1 = __shfl_sync(0xffffffffu, ch, 8 * t + 4);
+            qs0 = __shfl_sync(0xffffffffu, qs, 8 * t);
+            qs1 = __shfl_sync(0xffffffffu, qs, 8 * t + 4);
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 float f[8];
                 unpack8(raw[w], f);
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {   // even elements: low nibbles; odd: high
-                    unsigned short hi[2], lo[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float a = f[4 * k + o] * up, c = f[4 * k + 2 + o] * up;
-                        hi[k] = e4m3_of(a, c);
-                        const float2 r = h2_floats(h2_of_e4m3(hi[k]));
-                        lo[k] = e4m3_of((a - r.x) * 32.0f, (c - r.y) * 32.0f);
-                    }
-                    qa[w][2 * o] = join16(hi[0], hi[1]);
-                    qa[w][2 * o + 1] = join16(lo[0], lo[1]);
+                for (int k = 0; k < 4; ++k) {
+                    const float m = k & 1 ? up : up * 16.0f;
+                    qb[w][k] = h2_of(f[k] * m, f[4 + k] * m);
                 }
             }
         }
 
-        float acc[4 * VW][4];                   // o 2^-9: rows dims, columns heads 2 t, 2 t + 1
+        // rows: dimensions 2 i (times 2^-24) and 2 i + 1 (times 2^-20) of the lane's;
+        // columns: heads 2 t, 2 t + 1
+        float acc[4 * VW][4];
 #pragma unroll
         for (int i = 0; i < 4 * VW; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
-        float ref = kNoRef, l = 0.0f, om = 0.0f;   // of head g, over the lane's tokens
+        // of heads 2 t, 2 t + 1, over the lane's tokens
+        float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.0f, l1 = 0.0f, om0 = 0.0f, om1 = 0.0f;
 
         int st = 0;
         for (int i = j + warp; i < j1; i += kWarps) {
@@ -376,72 +374,85 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             __syncwarp();
             const unsigned base = ring + st * stage_bytes(D);
 
-            // ---- scores: head g, tokens 8 k + (2 t, 2 t + 1) of the tile --------
-            float y[8], sv[8], mv[8];
+            // ---- scores: token g of each 8, heads 2 t and 2 t + 1 --------------------
+            float y0[4], y1[4], sv[4], mv[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                unsigned kw[KW];
-                if constexpr (D == 128) {
-                    const int4 v = lds_v4(base + 8 * k * RB + koff);
-                    kw[0] = v.x;
-                    kw[1] = v.y;
-                    kw[2] = v.z;
-                    kw[3] = v.w;
-                } else {
-                    const uint2 v = lds_v2(base + 8 * k * RB + koff);
-                    kw[0] = v.x;
-                    kw[1] = v.y;
+            for (int k = 0; k < 4; k += 2) {
+                unsigned ka[2][KW];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if constexpr (D == 128) {
+                        const int4 v = lds_v4(base + 8 * (k + r) * RB + koff);
+                        ka[r][0] = v.x;
+                        ka[r][1] = v.y;
+                        ka[r][2] = v.z;
+                        ka[r][3] = v.w;
+                    } else {
+                        const uint2 v = lds_v2(base + 8 * (k + r) * RB + koff);
+                        ka[r][0] = v.x;
+                        ka[r][1] = v.y;
+                    }
                 }
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int w = 0; w < KW; ++w)
-                    mma_e4m3(c, qa[w][0], qa[w][1], qa[w][2], qa[w][3], kw[w] & 0x0F0F0F0Fu,
-                             (kw[w] >> 4) & 0x0F0F0F0Fu);
-                const int4 mt = lds_v4(base + 2 * code_bytes(D) + (8 * k + 2 * t) * 8);
-                const float a0 = __fmaf_rn(c[2], 0.03125f, c[0]) * ch;
-                const float a1 = __fmaf_rn(c[3], 0.03125f, c[1]) * ch;
-                y[2 * k] = __fmaf_rn(a0, bf_lo(mt.x), qsum * bf_hi(mt.x));
-                y[2 * k + 1] = __fmaf_rn(a1, bf_lo(mt.z), qsum * bf_hi(mt.z));
-                sv[2 * k] = bf_lo(mt.y);
-                mv[2 * k] = bf_hi(mt.y);
-                sv[2 * k + 1] = bf_lo(mt.w);
-                mv[2 * k + 1] = bf_hi(mt.w);
+                for (int w = 0; w < KW; ++w) {
+                    const unsigned u0 = ka[0][w], u1 = ka[1][w], v0 = u0 >> 8, v1 = u1 >> 8;
+                    mma_f16(c, u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u,
+                            u1 & 0x00F000F0u, qb[w][0], qb[w][1]);
+                    mma_f16(c, v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u,
+                            v1 & 0x00F000F0u, qb[w][2], qb[w][3]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint2 mt = lds_v2(base + 2 * code_bytes(D) + (8 * (k + r) + g) * 8);
+                    const float ks = bf_lo(mt.x), km = bf_hi(mt.x);
+                    sv[k + r] = bf_lo(mt.y);
+                    mv[k + r] = bf_hi(mt.y);
+                    y0[k + r] = __fmaf_rn(c[2 * r] * ch0, ks, qs0 * km);
+                    y1[k + r] = __fmaf_rn(c[2 * r + 1] * ch1, ks, qs1 * km);
+                }
             }
             if ((i + 1) * kTile > tokens) {     // the request's last tile
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int tok = i * kTile + 8 * (k >> 1) + 2 * t + ((k & 1) ^ (t >> 1));
-                    if (tok >= tokens) y[k] = -INFINITY;
-                }
+                for (int k = 0; k < 4; ++k)
+                    if (i * kTile + 8 * k + krow >= tokens) y0[k] = y1[k] = -INFINITY;
             }
 
             // ---- weights -----------------------------------------------------------
-            // ref is raised only where a weight would pass e4m3's 448 (or a
-            // probability with s near 0 would pass 2^90); the raise takes the
-            // tile's largest to 128
-            float pr[8], wt[8];
+            // ref is raised only where a weight would pass 2^15 (or a probability
+            // with s near 0 would pass 2^90); the raise takes the tile's largest
+            // to 2^10
+            float p0[4], p1[4];
             float big = 0.0f, bigp = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                pr[k] = ex2(y[k] - ref);
-                wt[k] = pr[k] * sv[k];
-                big = fmaxf(big, fabsf(wt[k]));
-                bigp = fmaxf(bigp, pr[k]);
+            for (int k = 0; k < 4; ++k) {
+                p0[k] = ex2(y0[k] - ref0);
+                p1[k] = ex2(y1[k] - ref1);
+                const float pm = fmaxf(p0[k], p1[k]);
+                big = fmaxf(big, fabsf(pm * sv[k]));
+                bigp = fmaxf(bigp, pm);
             }
-            if (__any_sync(0xffffffffu, big > 448.0f || bigp > 1.2e27f)) {
-                float z = kNoRef;
+            if (__any_sync(0xffffffffu, big > 32768.0f || bigp > 1.2e27f)) {
+                float z0 = kNoRef, z1 = kNoRef;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    z = fmaxf(z, y[k] + log2f(fmaxf(fabsf(sv[k]), 8.3e-25f)));
-                z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 1));
-                z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
-                const float up = fmaxf(ref, z - 7.0f);
-                const float f = ex2(ref - up);
-                ref = up;
-                l *= f;
-                om *= f;
-                const float f0 = __shfl_sync(0xffffffffu, f, 8 * t);
-                const float f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+                for (int k = 0; k < 4; ++k) {
+                    const float ls = log2f(fmaxf(fabsf(sv[k]), 8.3e-25f));
+                    z0 = fmaxf(z0, y0[k] + ls);
+                    z1 = fmaxf(z1, y1[k] + ls);
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, o));
+                    z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, o));
+                }
+                const float n0 = fmaxf(ref0, z0 - 10.0f), n1 = fmaxf(ref1, z1 - 10.0f);
+                const float f0 = ex2(ref0 - n0), f1 = ex2(ref1 - n1);
+                ref0 = n0;
+                ref1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+                om0 *= f0;
+                om1 *= f1;
 #pragma unroll
                 for (int q = 0; q < 4 * VW; ++q) {
                     acc[q][0] *= f0;
@@ -450,72 +461,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     acc[q][3] *= f1;
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    pr[k] = ex2(y[k] - ref);
-                    wt[k] = pr[k] * sv[k];
+                for (int k = 0; k < 4; ++k) {
+                    p0[k] = ex2(y0[k] - ref0);
+                    p1[k] = ex2(y1[k] - ref1);
                 }
             }
+            unsigned wb[4];                     // head g, tokens 2 t, 2 t + 1 of each 8
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                l += pr[k];
-                om = __fmaf_rn(pr[k], mv[k], om);
-            }
-            unsigned wb[3][2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                unsigned r0 = h2_of(wt[4 * q], wt[4 * q + 1]), r1 = h2_of(wt[4 * q + 2], wt[4 * q + 3]);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const unsigned short e0 = e4m3_of_h2(r0), e1 = e4m3_of_h2(r1);
-                    wb[k][q] = join16(e0, e1);
-                    if (k < 2) {
-                        r0 = h2_sub(r0, h2_of_e4m3(e0));
-                        r1 = h2_sub(r1, h2_of_e4m3(e1));
-                    }
-                }
+            for (int k = 0; k < 4; ++k) {
+                l0 += p0[k];
+                l1 += p1[k];
+                om0 = __fmaf_rn(p0[k], mv[k], om0);
+                om1 = __fmaf_rn(p1[k], mv[k], om1);
+                wb[k] = transpose8(h2_of(p0[k] * sv[k], p1[k] * sv[k]));
             }
 
             // ---- o += V^T w ----------------------------------------------------------
-            unsigned x[2][4][VW];               // [token quad][token][word]
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int k = 0; k < 4; k += 2) {
+                unsigned x[4][VW];              // tokens 2 t, 2 t + 1 of two groups of 8
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const unsigned at = base + code_bytes(D) + (2 * q + (k >> 1)) * 8 * RB +
-                                        ((k & 1) ? voff1 : voff0);
+                for (int r = 0; r < 4; ++r) {
+                    const unsigned at = base + code_bytes(D) + (k + (r >> 1)) * 8 * RB +
+                                        ((r & 1) ? voff1 : voff0);
                     if constexpr (D == 128) {
                         const uint2 v = lds_v2(at);
-                        x[q][k][0] = v.x;
-                        x[q][k][1] = v.y;
+                        x[r][0] = v.x;
+                        x[r][1] = v.y;
                     } else {
-                        x[q][k][0] = lds_1(at);
+                        x[r][0] = lds_1(at);
                     }
                 }
 #pragma unroll
-            for (int w = 0; w < VW; ++w) {
-                unsigned T[2][4];               // byte d of the quad's four tokens
+                for (int w = 0; w < VW; ++w) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const unsigned a = __byte_perm(x[q][0][w], x[q][1][w], 0x5140);
-                    const unsigned c = __byte_perm(x[q][2][w], x[q][3][w], 0x5140);
-                    const unsigned d = __byte_perm(x[q][0][w], x[q][1][w], 0x7362);
-                    const unsigned f = __byte_perm(x[q][2][w], x[q][3][w], 0x7362);
-                    T[q][0] = __byte_perm(a, c, 0x5410);
-                    T[q][1] = __byte_perm(a, c, 0x7632);
-                    T[q][2] = __byte_perm(d, f, 0x5410);
-                    T[q][3] = __byte_perm(d, f, 0x7632);
-                }
+                    for (int hf = 0; hf < 2; ++hf) {
+                        // four dimensions of both tokens, one token per half
+                        unsigned u0 = __byte_perm(x[0][w], x[1][w], hf ? 0x7632 : 0x5410);
+                        unsigned u1 = __byte_perm(x[2][w], x[3][w], hf ? 0x7632 : 0x5410);
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const unsigned a0 = T[0][d] & 0x0F0F0F0Fu, a1 = (T[0][d] >> 4) & 0x0F0F0F0Fu;
-                    const unsigned a2 = T[1][d] & 0x0F0F0F0Fu, a3 = (T[1][d] >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        mma_e4m3(acc[4 * w + d], a0, a1, a2, a3, wb[k][0], wb[k][1]);
+                        for (int s = 0; s < 2; ++s) {
+                            mma_f16(acc[4 * w + 2 * hf + s], u0 & 0x000F000Fu, u0 & 0x00F000F0u,
+                                    u1 & 0x000F000Fu, u1 & 0x00F000F0u, wb[k], wb[k + 1]);
+                            u0 >>= 8;
+                            u1 >>= 8;
+                        }
+                    }
                 }
             }
             __syncwarp();                       // the stage has been read
             fetch(i + kStages * kWarps, st);
+            lookup(i + (kStages + 1) * kWarps);
             st = st + 1 == kStages ? 0 : st + 1;
         }
         cp_async_wait_group<0>();
@@ -525,27 +521,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         float* so = reinterpret_cast<float*>(smem);              // [warp][8][D + 4]
         float* sref = so + kWarps * 8 * (D + 4);                 // [warp][8]
         float* sl = sref + kWarps * 8;
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        om += __shfl_xor_sync(0xffffffffu, om, 1);
-        om += __shfl_xor_sync(0xffffffffu, om, 2);
-        if (t == 0) {
-            sref[warp * 8 + g] = ref;
-            sl[warp * 8 + g] = l;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+            om0 += __shfl_xor_sync(0xffffffffu, om0, o);
+            om1 += __shfl_xor_sync(0xffffffffu, om1, o);
+        }
+        if (g == 0) {
+            sref[warp * 8 + 2 * t] = ref0;
+            sref[warp * 8 + 2 * t + 1] = ref1;
+            sl[warp * 8 + 2 * t] = l0;
+            sl[warp * 8 + 2 * t + 1] = l1;
         }
         {
-            const float m0 = __shfl_sync(0xffffffffu, om, 8 * t);
-            const float m1 = __shfl_sync(0xffffffffu, om, 8 * t + 4);
+            constexpr float kE = 16777216.0f, kO = 1048576.0f;   // 2^24, 2^20
             float* r0 = so + (warp * 8 + 2 * t) * (D + 4) + 8 * VW * g;
             float* r1 = r0 + (D + 4);
 #pragma unroll
             for (int q = 0; q < 4 * VW; q += 2) {
                 *reinterpret_cast<float4*>(r0 + 2 * q) =
-                    make_float4(__fmaf_rn(acc[q][0], 512.0f, m0), __fmaf_rn(acc[q][2], 512.0f, m0),
-                                __fmaf_rn(acc[q + 1][0], 512.0f, m0), __fmaf_rn(acc[q + 1][2], 512.0f, m0));
+                    make_float4(__fmaf_rn(acc[q][0], kE, om0), __fmaf_rn(acc[q][2], kO, om0),
+                                __fmaf_rn(acc[q + 1][0], kE, om0), __fmaf_rn(acc[q + 1][2], kO, om0));
                 *reinterpret_cast<float4*>(r1 + 2 * q) =
-                    make_float4(__fmaf_rn(acc[q][1], 512.0f, m1), __fmaf_rn(acc[q][3], 512.0f, m1),
-                                __fmaf_rn(acc[q + 1][1], 512.0f, m1), __fmaf_rn(acc[q + 1][3], 512.0f, m1));
+                    make_float4(__fmaf_rn(acc[q][1], kE, om1), __fmaf_rn(acc[q][3], kO, om1),
+                                __fmaf_rn(acc[q + 1][1], kE, om1), __fmaf_rn(acc[q + 1][3], kO, om1));
             }
         }
         __syncthreads();
@@ -580,12 +580,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         x0 += j1 - j;
         j = 0;
         first = false;
-        if (x0 < x1 && ++h == p.Hkv) {
-            h = 0;
-            do {
-                tokens = tokens_of(p, ++b);
-            } while (tokens == 0);
-        }
+        if (x0 < x1) do {
+            tokens = tokens_of(p, ++b);
+        } while (tokens == 0);
     }
 }
 
@@ -595,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     attn_i4_combine_kernel(const AttnI4Params p, const int grid) {
-    constexpr int NW = kCombineThreads / 32, E = D / 32;
+    constexpr int NW = kCombineThreads / 32, EL = D / 32;
     __shared__ long s_scan[NW];
     __shared__ float s_max[NW];
     __shared__ float so[NW][D];
@@ -617,19 +614,18 @@ __global__ void __launch_bounds__(kCombineThreads)
         all += m;
         if (i < b) before += m;
     }
-    long total, total_before;
-    cta_exclusive<kCombineThreads>(all, s_scan, total);
+    long T, a0;
+    cta_exclusive<kCombineThreads>(all, s_scan, T);
     __syncthreads();
-    cta_exclusive<kCombineThreads>(before, s_scan, total_before);
-    const long T = total * p.Hkv, Ec = run_ctas(T, grid);
-    const long a0 = total_before * p.Hkv + (long)h * n, a1 = a0 + n;
-    const int c0 = (int)(((a0 + 1) * Ec - 1) / T), c1 = (int)((a1 * Ec - 1) / T);
+    cta_exclusive<kCombineThreads>(before, s_scan, a0);
+    const long E = run_count(T, grid / p.Hkv), a1 = a0 + n;
+    const int c0 = (int)(((a0 + 1) * E - 1) / T), c1 = (int)((a1 * E - 1) / T);
     if (c0 == c1) return;                       // one CTA had all of it
     const PartView part = {p.part, D, G};
     const int hd = hq - h * G;
-    // CTA c0's part is its run's first segment only if the run begins with it
-    const bool c0_first = T * c0 / Ec >= a0;
-    auto slot = [&](int c) { return 2L * c + (c == c0 && !c0_first ? 1 : 0); };
+    // run c0's part is its first segment only if the run begins with it
+    const bool c0_first = T * c0 / E >= a0;
+    auto slot = [&](int c) { return 2L * (c * p.Hkv + h) + (c == c0 && !c0_first ? 1 : 0); };
     float top = kNoRef;
     for (int c = c0 + (int)threadIdx.x; c <= c1; c += kCombineThreads)
         top = fmaxf(top, __ldcg(part.o(slot(c), hd) + D));
@@ -638,18 +634,18 @@ __global__ void __launch_bounds__(kCombineThreads)
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w]);
-    float o[E], L = 0.0f;
+    float o[EL], L = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int e = 0; e < EL; ++e) o[e] = 0.0f;
     for (int c = c0 + warp; c <= c1; c += NW) {
         const float* po = part.o(slot(c), hd);
         const float f = ex2(__ldcg(po + D) - top);
         L = __fmaf_rn(f, __ldcg(po + D + 1), L);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = __fmaf_rn(f, __ldcg(po + lane + 32 * e), o[e]);
+        for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(f, __ldcg(po + lane + 32 * e), o[e]);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
+    for (int e = 0; e < EL; ++e) so[warp][lane + 32 * e] = o[e];
     if (lane == 0) s_l[warp] = L;
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kCombineThreads) {
@@ -667,9 +663,9 @@ __global__ void __launch_bounds__(kCombineThreads)
 constexpr int kWholeCtx = 256;
 
 int grid_of(int B, int Hkv, int max_ctx) {
-    const long tiles = (long)B * Hkv * ((max_ctx + kTile - 1) / kTile);
-    const long e = (tiles + kMinTiles - 1) / kMinTiles;
-    return (int)(e < kMaxCtas ? e : kMaxCtas);
+    const long tiles = (long)B * ((max_ctx + kTile - 1) / kTile);
+    const long runs = std::min((tiles + kMinTiles - 1) / kMinTiles, (long)kMaxCtas / Hkv);
+    return (int)std::max(1L, runs) * Hkv;
 }
 
 template <typename Kern, typename... Args>
