@@ -38,6 +38,8 @@
 // contexts, and its four warps take the run's tiles in turn, each with a
 // private cp.async ring (no CTA barrier inside a run). Runs that end inside a
 // (request, KV head) leave their (ref, sum, o) to a second kernel.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -261,12 +263,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int j1 = (int)min((long)n_all, j + (x1 - x0));
         const int32_t* table = p.block_table + (size_t)b * p.max_blocks;
 
-        // The page and the place in it of token `lane` of tile i, looked up one
-        // tile before the copies that need it.
-        int blk = -1, in_page = 0;
-        auto lookup = [&](int i) {
+        // The page and the place in it of token `lane` of tile i, asked for one
+        // tile before the copies that need it (and not looked at before them).
+        auto lookup = [&](int i, int& blk, int& in_page) {
             const unsigned tok = (unsigned)i * kTile + lane;
-            blk = -1;
+            blk = INT_MIN;                       // past the context
             if (i < j1 && (int)tok < tokens) {
                 unsigned q = __umulhi(tok, page_inv), r = tok - q * p.page;
                 if (r >= (unsigned)p.page) {
@@ -275,18 +276,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 blk = __ldg(table + q);
                 in_page = (int)r;
-                if (blk < 0 || blk >= p.num_blocks) {
-                    blk = -1;
-                    set_error(p.err, 0x2u);
-                }
             }
         };
         // Copies tile i into ring stage st. A token without a row (past the
         // context, or a bad page) gets s = m = 0 and the codes of row 0, which
         // count nothing then.
-        auto fetch = [&](int i, int st) {
+        auto fetch = [&](int i, int st, int blk, int in_page) {
             if (i < j1) {                        // warp-uniform
-                const bool ok = blk >= 0;
+                const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
+                if (!ok && (i * kTile + lane < tokens)) set_error(p.err, 0x2u);
                 const unsigned slot = ok ? (unsigned)(blk * p.page + in_page) : 0u;
                 const unsigned base = ring + st * stage_bytes(D);
 #pragma unroll
@@ -302,12 +300,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             cp_async_commit();
         };
+        int blk[kStages], in_page[kStages];
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            lookup(j + warp + s * kWarps);
-            fetch(j + warp + s * kWarps, s);
-        }
-        lookup(j + warp + kStages * kWarps);
+        for (int s = 0; s < kStages; ++s) lookup(j + warp + s * kWarps, blk[s], in_page[s]);
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) fetch(j + warp + s * kWarps, s, blk[s], in_page[s]);
+        int nblk, nin = 0;
+        lookup(j + warp + kStages * kWarps, nblk, nin);
 
         // ---- the query heads ------------------------------------------------------
         // head g's dimensions of chunk t: for word w, elements (0, 4) and (2, 6)
@@ -510,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
             __syncwarp();                       // the stage has been read
-            fetch(i + kStages * kWarps, st);
-            lookup(i + (kStages + 1) * kWarps);
+            fetch(i + kStages * kWarps, st, nblk, nin);
+            lookup(i + (kStages + 1) * kWarps, nblk, nin);
             st = st + 1 == kStages ? 0 : st + 1;
         }
         cp_async_wait_group<0>();
