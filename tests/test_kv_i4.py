@@ -136,11 +136,11 @@ def test_binding_refuses_wrong_tensors():
     import torch
     t = torch.zeros(4, dtype=torch.int64)
     with pytest.raises(a8w8.A8W8Error, match="int32"):
-        a8w8._typed(t, torch.int32, "x")
+        a8w8._typed(t, torch.int32, "x", -1)
     with pytest.raises(a8w8.A8W8Error, match="codes"):
         z = torch.zeros((32, 2, 32), dtype=torch.uint8)
         m = torch.zeros((32, 2, 2), dtype=torch.bfloat16)
-        a8w8._cache_i4(z, z, m, m[:31], 2, 64, 16, "x")
+        a8w8._cache_i4(z, z, m, m[:31], 2, 64, 16, "x", -1)
 
 
 # ---------------------------------------------------------------------------

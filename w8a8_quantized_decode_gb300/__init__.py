@@ -481,30 +481,44 @@ def a8w8_prefill_layer_i8kv(weights: dict, cfg: dict, hidden, slot_mapping, bloc
         None if t is None else ctypes.byref(t), _stream(stream)))
 
 
-def _typed(t, dtype, what, shape=None):
-    """Device pointer of t after checks of its type, device and (where given) shape: the new
-    page and 4-bit entries index with these tensors, so a wrong one is refused here."""
-    if t is None or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or \
-            t.device.index != _torch().cuda.current_device() or \
-            (shape is not None and tuple(t.shape) != shape):
-        raise A8W8Error(ERR_INVALID_ARG, f"{what}: need a contiguous {dtype} tensor on the "
-                        f"current CUDA device" + (f" of shape {shape}" if shape else ""))
+def _refuse(what, t, dtype, shape):
+    raise A8W8Error(ERR_INVALID_ARG, f"{what}: need a contiguous {dtype} tensor on the current "
+                    f"CUDA device" + (f" of shape {tuple(shape)}" if shape is not None else ""))
+
+
+def _typed(t, dtype, what, dev, shape=None):
+    """Device pointer of t after checks of its type, device (the current one, by index) and,
+    where given, shape: the 4-bit and page entries index with these tensors, so a wrong one is
+    refused here."""
+    if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
+            (shape is not None and t.shape != shape):
+        _refuse(what, t, dtype, shape)
     return t.data_ptr()
 
 
-def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what):
+def _device() -> int:
+    return _torch().cuda.current_device()
+
+
+def _raw_stream(stream, dev):
+    """The cudaStream_t of `stream`, or of the current stream of device dev."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
     """Pointers and page count of a 4-bit cache: codes [slots, Hkv, D / 2] uint8 and (s, m)
     pairs [slots, Hkv, 2] bfloat16, in whole pages."""
     torch = _torch()
-    slots = k_meta.numel() // (2 * Hkv)
-    if page_size <= 0 or slots % page_size or k_meta.numel() != slots * Hkv * 2 or \
-            v_meta.numel() != slots * Hkv * 2 or k_codes.numel() != slots * Hkv * D // 2 or \
-            v_codes.numel() != slots * Hkv * D // 2:
+    pairs = k_meta.numel()
+    slots = pairs // (2 * Hkv)
+    codes = slots * Hkv * D // 2
+    if page_size <= 0 or slots % page_size or pairs != slots * Hkv * 2 or \
+            v_meta.numel() != pairs or k_codes.numel() != codes or v_codes.numel() != codes:
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: codes [slots, {Hkv}, {D // 2}] and meta "
                         f"[slots, {Hkv}, 2] of whole pages of {page_size} tokens expected")
     u8, bf = torch.uint8, torch.bfloat16
-    return (_typed(k_codes, u8, what), _typed(v_codes, u8, what), _typed(k_meta, bf, what),
-            _typed(v_meta, bf, what)), slots // page_size
+    return (_typed(k_codes, u8, what, dev), _typed(v_codes, u8, what, dev),
+            _typed(k_meta, bf, what, dev), _typed(v_meta, bf, what, dev)), slots // page_size
 
 
 def paged_kv_write_i4(k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta, page_size,
@@ -512,13 +526,13 @@ def paged_kv_write_i4(k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta, page
     """4-bit KV variant: quantise k, v [T, Hkv, D] bf16 row by row into codes
     [slots, Hkv, D / 2] uint8 and (s, m) pairs [slots, Hkv, 2] bf16."""
     torch = _torch()
-    what = "paged_kv_write_i4"
-    T, Hkv, D = k.shape
-    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what)
+    what, dev = "paged_kv_write_i4", _device()
+    T, Hkv, D = shape = k.shape
+    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     _check(lib().paged_kv_write_i4(
-        _typed(k, torch.bfloat16, what), _typed(v, torch.bfloat16, what, (T, Hkv, D)), T, Hkv, D,
-        _typed(slot_mapping, torch.int32, what, (T,)), *ptrs, num_blocks, page_size,
-        _stream(stream)))
+        _typed(k, torch.bfloat16, what, dev), _typed(v, torch.bfloat16, what, dev, shape), T, Hkv,
+        D, _typed(slot_mapping, torch.int32, what, dev, (T,)), *ptrs, num_blocks, page_size,
+        _raw_stream(stream, dev)))
 
 
 def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, out=None,
@@ -526,19 +540,19 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     """The rows at slot_mapping [T] of a 4-bit cache as k, v [T, Hkv, D] bf16 (zeros where the
     slot is negative); `out` may give the pair of tensors to fill."""
     torch = _torch()
-    what = "paged_kv_read_i4"
+    what, dev = "paged_kv_read_i4", _device()
     Hkv, D = k_codes.shape[-2], 2 * k_codes.shape[-1]
     T = slot_mapping.numel()
-    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what)
+    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
+    shape = (T, Hkv, D)
     if out is None:
-        k = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=k_codes.device)
-        v = torch.empty_like(k)
-    else:
-        k, v = out
+        both = torch.empty((2, *shape), dtype=torch.bfloat16, device=k_codes.device)
+        out = both[0], both[1]
+    k, v = out
     _check(lib().paged_kv_read_i4(
-        *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, (T,)), T, Hkv, D,
-        _typed(k, torch.bfloat16, what, (T, Hkv, D)), _typed(v, torch.bfloat16, what, (T, Hkv, D)),
-        _stream(stream)))
+        *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, (T,)), T, Hkv, D,
+        _typed(k, torch.bfloat16, what, dev, shape), _typed(v, torch.bfloat16, what, dev, shape),
+        _raw_stream(stream, dev)))
     return k, v
 
 
@@ -551,10 +565,10 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     """Decode attention over the 4-bit KV cache (codes [slots, Hkv, D / 2] uint8 and (s, m)
     pairs [slots, Hkv, 2] bf16), in float32, narrowed to bf16 once."""
     torch = _torch()
-    what = "paged_decode_attention_i4kv"
-    B, Hq, D = q.shape
+    what, dev = "paged_decode_attention_i4kv", _device()
+    B, Hq, D = shape = q.shape
     Hkv = k_codes.shape[-2]
-    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what)
+    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     max_blocks = block_table.shape[-1]
     scale = (1.0 / D ** 0.5) if softmax_scale is None else softmax_scale
     L = lib()
@@ -564,12 +578,12 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = out if out is not None else torch.empty_like(q)
     _check(L.paged_decode_attention_i4kv(
-        _typed(q, torch.bfloat16, what), *ptrs,
-        _typed(block_table, torch.int32, what, (B, max_blocks)),
-        _typed(ctx_lens, torch.int32, what, (B,)), B, Hq, Hkv, D, page_size, max_blocks,
-        num_blocks, scale, _typed(o, torch.bfloat16, what, (B, Hq, D)),
-        None if ws is None else _typed(ws, torch.uint8, what), 0 if ws is None else ws.numel(),
-        _stream(stream)))
+        _typed(q, torch.bfloat16, what, dev), *ptrs,
+        _typed(block_table, torch.int32, what, dev, (B, max_blocks)),
+        _typed(ctx_lens, torch.int32, what, dev, (B,)), B, Hq, Hkv, D, page_size, max_blocks,
+        num_blocks, scale, _typed(o, torch.bfloat16, what, dev, shape),
+        None if ws is None else _typed(ws, torch.uint8, what, dev), 0 if ws is None else ws.numel(),
+        _raw_stream(stream, dev)))
     return o
 
 
@@ -584,89 +598,88 @@ class PagePool:
         self.num_blocks, self.page_size = int(num_blocks), int(page_size)
         if self.num_blocks <= 0 or self.page_size <= 0 or not self.caches:
             raise A8W8Error(ERR_INVALID_ARG, "PagePool: caches, num_blocks and page_size expected")
-        sizes = []
+        self.index = self.caches[0].get_device()
+        ptrs, sizes = [], []
         for c in self.caches:
             size = c.numel() * c.element_size()
-            if not c.is_cuda or not c.is_contiguous() or c.device != self.caches[0].device or \
+            if self.index < 0 or c.get_device() != self.index or not c.is_contiguous() or \
                     size % self.num_blocks:
                 raise A8W8Error(ERR_INVALID_ARG, "PagePool: each cache is a contiguous CUDA tensor "
                                 f"of {num_blocks} pages, all on one device")
+            ptrs.append(c.data_ptr())
             sizes.append(size // self.num_blocks)
         self.device = self.caches[0].device
-        n = len(self.caches)
-        self._args = ((_p * n)(*[c.data_ptr() for c in self.caches]), (_sz * n)(*sizes), n)
+        n = len(ptrs)
+        self._args = ((_p * n)(*ptrs), (_sz * n)(*sizes), n)
 
-    def _here(self, what):
-        if self.device.index != _torch().cuda.current_device():
+    def _here(self, what) -> int:
+        dev = _device()
+        if dev != self.index:
             raise A8W8Error(ERR_INVALID_ARG, f"{what}: the pool is not on the current CUDA device")
-        return self._args
+        return dev
 
-    def _tables(self, what, block_table, refcount, ctx_lens=None):
+    def _tables(self, what, dev, block_table, refcount, ctx_lens=None):
         i32 = _torch().int32
         if block_table.dim() != 2:
             raise A8W8Error(ERR_INVALID_ARG, f"{what}: block_table is [B, max_blocks]")
         B, max_blocks = block_table.shape
-        return (_typed(block_table, i32, what),
-                None if ctx_lens is None else _typed(ctx_lens, i32, what, (B,)),
-                _typed(refcount, i32, what, (self.num_blocks,)), B, max_blocks)
+        return (_typed(block_table, i32, what, dev),
+                None if ctx_lens is None else _typed(ctx_lens, i32, what, dev, (B,)),
+                _typed(refcount, i32, what, dev, (self.num_blocks,)), B, max_blocks)
 
 
 def pages_workspace_bytes(num_blocks: int, B: int, n: int) -> int:
     return lib().a8w8_pages_workspace_bytes(num_blocks, B, n)
 
 
-def _pages_ws(pool, B, n, ws, what):
+def _pages_ws(pool, B, n, ws, what, dev):
     torch = _torch()
     if ws is None:
         ws = torch.empty(pages_workspace_bytes(pool.num_blocks, B, n), dtype=torch.uint8,
                          device=pool.device)
-    return _typed(ws, torch.uint8, what), ws.numel()
+    return _typed(ws, torch.uint8, what, dev), ws.numel()
 
 
 def paged_copy_pages(pool, src, dst, stream=None):
     """Copy page src[i] to page dst[i] (int32 [n] on the device) in every cache of the pool."""
     what = "paged_copy_pages"
-    i32 = _torch().int32
-    n = src.numel()
-    _check(lib().paged_copy_pages(*pool._here(what), pool.num_blocks, _typed(src, i32, what, (n,)),
-                                  _typed(dst, i32, what, (n,)), n, _stream(stream)))
+    i32, dev, n = _torch().int32, pool._here(what), src.numel()
+    _check(lib().paged_copy_pages(*pool._args, pool.num_blocks, _typed(src, i32, what, dev, (n,)),
+                                  _typed(dst, i32, what, dev, (n,)), n, _raw_stream(stream, dev)))
 
 
 def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None, stream=None):
     """Fork row parents[i] into the free row children[i]: full pages shared, the page in
     progress copied. block_table, ctx_lens and refcount are updated in place."""
     what = "paged_fork"
-    i32 = _torch().int32
-    n = parents.numel()
-    bt, cl, rc, B, max_blocks = pool._tables(what, block_table, refcount, ctx_lens)
-    _check(lib().paged_fork(*pool._here(what), pool.num_blocks, pool.page_size, bt, cl, rc, B,
-                            max_blocks, _typed(parents, i32, what, (n,)),
-                            _typed(children, i32, what, (n,)), n,
-                            *_pages_ws(pool, B, n, ws, what), _stream(stream)))
+    i32, dev, n = _torch().int32, pool._here(what), parents.numel()
+    bt, cl, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount, ctx_lens)
+    _check(lib().paged_fork(*pool._args, pool.num_blocks, pool.page_size, bt, cl, rc, B,
+                            max_blocks, _typed(parents, i32, what, dev, (n,)),
+                            _typed(children, i32, what, dev, (n,)), n,
+                            *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
 
 
 def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=None):
     """Give row rows[i] pages for tokens[i] tokens. block_table and refcount are updated in
     place."""
     what = "paged_reserve"
-    i32 = _torch().int32
-    n = rows.numel()
-    bt, _, rc, B, max_blocks = pool._tables(what, block_table, refcount)
-    pool._here(what)
+    i32, dev, n = _torch().int32, pool._here(what), rows.numel()
+    bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     _check(lib().paged_reserve(bt, rc, B, max_blocks, pool.num_blocks, pool.page_size,
-                               _typed(rows, i32, what, (n,)), _typed(tokens, i32, what, (n,)), n,
-                               *_pages_ws(pool, B, n, ws, what), _stream(stream)))
+                               _typed(rows, i32, what, dev, (n,)),
+                               _typed(tokens, i32, what, dev, (n,)), n,
+                               *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
 
 
 def paged_free(pool, block_table, ctx_lens, refcount, rows, stream=None):
     """Free the listed rows: their pages lose a reference, their table rows become -1, their
     contexts 0."""
     what = "paged_free"
-    n = rows.numel()
-    bt, cl, rc, B, max_blocks = pool._tables(what, block_table, refcount, ctx_lens)
-    pool._here(what)
+    i32, dev, n = _torch().int32, pool._here(what), rows.numel()
+    bt, cl, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount, ctx_lens)
     _check(lib().paged_free(bt, cl, rc, B, max_blocks, pool.num_blocks,
-                            _typed(rows, _torch().int32, what, (n,)), n, _stream(stream)))
+                            _typed(rows, i32, what, dev, (n,)), n, _raw_stream(stream, dev)))
 
 
 def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=None):
@@ -674,12 +687,13 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
     (int32 [1] on the device): pages from there on are free."""
     torch = _torch()
     what = "paged_compact"
-    bt, _, rc, B, max_blocks = pool._tables(what, block_table, refcount)
+    dev = pool._here(what)
+    bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     if num_live is None:
         num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
-    _check(lib().paged_compact(*pool._here(what), pool.num_blocks, bt, rc, B, max_blocks,
-                               _typed(num_live, torch.int32, what, (1,)),
-                               *_pages_ws(pool, B, 0, ws, what), _stream(stream)))
+    _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
+                               _typed(num_live, torch.int32, what, dev, (1,)),
+                               *_pages_ws(pool, B, 0, ws, what, dev), _raw_stream(stream, dev)))
     return num_live
 
 

@@ -50,12 +50,12 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;            // tokens a warp takes at a time
-constexpr int kStages = 3;           // ring depth per warp
+constexpr int kStages = 2;           // ring depth per warp
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = 152 * kCtasPerSm;
 constexpr int kMinTiles = 4;         // tiles per CTA at least: one per warp
 constexpr int kCombineThreads = 128;
-constexpr float kNoRef = -1e30f;     // ref of a head that has seen no token
+constexpr float kNoRef = -1e30f;     // ref of a warp that has seen no token
 
 constexpr int code_bytes(int D) { return kTile * D / 2; }
 constexpr int stage_bytes(int D) { return 2 * code_bytes(D) + kTile * 8; }
@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
         // of heads 2 t, 2 t + 1, over the lane's tokens
-        float ref0 = kNoRef, ref1 = kNoRef, l0 = 0.0f, l1 = 0.0f, om0 = 0.0f, om1 = 0.0f;
+        float ref0 = 0.0f, ref1 = 0.0f, l0 = 0.0f, l1 = 0.0f, om0 = 0.0f, om1 = 0.0f;
+        bool fresh = true;                      // no tile yet
 
         int st = 0;
         for (int i = j + warp; i < j1; i += kWarps) {
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const unsigned base = ring + st * stage_bytes(D);
 
             // ---- scores: token g of each 8, heads 2 t and 2 t + 1 --------------------
-            float y0[4], y1[4], sv[4], mv[4];
+            float y0[4], y1[4], sv[4], mv[4];   // y - ref
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
                 unsigned ka[2][KW];
@@ -407,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float ks = bf_lo(mt.x), km = bf_hi(mt.x);
                     sv[k + r] = bf_lo(mt.y);
                     mv[k + r] = bf_hi(mt.y);
-                    y0[k + r] = __fmaf_rn(c[2 * r] * ch0, ks, qs0 * km);
-                    y1[k + r] = __fmaf_rn(c[2 * r + 1] * ch1, ks, qs1 * km);
+                    y0[k + r] = __fmaf_rn(c[2 * r] * ks, ch0, __fmaf_rn(qs0, km, -ref0));
+                    y1[k + r] = __fmaf_rn(c[2 * r + 1] * ks, ch1, __fmaf_rn(qs1, km, -ref1));
                 }
             }
             if ((i + 1) * kTile > tokens) {     // the request's last tile
@@ -425,13 +426,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             float big = 0.0f, bigp = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                p0[k] = ex2(y0[k] - ref0);
-                p1[k] = ex2(y1[k] - ref1);
+                p0[k] = ex2(y0[k]);
+                p1[k] = ex2(y1[k]);
                 const float pm = fmaxf(p0[k], p1[k]);
-                big = fmaxf(big, fabsf(pm * sv[k]));
+                big = fmaxf(big, pm * fabsf(sv[k]));
                 bigp = fmaxf(bigp, pm);
             }
-            if (__any_sync(0xffffffffu, big > 32768.0f || bigp > 1.2e27f)) {
+            if (fresh || __any_sync(0xffffffffu, big > 32768.0f || bigp > 1.2e27f)) {
                 float z0 = kNoRef, z1 = kNoRef;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -444,10 +445,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, o));
                     z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, o));
                 }
-                const float n0 = fmaxf(ref0, z0 - 10.0f), n1 = fmaxf(ref1, z1 - 10.0f);
-                const float f0 = ex2(ref0 - n0), f1 = ex2(ref1 - n1);
-                ref0 = n0;
-                ref1 = n1;
+                // how far ref rises; on the first tile it stands at 0 with nothing
+                // summed, and takes the tile's level whatever its sign
+                const float low = fresh ? kNoRef : 0.0f;
+                float d0 = fmaxf(low, z0 - 10.0f), d1 = fmaxf(low, z1 - 10.0f);
+                if (d0 <= kNoRef) d0 = 0.0f;
+                if (d1 <= kNoRef) d1 = 0.0f;
+                const float f0 = fresh ? 0.0f : ex2(-d0), f1 = fresh ? 0.0f : ex2(-d1);
+                ref0 += d0;
+                ref1 += d1;
+                fresh = false;
                 l0 *= f0;
                 l1 *= f1;
                 om0 *= f0;
@@ -461,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    p0[k] = ex2(y0[k] - ref0);
-                    p1[k] = ex2(y1[k] - ref1);
+                    p0[k] = ex2(y0[k] - d0);
+                    p1[k] = ex2(y1[k] - d1);
                 }
             }
             unsigned wb[4];                     // head g, tokens 2 t, 2 t + 1 of each 8
@@ -528,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             om1 += __shfl_xor_sync(0xffffffffu, om1, o);
         }
         if (g == 0) {
-            sref[warp * 8 + 2 * t] = ref0;
-            sref[warp * 8 + 2 * t + 1] = ref1;
+            sref[warp * 8 + 2 * t] = fresh ? kNoRef : ref0;
+            sref[warp * 8 + 2 * t + 1] = fresh ? kNoRef : ref1;
             sl[warp * 8 + 2 * t] = l0;
             sl[warp * 8 + 2 * t + 1] = l1;
         }
@@ -596,17 +603,13 @@ __global__ void __launch_bounds__(kCombineThreads)
     __shared__ float s_max[NW];
     __shared__ float so[NW][D];
     __shared__ float s_l[NW];
-    pdl_wait();
-    pdl_trigger();
+    // The contexts are an input of the first kernel too, which has passed its
+    // own wait by now: they may be read before this kernel's.
     const int hq = blockIdx.x, b = blockIdx.y;
     const int G = p.Hq / p.Hkv, h = hq / G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bf16* out = p.out + ((size_t)b * p.Hq + hq) * D;
     const int n = tiles_of(tokens_of(p, b));
-    if (n == 0) {
-        for (int d = threadIdx.x; d < D; d += kCombineThreads) out[d] = __float2bfloat16_rn(0.0f);
-        return;
-    }
     long all = 0, before = 0;
     for (int i = threadIdx.x; i < p.B; i += kCombineThreads) {
         const int m = tiles_of(tokens_of(p, i));
@@ -617,6 +620,12 @@ __global__ void __launch_bounds__(kCombineThreads)
     cta_exclusive<kCombineThreads>(all, s_scan, T);
     __syncthreads();
     cta_exclusive<kCombineThreads>(before, s_scan, a0);
+    pdl_wait();
+    pdl_trigger();
+    if (n == 0) {
+        for (int d = threadIdx.x; d < D; d += kCombineThreads) out[d] = __float2bfloat16_rn(0.0f);
+        return;
+    }
     const long E = run_count(T, grid / p.Hkv), a1 = a0 + n;
     const int c0 = (int)(((a0 + 1) * E - 1) / T), c1 = (int)((a1 * E - 1) / T);
     if (c0 == c1) return;                       // one CTA had all of it
