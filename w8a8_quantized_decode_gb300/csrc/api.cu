@@ -1026,9 +1026,11 @@ a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_cod
     if (Hq % Hkv || Hq / Hkv > 8) return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "Hq/Hkv must be an integer <= 8");
     if ((long long)max_blocks * page_size > (1 << 24))
         return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "context longer than 2^24 tokens");
-    if (B > 65535 || (long long)B * Hq > (1 << 24) || (long long)num_blocks * page_size > INT32_MAX)
+    if (B > 65535 || (long long)B * Hq > (1 << 24) || (long long)num_blocks * page_size > INT32_MAX ||
+        (long long)B * max_blocks * page_size > (1LL << 35))
         return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
-                    "more than 65535 requests, 2^24 (request, head) pairs or 2^31 - 1 slots");
+                    "more than 65535 requests, 2^24 (request, head) pairs, 2^31 - 1 slots or 2^35 "
+                    "tokens");
     a8w8_status s = check_ptrs({q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, out},
                                "paged_decode_attention_i4kv");
     if (s != A8W8_OK) return s;

@@ -59,16 +59,16 @@ constexpr float kNoRef = -1e30f;     // ref of a warp that has seen no token
 
 constexpr int code_bytes(int D) { return kTile * D / 2; }
 constexpr int stage_bytes(int D) { return 2 * code_bytes(D) + kTile * 8; }
-constexpr int merge_bytes(int D) { return kWarps * 8 * (D + 4) * 4 + 2 * kWarps * 8 * 4; }
+constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
+// Beside the rings, the warps' (o, ref, sum) of the segment that just ended:
+// the next segment's first copies run while they are joined.
 constexpr int smem_bytes(int D) {
-    const int ring = kWarps * kStages * stage_bytes(D);
-    return ring > merge_bytes(D) ? ring : merge_bytes(D);
+    return ring_bytes(D) + kWarps * 8 * (D + 4) * 4 + 2 * kWarps * 8 * 4;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], unsigned a0, unsigned a1, unsigned a2,
                                         unsigned a3, unsigned b0, unsigned b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -81,7 +81,7 @@ __device__ __forceinline__ unsigned h2_of(float a, float b) {   // a in the low 
 // 8 x 8 halves, row lane / 4, columns 2 (lane % 4) and the next: transposed.
 __device__ __forceinline__ unsigned transpose8(unsigned v) {
     unsigned r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -95,16 +95,6 @@ __device__ __forceinline__ void cp16(unsigned s, const void* g) {
 __device__ __forceinline__ void cp4z(unsigned s, const void* g, unsigned n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(g), "r"(n) : "memory");
 }
-__device__ __forceinline__ uint2 lds_v2(unsigned s) {
-    uint2 r;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(s));
-    return r;
-}
-__device__ __forceinline__ unsigned lds_1(unsigned s) {
-    unsigned r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(s));
-    return r;
-}
 __device__ __forceinline__ float bf_lo(unsigned w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(unsigned w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -115,44 +105,60 @@ __device__ __forceinline__ int tokens_of(const AttnI4Params& p, int b) {
 }
 __device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kTile - 1) / kTile; }
 
-// Exclusive sum of v over the CTA's NT threads (total in `total`).
-template <int NT>
-__device__ __forceinline__ long cta_exclusive(long v, long* s, long& total) {
+// Exclusive sum of v over the CTA's threads (total in `total`); `s` is one
+// unsigned per warp.
+__device__ __forceinline__ unsigned cta_exclusive(unsigned v, unsigned* s, unsigned& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long x = v;
+    unsigned x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long y = __shfl_up_sync(0xffffffffu, x, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) s[warp] = x;
     __syncthreads();
-    long before = 0;
+    unsigned before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s[w];
         total += s[w];
     }
     return before + x - v;
 }
 
-// The runs: run r of E takes tiles [r T / E, (r + 1) T / E) of T = sum_b
-// tiles(b), request after request; the CTAs of a run's KV heads stand side by
-// side (CTA r Hkv + h), so that the sectors that hold several heads' (s, m)
-// words and the lines that hold their codes are read together.
-__device__ __forceinline__ long run_count(long T, int runs) {
-    const long e = (T + kMinTiles - 1) / kMinTiles;
-    return e < runs ? e : runs;
-}
+// The runs: run r of E begins at tile floor(r T / E) of T = sum_b tiles(b),
+// request after request; the CTAs of a run's KV heads stand side by side (CTA
+// r Hkv + h), so that the sectors that hold several heads' (s, m) words and
+// the lines that hold their codes are read together.
+struct Runs {
+    unsigned T, E, q, rem;   // T = q E + rem
+    __device__ __forceinline__ Runs(unsigned tiles, unsigned runs) {
+        T = tiles;
+        E = min((tiles + kMinTiles - 1) / kMinTiles, runs);
+        q = E ? T / E : 0;
+        rem = T - q * E;
+    }
+    __device__ __forceinline__ unsigned start(unsigned r) const { return q * r + rem * r / E; }
+    __device__ __forceinline__ unsigned owner(unsigned tile) const {
+        return (unsigned)((((unsigned long long)tile + 1) * E - 1) / T);
+    }
+};
 
+// The workspace: what the second kernel has to join for each request, then
+// two parts per CTA of the first (a run ends inside at most two requests'
+// tiles), each G heads of o [D], ref and sum.
+//   plan.x = 2 (first run) + (0 if that run begins inside the request),
+//   plan.y = last run; the same run twice: nothing to join; plan.x = -1: no
+//   tokens.
 struct PartView {
     float* base;
     int D, G;
-    __device__ float* o(long slot, int head) const {
-        return base + (slot * G + head) * (long)(D + 4);
+    __device__ __forceinline__ float* o(unsigned slot, int head) const {
+        return base + ((size_t)slot * G + head) * (D + 4);
     }
 };
+__host__ __device__ inline size_t plan_bytes(int B) { return ((size_t)B * 8 + 255) / 256 * 256; }
 
 template <int D>
 struct Frag {
@@ -168,21 +174,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     constexpr int KW = Frag<D>::KW, VW = Frag<D>::VW;
     constexpr int RB = D / 2;                   // bytes of a row's codes
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ long s_scan[kWarps];
-    __shared__ long s_first;
+    __shared__ unsigned s_scan[kWarps];
+    __shared__ unsigned s_first;
     __shared__ int s_b;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv;
     const unsigned sbase = (unsigned)__cvta_generic_to_shared(smem);
     const unsigned ring = sbase + warp * kStages * stage_bytes(D);
+    const unsigned char* rings = smem + warp * kStages * stage_bytes(D);
 
     pdl_wait();
     pdl_trigger();
 
     // ---- where the run begins -------------------------------------------------
-    long x0, x1;                   // the run's tiles
-    int b, h, j, tokens;           // its first tile: request, KV head, tile of the request
+    int b, h, j, tokens;           // the run's first tile: request, KV head, tile of the request
+    int left;                      // tiles of the run from there on
+    int2* plan = reinterpret_cast<int2*>(p.part);
     if (whole) {
         b = blockIdx.x / p.Hkv;
         h = blockIdx.x - b * p.Hkv;
@@ -197,33 +205,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int i = threadIdx.x; i < G * D; i += kThreads) out[i] = __float2bfloat16_rn(0.0f);
             return;
         }
-        x0 = 0;
-        x1 = tiles_of(tokens);
+        left = tiles_of(tokens);
     } else {
         const int per = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-        long mine = 0;
+        unsigned mine = 0;
         for (int i = b0; i < b1; ++i) {
-            if (blockIdx.x == 0) {
-                const int c = p.ctx_lens[i];
-                if (c < 0 || c > p.max_blocks * p.page) set_error(p.err, 0x4u);
+            const int n = tokens_of(p, i);
+            if (blockIdx.x == 0 && n == 0) {
+                plan[i] = make_int2(-1, -1);
+                if (p.ctx_lens[i] != 0) set_error(p.err, 0x4u);
             }
-            mine += tiles_of(tokens_of(p, i));
+            mine += tiles_of(n);
         }
-        long T;
-        const long before = cta_exclusive<kThreads>(mine, s_scan, T);
-        const long E = run_count(T, gridDim.x / p.Hkv);
-        const long r = blockIdx.x / p.Hkv;
-        h = blockIdx.x - (int)r * p.Hkv;
-        if (r >= E) return;
-        x0 = T * r / E;
-        x1 = T * (r + 1) / E;
-        if (mine > 0 && x0 >= before && x0 < before + mine) {
-            long at = before;
+        unsigned T;
+        const unsigned before = cta_exclusive(mine, s_scan, T);
+        const Runs runs(T, gridDim.x / p.Hkv);
+        const unsigned r = blockIdx.x / p.Hkv;
+        h = blockIdx.x - r * p.Hkv;
+        if (r >= runs.E) return;
+        const unsigned x0 = runs.start(r), x1 = runs.start(r + 1);
+        if (mine > 0 && x0 >= before && x0 - before < mine) {
+            unsigned at = before;
             int i = b0;
             for (;; ++i) {
-                const int n = tiles_of(tokens_of(p, i));
-                if (x0 < at + n) break;
+                const unsigned n = tiles_of(tokens_of(p, i));
+                if (x0 - at < n) break;
                 at += n;
             }
             s_b = i;
@@ -232,7 +239,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         __syncthreads();
         b = s_b;
         tokens = tokens_of(p, b);
-        j = (int)(x0 - s_first);
+        j = x0 - s_first;
+        left = x1 - x0;
+        // the requests that begin in this run: which runs hold their parts
+        if (h == 0 && threadIdx.x == 0) {
+            int rest = left;
+            for (int i = b, at = j; rest > 0; ++i, at = 0) {
+                const int n = tiles_of(tokens_of(p, i));
+                if (n == 0) continue;
+                if (at == 0) {
+                    const unsigned last = x1 - rest + n - 1;   // its last tile
+                    plan[i] = make_int2(2 * r + (i == b ? 0 : 1),
+                                        n <= rest ? r : runs.owner(last));
+                }
+                rest -= n - at;
+            }
+        }
     }
 
     // ---- lane constants -----------------------------------------------------
@@ -257,69 +279,75 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const unsigned char* km = reinterpret_cast<const unsigned char*>(p.c.k_meta) + h * 4;
     const unsigned char* vm = reinterpret_cast<const unsigned char*>(p.c.v_meta) + h * 4;
 
-    bool first = true;                          // the run's first segment
-    while (x0 < x1) {
-        const int n_all = tiles_of(tokens);
-        const int j1 = (int)min((long)n_all, j + (x1 - x0));
-        const int32_t* table = p.block_table + (size_t)b * p.max_blocks;
-
-        // The page and the place in it of token `lane` of tile i, asked for one
-        // tile before the copies that need it (and not looked at before them).
-        auto lookup = [&](int i, int& blk, int& in_page) {
-            const unsigned tok = (unsigned)i * kTile + lane;
-            blk = INT_MIN;                       // past the context
-            if (i < j1 && (int)tok < tokens) {
-                unsigned q = __umulhi(tok, page_inv), r = tok - q * p.page;
-                if (r >= (unsigned)p.page) {
-                    ++q;
-                    r -= p.page;
-                }
-                blk = __ldg(table + q);
-                in_page = (int)r;
+    // ---- a segment: the run's tiles of one request ---------------------------
+    int n_all, j1;                              // the request's tiles; the segment's end
+    const int32_t* table;
+    int blk[kStages], in_page[kStages], nblk, nin = 0;
+    // The page and the place in it of token `lane` of tile i, asked for one
+    // tile before the copies that need it (and not looked at before them).
+    auto lookup = [&](int i, int& blk, int& in_page) {
+        const unsigned tok = (unsigned)i * kTile + lane;
+        blk = INT_MIN;                       // past the context
+        if (i < j1 && (int)tok < tokens) {
+            unsigned q = __umulhi(tok, page_inv), r = tok - q * p.page;
+            if (r >= (unsigned)p.page) {
+                ++q;
+                r -= p.page;
             }
-        };
-        // Copies tile i into ring stage st. A token without a row (past the
-        // context, or a bad page) gets s = m = 0 and the codes of row 0, which
-        // count nothing then.
-        auto fetch = [&](int i, int st, int blk, int in_page) {
-            if (i < j1) {                        // warp-uniform
-                const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
-                if (!ok && (i * kTile + lane < tokens)) set_error(p.err, 0x2u);
-                const unsigned slot = ok ? (unsigned)(blk * p.page + in_page) : 0u;
-                const unsigned base = ring + st * stage_bytes(D);
+            blk = __ldg(table + q);
+            in_page = (int)r;
+        }
+    };
+    // Copies tile i into ring stage st. A token without a row (past the
+    // context, or a bad page) gets s = m = 0 and the codes of row 0, which
+    // count nothing then.
+    auto fetch = [&](int i, int st, int blk, int in_page) {
+        if (i < j1) {                        // warp-uniform
+            const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
+            if (!ok && (i * kTile + lane < tokens)) set_error(p.err, 0x2u);
+            const unsigned slot = ok ? (unsigned)(blk * p.page + in_page) : 0u;
+            const unsigned base = ring + st * stage_bytes(D);
 #pragma unroll
-                for (int k = 0; k < kTile / RPI; ++k) {
-                    const unsigned sl = __shfl_sync(0xffffffffu, slot, k * RPI + crow);
-                    const unsigned d = base + k * RPI * RB + coff;
-                    cp16(d, kc + (size_t)sl * rstride);
-                    cp16(d + code_bytes(D), vc + (size_t)sl * rstride);
-                }
-                const unsigned d = base + 2 * code_bytes(D) + mcol * 8;
-                cp4z(d, km + (size_t)slot * mstride, ok ? 4u : 0u);
-                cp4z(d + 4, vm + (size_t)slot * mstride, ok ? 4u : 0u);
+            for (int k = 0; k < kTile / RPI; ++k) {
+                const unsigned sl = __shfl_sync(0xffffffffu, slot, k * RPI + crow);
+                const unsigned d = base + k * RPI * RB + coff;
+                cp16(d, kc + (size_t)sl * rstride);
+                cp16(d + code_bytes(D), vc + (size_t)sl * rstride);
             }
-            cp_async_commit();
-        };
-        int blk[kStages], in_page[kStages];
+            const unsigned d = base + 2 * code_bytes(D) + mcol * 8;
+            cp4z(d, km + (size_t)slot * mstride, ok ? 4u : 0u);
+            cp4z(d + 4, vm + (size_t)slot * mstride, ok ? 4u : 0u);
+        }
+        cp_async_commit();
+    };
+    auto open = [&] {
+        n_all = tiles_of(tokens);
+        j1 = min(n_all, j + left);
+        table = p.block_table + (size_t)b * p.max_blocks;
 #pragma unroll
         for (int s = 0; s < kStages; ++s) lookup(j + warp + s * kWarps, blk[s], in_page[s]);
+    };
+    int4 raw[KW];                           // the query head's values, as loaded
+    auto copy_first = [&] {
 #pragma unroll
         for (int s = 0; s < kStages; ++s) fetch(j + warp + s * kWarps, s, blk[s], in_page[s]);
-        int nblk, nin = 0;
         lookup(j + warp + kStages * kWarps, nblk, nin);
-
+        const bf16* q = p.q + ((size_t)b * p.Hq + (size_t)h * G + (g < G ? g : 0)) * D + t * (D / 4);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) raw[w] = g < G ? ld_cg_v4(q + 8 * w) : make_int4(0, 0, 0, 0);
+    };
+    open();
+    copy_first();
+    for (bool first = true;; first = false) {
         // ---- the query heads ------------------------------------------------------
         // head g's dimensions of chunk t: for word w, elements (0, 4) and (2, 6)
         // times 16 meet the low nibbles of the masks, (1, 5) and (3, 7) the high
         unsigned qb[KW][4];
         float ch0, ch1, qs0, qs1;               // score factors of heads 2 t, 2 t + 1
         {
-            const bf16* q = p.q + ((size_t)b * p.Hq + (size_t)h * G + (g < G ? g : 0)) * D + t * (D / 4);
             float sum = 0.0f, top = 0.0f;
-            int4 raw[KW];
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
-                raw[w] = g < G ? ld_cg_v4(q + 8 * w) : make_int4(0, 0, 0, 0);
                 float f[8];
                 unpack8(raw[w], f);
 #pragma unroll
@@ -372,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int i = j + warp; i < j1; i += kWarps) {
             cp_async_wait_group<kStages - 1>();
             __syncwarp();
-            const unsigned base = ring + st * stage_bytes(D);
+            const unsigned char* base = rings + st * stage_bytes(D);
 
             // ---- scores: token g of each 8, heads 2 t and 2 t + 1 --------------------
             float y0[4], y1[4], sv[4], mv[4];   // y - ref
@@ -382,13 +410,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     if constexpr (D == 128) {
-                        const int4 v = lds_v4(base + 8 * (k + r) * RB + koff);
+                        const int4 v = *reinterpret_cast<const int4*>(base + 8 * (k + r) * RB + koff);
                         ka[r][0] = v.x;
                         ka[r][1] = v.y;
                         ka[r][2] = v.z;
                         ka[r][3] = v.w;
                     } else {
-                        const uint2 v = lds_v2(base + 8 * (k + r) * RB + koff);
+                        const uint2 v = *reinterpret_cast<const uint2*>(base + 8 * (k + r) * RB + koff);
                         ka[r][0] = v.x;
                         ka[r][1] = v.y;
                     }
@@ -404,7 +432,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint2 mt = lds_v2(base + 2 * code_bytes(D) + (8 * (k + r) + g) * 8);
+                    const uint2 mt = *reinterpret_cast<const uint2*>(base + 2 * code_bytes(D) +
+                                                                     (8 * (k + r) + g) * 8);
                     const float ks = bf_lo(mt.x), km = bf_hi(mt.x);
                     sv[k + r] = bf_lo(mt.y);
                     mv[k + r] = bf_hi(mt.y);
@@ -488,14 +517,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 unsigned x[4][VW];              // tokens 2 t, 2 t + 1 of two groups of 8
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const unsigned at = base + code_bytes(D) + (k + (r >> 1)) * 8 * RB +
-                                        ((r & 1) ? voff1 : voff0);
+                    const unsigned char* at = base + code_bytes(D) + (k + (r >> 1)) * 8 * RB +
+                                              ((r & 1) ? voff1 : voff0);
                     if constexpr (D == 128) {
-                        const uint2 v = lds_v2(at);
+                        const uint2 v = *reinterpret_cast<const uint2*>(at);
                         x[r][0] = v.x;
                         x[r][1] = v.y;
                     } else {
-                        x[r][0] = lds_1(at);
+                        x[r][0] = *reinterpret_cast<const unsigned*>(at);
                     }
                 }
 #pragma unroll
@@ -520,11 +549,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             lookup(i + (kStages + 1) * kWarps, nblk, nin);
             st = st + 1 == kStages ? 0 : st + 1;
         }
-        cp_async_wait_group<0>();
-        __syncthreads();                        // the rings become the merge buffer
-
-        // ---- the four warps' parts ---------------------------------------------
-        float* so = reinterpret_cast<float*>(smem);              // [warp][8][D + 4]
+        // ---- the next segment's first copies, then this one's parts ---------------
+        const int mb = b;
+        const bool all = j == 0 && j1 == n_all;
+        left -= j1 - j;
+        j = 0;
+        const bool more = left > 0;
+        if (more) {
+            do {
+                tokens = tokens_of(p, ++b);
+            } while (tokens == 0);
+            open();
+        }
+        if (!first) __syncthreads();            // the last segment's parts have been read
+        float* so = reinterpret_cast<float*>(smem + ring_bytes(D));   // [warp][8][D + 4]
         float* sref = so + kWarps * 8 * (D + 4);                 // [warp][8]
         float* sl = sref + kWarps * 8;
 #pragma unroll
@@ -554,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                                 __fmaf_rn(acc[q + 1][1], kE, om1), __fmaf_rn(acc[q + 1][3], kO, om1));
             }
         }
+        if (more) copy_first();
         __syncthreads();
-        const bool all = j == 0 && j1 == n_all;
-        const PartView part = {p.part, D, G};
+        const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
         for (int i = threadIdx.x; i < G * D; i += kThreads) {
             const int hd = i / D, d = i - hd * D;
             float top = sref[hd];
@@ -570,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 L = __fmaf_rn(f, sl[w * 8 + hd], L);
             }
             if (all) {
-                p.out[((size_t)b * p.Hq + (size_t)h * G + hd) * D + d] = f2bf(__fdividef(o, L));
+                p.out[((size_t)mb * p.Hq + (size_t)h * G + hd) * D + d] = f2bf(__fdividef(o, L));
             } else {
-                float* po = part.o(2L * blockIdx.x + (first ? 0 : 1), hd);
+                float* po = part.o(2 * blockIdx.x + (first ? 0 : 1), hd);
                 po[d] = o;
                 if (d == 0) {
                     po[D] = top;
@@ -580,15 +618,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
         }
-        __syncthreads();                        // the buffer becomes the rings again
-
-        // ---- the next segment -----------------------------------------------------
-        x0 += j1 - j;
-        j = 0;
-        first = false;
-        if (x0 < x1) do {
-            tokens = tokens_of(p, ++b);
-        } while (tokens == 0);
+        if (!more) break;
     }
 }
 
@@ -596,44 +626,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 // writes the zeros of requests without tokens. One CTA per query head and
 // request; its warps take the parts in turn.
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads)
-    attn_i4_combine_kernel(const AttnI4Params p, const int grid) {
+__global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const AttnI4Params p) {
     constexpr int NW = kCombineThreads / 32, EL = D / 32;
-    __shared__ long s_scan[NW];
     __shared__ float s_max[NW];
     __shared__ float so[NW][D];
     __shared__ float s_l[NW];
-    // The contexts are an input of the first kernel too, which has passed its
-    // own wait by now: they may be read before this kernel's.
     const int hq = blockIdx.x, b = blockIdx.y;
     const int G = p.Hq / p.Hkv, h = hq / G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bf16* out = p.out + ((size_t)b * p.Hq + hq) * D;
-    const int n = tiles_of(tokens_of(p, b));
-    long all = 0, before = 0;
-    for (int i = threadIdx.x; i < p.B; i += kCombineThreads) {
-        const int m = tiles_of(tokens_of(p, i));
-        all += m;
-        if (i < b) before += m;
-    }
-    long T, a0;
-    cta_exclusive<kCombineThreads>(all, s_scan, T);
-    __syncthreads();
-    cta_exclusive<kCombineThreads>(before, s_scan, a0);
     pdl_wait();
     pdl_trigger();
-    if (n == 0) {
+    const int2 plan = __ldcg(reinterpret_cast<const int2*>(p.part) + b);
+    if (plan.x < 0) {
         for (int d = threadIdx.x; d < D; d += kCombineThreads) out[d] = __float2bfloat16_rn(0.0f);
         return;
     }
-    const long E = run_count(T, grid / p.Hkv), a1 = a0 + n;
-    const int c0 = (int)(((a0 + 1) * E - 1) / T), c1 = (int)((a1 * E - 1) / T);
+    const int c0 = plan.x >> 1, c1 = plan.y;
     if (c0 == c1) return;                       // one CTA had all of it
-    const PartView part = {p.part, D, G};
+    const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
     const int hd = hq - h * G;
-    // run c0's part is its first segment only if the run begins with it
-    const bool c0_first = T * c0 / E >= a0;
-    auto slot = [&](int c) { return 2L * (c * p.Hkv + h) + (c == c0 && !c0_first ? 1 : 0); };
+    auto slot = [&](int c) { return 2u * (c * p.Hkv + h) + (c == c0 ? plan.x & 1 : 0); };
     float top = kNoRef;
     for (int c = c0 + (int)threadIdx.x; c <= c1; c += kCombineThreads)
         top = fmaxf(top, __ldcg(part.o(slot(c), hd) + D));
@@ -706,14 +719,14 @@ cudaError_t launch_attention_i4_d(const AttnI4Params& p, const Launch& L) {
     const int grid = grid_of(p.B, p.Hkv, max_ctx);
     e = launch_i4(attn_i4_kernel<D>, dim3(grid), kThreads, smem, L, p, inv, false);
     if (e != cudaSuccess) return e;
-    return launch_i4(attn_i4_combine_kernel<D>, dim3(p.Hq, p.B), kCombineThreads, 0, L, p, grid);
+    return launch_i4(attn_i4_combine_kernel<D>, dim3(p.Hq, p.B), kCombineThreads, 0, L, p);
 }
 
 }  // namespace
 
 size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx) {
     if (max_ctx <= kWholeCtx) return 0;
-    return (size_t)grid_of(B, Hkv, max_ctx) * 2 * (Hq / Hkv) * (D + 4) * 4;
+    return plan_bytes(B) + (size_t)grid_of(B, Hkv, max_ctx) * 2 * (Hq / Hkv) * (D + 4) * 4;
 }
 
 cudaError_t launch_attention_i4(const AttnI4Params& p, const Launch& L) {
