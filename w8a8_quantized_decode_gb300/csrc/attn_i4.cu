@@ -51,9 +51,9 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;            // tokens a warp takes at a time
 constexpr int kStages = 2;           // ring depth per warp
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 152 * kCtasPerSm;
-constexpr int kMinTiles = 4;         // tiles per CTA at least: one per warp
+constexpr int kMinTiles = 4;         // tiles per run at least
 constexpr int kCombineThreads = 128;
 constexpr float kNoRef = -1e30f;     // ref of a warp that has seen no token
 
@@ -62,8 +62,8 @@ constexpr int stage_bytes(int D) { return 2 * code_bytes(D) + kTile * 8; }
 constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
 // Beside the rings, the warps' (o, ref, sum) of the segment that just ended:
 // the next segment's first copies run while they are joined.
-constexpr int smem_bytes(int D) {
-    return ring_bytes(D) + kWarps * 8 * (D + 4) * 4 + 2 * kWarps * 8 * 4;
+constexpr int smem_bytes(int D, int HW) {
+    return ring_bytes(D) + (HW == kWarps ? 0 : kWarps * 8 * (D + 4) * 4 + 2 * kWarps * 8 * 4);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], unsigned a0, unsigned a1, unsigned a2,
@@ -168,11 +168,13 @@ struct Frag {
 
 // One CTA's share: the tiles of its run (or, with `whole`, all tiles of one
 // (request, KV head) per CTA).
-template <int D>
+template <int D, int HW>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     attn_i4_kernel(const AttnI4Params p, const unsigned page_inv, const bool whole) {
     constexpr int KW = Frag<D>::KW, VW = Frag<D>::VW;
     constexpr int RB = D / 2;                   // bytes of a row's codes
+    constexpr int TW = kWarps / HW;             // warps that share a head
+    static_assert(HW * TW == kWarps, "warps are heads x token shares");
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ unsigned s_scan[kWarps];
     __shared__ unsigned s_first;
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv;
+    const int hw = warp % HW, tw = warp / HW;
+    const int HG = p.Hkv / HW;                  // CTAs of a run
     const unsigned sbase = (unsigned)__cvta_generic_to_shared(smem);
     const unsigned ring = sbase + warp * kStages * stage_bytes(D);
     const unsigned char* rings = smem + warp * kStages * stage_bytes(D);
@@ -190,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- where the run begins -------------------------------------------------
     int b, h, j, tokens;           // the run's first tile: request, KV head, tile of the request
     int left;                      // tiles of the run from there on
+    unsigned r = 0;                // the run
     int2* plan = reinterpret_cast<int2*>(p.part);
     if (whole) {
         b = blockIdx.x / p.Hkv;
@@ -220,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         unsigned T;
         const unsigned before = cta_exclusive(mine, s_scan, T);
-        const Runs runs(T, gridDim.x / p.Hkv);
-        const unsigned r = blockIdx.x / p.Hkv;
-        h = blockIdx.x - r * p.Hkv;
+        const Runs runs(T, gridDim.x / HG);
+        r = blockIdx.x / HG;
+        h = (blockIdx.x - r * HG) * HW + hw;
         if (r >= runs.E) return;
         const unsigned x0 = runs.start(r), x1 = runs.start(r + 1);
         if (mine > 0 && x0 >= before && x0 - before < mine) {
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         j = x0 - s_first;
         left = x1 - x0;
         // the requests that begin in this run: which runs hold their parts
-        if (h == 0 && threadIdx.x == 0) {
+        if (blockIdx.x == r * HG && threadIdx.x == 0) {
             int rest = left;
             for (int i = b, at = j; rest > 0; ++i, at = 0) {
                 const int n = tiles_of(tokens_of(p, i));
@@ -325,13 +330,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         j1 = min(n_all, j + left);
         table = p.block_table + (size_t)b * p.max_blocks;
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) lookup(j + warp + s * kWarps, blk[s], in_page[s]);
+        for (int s = 0; s < kStages; ++s) lookup(j + tw + s * TW, blk[s], in_page[s]);
     };
     int4 raw[KW];                           // the query head's values, as loaded
     auto copy_first = [&] {
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) fetch(j + warp + s * kWarps, s, blk[s], in_page[s]);
-        lookup(j + warp + kStages * kWarps, nblk, nin);
+        for (int s = 0; s < kStages; ++s) fetch(j + tw + s * TW, s, blk[s], in_page[s]);
+        lookup(j + tw + kStages * TW, nblk, nin);
         const bf16* q = p.q + ((size_t)b * p.Hq + (size_t)h * G + (g < G ? g : 0)) * D + t * (D / 4);
 #pragma unroll
         for (int w = 0; w < KW; ++w) raw[w] = g < G ? ld_cg_v4(q + 8 * w) : make_int4(0, 0, 0, 0);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         bool fresh = true;                      // no tile yet
 
         int st = 0;
-        for (int i = j + warp; i < j1; i += kWarps) {
+        for (int i = j + tw; i < j1; i += TW) {
             cp_async_wait_group<kStages - 1>();
             __syncwarp();
             const unsigned char* base = rings + st * stage_bytes(D);
@@ -545,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
             __syncwarp();                       // the stage has been read
-            fetch(i + kStages * kWarps, st, nblk, nin);
-            lookup(i + (kStages + 1) * kWarps, nblk, nin);
+            fetch(i + kStages * TW, st, nblk, nin);
+            lookup(i + (kStages + 1) * TW, nblk, nin);
             st = st + 1 == kStages ? 0 : st + 1;
         }
         // ---- the next segment's first copies, then this one's parts ---------------
@@ -561,10 +566,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             } while (tokens == 0);
             open();
         }
-        if (!first) __syncthreads();            // the last segment's parts have been read
-        float* so = reinterpret_cast<float*>(smem + ring_bytes(D));   // [warp][8][D + 4]
-        float* sref = so + kWarps * 8 * (D + 4);                 // [warp][8]
-        float* sl = sref + kWarps * 8;
+        if (TW > 1 && !first) __syncthreads();  // the last segment's parts have been read
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
@@ -572,49 +574,90 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             om0 += __shfl_xor_sync(0xffffffffu, om0, o);
             om1 += __shfl_xor_sync(0xffffffffu, om1, o);
         }
-        if (g == 0) {
-            sref[warp * 8 + 2 * t] = fresh ? kNoRef : ref0;
-            sref[warp * 8 + 2 * t + 1] = fresh ? kNoRef : ref1;
-            sl[warp * 8 + 2 * t] = l0;
-            sl[warp * 8 + 2 * t + 1] = l1;
-        }
-        {
-            constexpr float kE = 16777216.0f, kO = 1048576.0f;   // 2^24, 2^20
-            float* r0 = so + (warp * 8 + 2 * t) * (D + 4) + 8 * VW * g;
-            float* r1 = r0 + (D + 4);
-#pragma unroll
-            for (int q = 0; q < 4 * VW; q += 2) {
-                *reinterpret_cast<float4*>(r0 + 2 * q) =
-                    make_float4(__fmaf_rn(acc[q][0], kE, om0), __fmaf_rn(acc[q][2], kO, om0),
-                                __fmaf_rn(acc[q + 1][0], kE, om0), __fmaf_rn(acc[q + 1][2], kO, om0));
-                *reinterpret_cast<float4*>(r1 + 2 * q) =
-                    make_float4(__fmaf_rn(acc[q][1], kE, om1), __fmaf_rn(acc[q][3], kO, om1),
-                                __fmaf_rn(acc[q + 1][1], kE, om1), __fmaf_rn(acc[q + 1][3], kO, om1));
-            }
-        }
-        if (more) copy_first();
-        __syncthreads();
+        if (fresh) ref0 = ref1 = kNoRef;
+        // dimensions 4 VW 2 g + i of head 2 t + e
+        constexpr int LD = 8 * VW;
+        auto value = [&](int e, int i) {
+            return __fmaf_rn(acc[i >> 1][2 * (i & 1) + e], i & 1 ? 1048576.0f : 16777216.0f,
+                             e ? om1 : om0);
+        };
         const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
-        for (int i = threadIdx.x; i < G * D; i += kThreads) {
-            const int hd = i / D, d = i - hd * D;
-            float top = sref[hd];
+        const unsigned slot = 2 * (r * p.Hkv + h) + (first ? 0 : 1);
+        if constexpr (TW == 1) {
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sref[w * 8 + hd]);
-            float o = 0.0f, L = 0.0f;
+            for (int e = 0; e < 2; ++e) {
+                const int hd = 2 * t + e;
+                if (hd >= G) continue;
+                const float L = e ? l1 : l0;
+                if (all) {
+                    bf16* po = p.out + ((size_t)mb * p.Hq + (size_t)h * G + hd) * D + LD * g;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(sref[w * 8 + hd] - top);
-                o = __fmaf_rn(f, so[(w * 8 + hd) * (D + 4) + d], o);
-                L = __fmaf_rn(f, sl[w * 8 + hd], L);
+                    for (int i = 0; i < LD; i += 8) {
+                        unsigned w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(
+                                __fdividef(value(e, i + 2 * k), L),
+                                __fdividef(value(e, i + 2 * k + 1), L));
+                            w[k] = *reinterpret_cast<const unsigned*>(&v);
+                        }
+                        *reinterpret_cast<int4*>(po + i) = make_int4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float* po = part.o(slot, hd);
+#pragma unroll
+                    for (int i = 0; i < LD; i += 4)
+                        *reinterpret_cast<float4*>(po + LD * g + i) = make_float4(
+                            value(e, i), value(e, i + 1), value(e, i + 2), value(e, i + 3));
+                    if (g == 0) {
+                        po[D] = e ? ref1 : ref0;
+                        po[D + 1] = L;
+                    }
+                }
             }
-            if (all) {
-                p.out[((size_t)mb * p.Hq + (size_t)h * G + hd) * D + d] = f2bf(__fdividef(o, L));
-            } else {
-                float* po = part.o(2 * blockIdx.x + (first ? 0 : 1), hd);
-                po[d] = o;
-                if (d == 0) {
-                    po[D] = top;
-                    po[D + 1] = L;
+            if (more) copy_first();
+        } else {
+            float* so = reinterpret_cast<float*>(smem + ring_bytes(D));   // [warp][8][D + 4]
+            float* sref = so + kWarps * 8 * (D + 4);                      // [warp][8]
+            float* sl = sref + kWarps * 8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hd = warp * 8 + 2 * t + e;
+                if (g == 0) {
+                    sref[hd] = e ? ref1 : ref0;
+                    sl[hd] = e ? l1 : l0;
+                }
+                float* po = so + hd * (D + 4) + LD * g;
+#pragma unroll
+                for (int i = 0; i < LD; i += 4)
+                    *reinterpret_cast<float4*>(po + i) = make_float4(
+                        value(e, i), value(e, i + 1), value(e, i + 2), value(e, i + 3));
+            }
+            if (more) copy_first();
+            __syncthreads();
+            for (int i = threadIdx.x; i < HW * G * D; i += kThreads) {
+                const int x = i / (G * D), hd = (i - x * G * D) / D, d = i % D;
+                float top = kNoRef;
+#pragma unroll
+                for (int w = 0; w < TW; ++w) top = fmaxf(top, sref[(w * HW + x) * 8 + hd]);
+                float o = 0.0f, L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < TW; ++w) {
+                    const int at = (w * HW + x) * 8 + hd;
+                    const float f = ex2(sref[at] - top);
+                    o = __fmaf_rn(f, so[at * (D + 4) + d], o);
+                    L = __fmaf_rn(f, sl[at], L);
+                }
+                const int hx = h - hw + x;
+                if (all) {
+                    p.out[((size_t)mb * p.Hq + (size_t)hx * G + hd) * D + d] = f2bf(__fdividef(o, L));
+                } else {
+                    float* po = part.o(slot + 2 * (x - hw), hd);
+                    po[d] = o;
+                    if (d == 0) {
+                        po[D] = top;
+                        po[D + 1] = L;
+                    }
                 }
             }
         }
@@ -683,10 +726,12 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
 // Contexts of at most this many tokens go to one CTA per (request, KV head).
 constexpr int kWholeCtx = 256;
 
-int grid_of(int B, int Hkv, int max_ctx) {
+// KV heads that a CTA's warps stand for when it takes a run.
+int heads_per_cta(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
+int runs_of(int B, int Hkv, int max_ctx) {
     const long tiles = (long)B * ((max_ctx + kTile - 1) / kTile);
-    const long runs = std::min((tiles + kMinTiles - 1) / kMinTiles, (long)kMaxCtas / Hkv);
-    return (int)std::max(1L, runs) * Hkv;
+    const long fit = kMaxCtas / (Hkv / heads_per_cta(Hkv));
+    return (int)std::max(1L, std::min((tiles + kMinTiles - 1) / kMinTiles, fit));
 }
 
 template <typename Kern, typename... Args>
@@ -704,20 +749,26 @@ cudaError_t launch_i4(Kern kern, dim3 grid, int block, size_t smem, const Launch
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D>
-cudaError_t launch_attention_i4_d(const AttnI4Params& p, const Launch& L) {
-    const size_t smem = smem_bytes(D);
-    cudaError_t e = once_per_context((const void*)attn_i4_kernel<D>, [&] {
-        return cudaFuncSetAttribute(attn_i4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem);
+template <int D, int HW>
+cudaError_t launch_runs(const AttnI4Params& p, int grid, bool whole, const Launch& L) {
+    const size_t smem = smem_bytes(D, HW);
+    cudaError_t e = once_per_context((const void*)attn_i4_kernel<D, HW>, [&] {
+        return cudaFuncSetAttribute(attn_i4_kernel<D, HW>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
     const unsigned inv = 0xFFFFFFFFu / (unsigned)p.page;
+    return launch_i4(attn_i4_kernel<D, HW>, dim3(grid), kThreads, smem, L, p, inv, whole);
+}
+
+template <int D>
+cudaError_t launch_attention_i4_d(const AttnI4Params& p, const Launch& L) {
     const int max_ctx = p.max_blocks * p.page;
-    if (max_ctx <= kWholeCtx)
-        return launch_i4(attn_i4_kernel<D>, dim3(p.B * p.Hkv), kThreads, smem, L, p, inv, true);
-    const int grid = grid_of(p.B, p.Hkv, max_ctx);
-    e = launch_i4(attn_i4_kernel<D>, dim3(grid), kThreads, smem, L, p, inv, false);
+    if (max_ctx <= kWholeCtx) return launch_runs<D, 1>(p, p.B * p.Hkv, true, L);
+    const int HW = heads_per_cta(p.Hkv), grid = runs_of(p.B, p.Hkv, max_ctx) * (p.Hkv / HW);
+    cudaError_t e = HW == 4   ? launch_runs<D, 4>(p, grid, false, L)
+                    : HW == 2 ? launch_runs<D, 2>(p, grid, false, L)
+                              : launch_runs<D, 1>(p, grid, false, L);
     if (e != cudaSuccess) return e;
     return launch_i4(attn_i4_combine_kernel<D>, dim3(p.Hq, p.B), kCombineThreads, 0, L, p);
 }
@@ -726,7 +777,7 @@ cudaError_t launch_attention_i4_d(const AttnI4Params& p, const Launch& L) {
 
 size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx) {
     if (max_ctx <= kWholeCtx) return 0;
-    return plan_bytes(B) + (size_t)grid_of(B, Hkv, max_ctx) * 2 * (Hq / Hkv) * (D + 4) * 4;
+    return plan_bytes(B) + (size_t)runs_of(B, Hkv, max_ctx) * 2 * Hq * (D + 4) * 4;
 }
 
 cudaError_t launch_attention_i4(const AttnI4Params& p, const Launch& L) {
