@@ -84,6 +84,31 @@ __device__ __forceinline__ unsigned transpose8(unsigned v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
+// Two floats in one register pair: one instruction for the lane's two heads.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -348,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // head g's dimensions of chunk t: for word w, elements (0, 4) and (2, 6)
         // times 16 meet the low nibbles of the masks, (1, 5) and (3, 7) the high
         unsigned qb[KW][4];
-        float ch0, ch1, qs0, qs1;               // score factors of heads 2 t, 2 t + 1
+        f32x2 ch, qs;                           // score factors of heads 2 t, 2 t + 1
         {
             float sum = 0.0f, top = 0.0f;
 #pragma unroll
@@ -370,14 +395,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int e = max(-107, min(126, 137 - (int)(__float_as_uint(top) >> 23)));
             const float up = __uint_as_float((unsigned)(127 + e) << 23);
             const float sc = p.scale * 1.4426950408889634f;
-            float ch = __uint_as_float((unsigned)(127 + 20 - e) << 23) * sc;
+            float f = __uint_as_float((unsigned)(127 + 20 - e) << 23) * sc;
             // a NaN shows in the sum; from 2^118 on FP16 would overflow
-            if (!(fabsf(sum) <= 3e38f) || top >= 3.3e35f) ch = __uint_as_float(0x7FC00000u);
-            const float qs = sum * sc;
-            ch0 = __shfl_sync(0xffffffffu, ch, 8 * t);
-            ch1 = __shfl_sync(0xffffffffu, ch, 8 * t + 4);
-            qs0 = __shfl_sync(0xffffffffu, qs, 8 * t);
-            qs1 = __shfl_sync(0xffffffffu, qs, 8 * t + 4);
+            if (!(fabsf(sum) <= 3e38f) || top >= 3.3e35f) f = __uint_as_float(0x7FC00000u);
+            sum *= sc;
+            ch = pair(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
+            qs = pair(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 float f[8];
@@ -390,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         }
 
-        // rows: dimensions 2 i (times 2^-24) and 2 i + 1 (times 2^-20) of the lane's;
-        // columns: heads 2 t, 2 t + 1
+        // times 2^-24, rows: sums of the low nibbles (dimension 2 i of the lane's) and
+        // of the whole bytes c_2i + 16 c_2i+1; columns: heads 2 t, 2 t + 1
         float acc[4 * VW][4];
 #pragma unroll
         for (int i = 0; i < 4 * VW; ++i)
@@ -442,8 +465,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float ks = bf_lo(mt.x), km = bf_hi(mt.x);
                     sv[k + r] = bf_lo(mt.y);
                     mv[k + r] = bf_hi(mt.y);
-                    y0[k + r] = __fmaf_rn(c[2 * r] * ks, ch0, __fmaf_rn(qs0, km, -ref0));
-                    y1[k + r] = __fmaf_rn(c[2 * r + 1] * ks, ch1, __fmaf_rn(qs1, km, -ref1));
+                    const f32x2 y = fma2(mul2(pair(c[2 * r], c[2 * r + 1]), pair(ks, ks)), ch,
+                                         fma2(qs, pair(km, km), pair(-ref0, -ref1)));
+                    split(y, y0[k + r], y1[k + r]);
                 }
             }
             if ((i + 1) * kTile > tokens) {     // the request's last tile
@@ -453,20 +477,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
 
             // ---- weights -----------------------------------------------------------
-            // ref is raised only where a weight would pass 2^15 (or a probability
-            // with s near 0 would pass 2^90); the raise takes the tile's largest
-            // to 2^10
+            // ref is raised only where the tile's largest p times its largest s
+            // passes 2^15, which bounds every weight (s counts 2^-75 at least, so
+            // that p stays below 2^90); the raise takes the largest p s to 2^10
             float p0[4], p1[4];
-            float big = 0.0f, bigp = 0.0f;
+            float bigp = 0.0f, bigs = 2.7e-23f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 p0[k] = ex2(y0[k]);
                 p1[k] = ex2(y1[k]);
-                const float pm = fmaxf(p0[k], p1[k]);
-                big = fmaxf(big, pm * fabsf(sv[k]));
-                bigp = fmaxf(bigp, pm);
+                bigp = fmaxf(bigp, fmaxf(p0[k], p1[k]));
+                bigs = fmaxf(bigs, fabsf(sv[k]));
             }
-            if (fresh || __any_sync(0xffffffffu, big > 32768.0f || bigp > 1.2e27f)) {
+            if (fresh || __any_sync(0xffffffffu, bigp * bigs > 32768.0f)) {
                 float z0 = kNoRef, z1 = kNoRef;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -509,11 +532,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             unsigned wb[4];                     // head g, tokens 2 t, 2 t + 1 of each 8
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                l0 += p0[k];
-                l1 += p1[k];
-                om0 = __fmaf_rn(p0[k], mv[k], om0);
-                om1 = __fmaf_rn(p1[k], mv[k], om1);
-                wb[k] = transpose8(h2_of(p0[k] * sv[k], p1[k] * sv[k]));
+                const f32x2 pp = pair(p0[k], p1[k]);
+                split(add2(pair(l0, l1), pp), l0, l1);
+                split(fma2(pp, pair(mv[k], mv[k]), pair(om0, om1)), om0, om1);
+                float w0, w1;
+                split(mul2(pp, pair(sv[k], sv[k])), w0, w1);
+                wb[k] = transpose8(h2_of(w0, w1));
             }
 
             // ---- o += V^T w ----------------------------------------------------------
@@ -537,14 +561,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         // four dimensions of both tokens, one token per half
-                        unsigned u0 = __byte_perm(x[0][w], x[1][w], hf ? 0x7632 : 0x5410);
-                        unsigned u1 = __byte_perm(x[2][w], x[3][w], hf ? 0x7632 : 0x5410);
+                        const unsigned u0 = __byte_perm(x[0][w], x[1][w], hf ? 0x7632 : 0x5410);
+                        const unsigned u1 = __byte_perm(x[2][w], x[3][w], hf ? 0x7632 : 0x5410);
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            mma_f16(acc[4 * w + 2 * hf + s], u0 & 0x000F000Fu, u0 & 0x00F000F0u,
-                                    u1 & 0x000F000Fu, u1 & 0x00F000F0u, wb[k], wb[k + 1]);
-                            u0 >>= 8;
-                            u1 >>= 8;
+                            // both tokens' byte s alone (one permute with zero for the
+                            // upper one), then its low nibble
+                            const unsigned b0 = s ? __byte_perm(u0, 0, 0x4341) : u0 & 0x00FF00FFu;
+                            const unsigned b1 = s ? __byte_perm(u1, 0, 0x4341) : u1 & 0x00FF00FFu;
+                            mma_f16(acc[4 * w + 2 * hf + s], b0 & 0x000F000Fu, b0,
+                                    b1 & 0x000F000Fu, b1, wb[k], wb[k + 1]);
                         }
                     }
                 }
@@ -578,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // dimensions 4 VW 2 g + i of head 2 t + e
         constexpr int LD = 8 * VW;
         auto value = [&](int e, int i) {
-            return __fmaf_rn(acc[i >> 1][2 * (i & 1) + e], i & 1 ? 1048576.0f : 16777216.0f,
-                             e ? om1 : om0);
+            const float lo = acc[i >> 1][e];
+            return i & 1 ? __fmaf_rn(acc[i >> 1][2 + e] - lo, 1048576.0f, e ? om1 : om0)
+                         : __fmaf_rn(lo, 16777216.0f, e ? om1 : om0);
         };
         const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
         const unsigned slot = 2 * (r * p.Hkv + h) + (first ? 0 : 1);
@@ -667,15 +694,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // Joins the parts of each (request, query head) that several CTAs share, and
 // writes the zeros of requests without tokens. One CTA per query head and
-// request; its warps take the parts in turn.
+// request; its warps take the parts in turn, each with a running ref, so that
+// a part is one round of loads, and then join theirs.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const AttnI4Params p) {
     constexpr int NW = kCombineThreads / 32, EL = D / 32;
-    __shared__ float s_max[NW];
+    __shared__ float s_ref[NW], s_l[NW];
     __shared__ float so[NW][D];
-    __shared__ float s_l[NW];
     const int hq = blockIdx.x, b = blockIdx.y;
-    const int G = p.Hq / p.Hkv, h = hq / G;
+    const int G = p.Hq / p.Hkv, h = hq / G, hd = hq - h * G;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bf16* out = p.out + ((size_t)b * p.Hq + hq) * D;
     pdl_wait();
@@ -688,36 +715,37 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
     const int c0 = plan.x >> 1, c1 = plan.y;
     if (c0 == c1) return;                       // one CTA had all of it
     const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
-    const int hd = hq - h * G;
-    auto slot = [&](int c) { return 2u * (c * p.Hkv + h) + (c == c0 ? plan.x & 1 : 0); };
-    float top = kNoRef;
-    for (int c = c0 + (int)threadIdx.x; c <= c1; c += kCombineThreads)
-        top = fmaxf(top, __ldcg(part.o(slot(c), hd) + D));
-    top = warp_max(top);
-    if (lane == 0) s_max[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w]);
-    float o[EL], L = 0.0f;
+    float ref = kNoRef, L = 0.0f, o[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) o[e] = 0.0f;
     for (int c = c0 + warp; c <= c1; c += NW) {
-        const float* po = part.o(slot(c), hd);
-        const float f = ex2(__ldcg(po + D) - top);
-        L = __fmaf_rn(f, __ldcg(po + D + 1), L);
+        const float* po = part.o(2u * (c * p.Hkv + h) + (c == c0 ? plan.x & 1 : 0), hd);
+        const float2 rl = __ldcg(reinterpret_cast<const float2*>(po + D));
+        float v[EL];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(f, __ldcg(po + lane + 32 * e), o[e]);
+        for (int e = 0; e < EL; ++e) v[e] = __ldcg(po + lane + 32 * e);
+        const float up = fmaxf(ref, rl.x), f = ex2(ref - up), g = ex2(rl.x - up);
+        ref = up;
+        L = __fmaf_rn(L, f, rl.y * g);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(o[e], f, v[e] * g);
     }
 #pragma unroll
     for (int e = 0; e < EL; ++e) so[warp][lane + 32 * e] = o[e];
-    if (lane == 0) s_l[warp] = L;
+    if (lane == 0) {
+        s_ref[warp] = ref;
+        s_l[warp] = L;
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kCombineThreads) {
-        float O = 0.0f, Ls = 0.0f;
+        float top = kNoRef, O = 0.0f, Ls = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, s_ref[w]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            O += so[w][d];
-            Ls += s_l[w];
+            const float f = ex2(s_ref[w] - top);
+            O = __fmaf_rn(f, so[w][d], O);
+            Ls = __fmaf_rn(f, s_l[w], Ls);
         }
         out[d] = f2bf(__fdividef(O, Ls));
     }
