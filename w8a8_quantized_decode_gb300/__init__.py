@@ -154,6 +154,8 @@ def build(force: bool = False) -> str:
 def lib():
     """Load liba8w8.so (raises if it is missing; it is never bypassed)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -481,18 +483,18 @@ def a8w8_prefill_layer_i8kv(weights: dict, cfg: dict, hidden, slot_mapping, bloc
         None if t is None else ctypes.byref(t), _stream(stream)))
 
 
-def _refuse(what, t, dtype, shape):
+def _refuse(what, dtype, numel):
     raise A8W8Error(ERR_INVALID_ARG, f"{what}: need a contiguous {dtype} tensor on the current "
-                    f"CUDA device" + (f" of shape {tuple(shape)}" if shape is not None else ""))
+                    f"CUDA device" + (f" of {numel} elements" if numel is not None else ""))
 
 
-def _typed(t, dtype, what, dev, shape=None):
+def _typed(t, dtype, what, dev, numel=None):
     """Device pointer of t after checks of its type, device (the current one, by index) and,
-    where given, shape: the 4-bit and page entries index with these tensors, so a wrong one is
+    where given, size: the 4-bit and page entries index with these tensors, so a wrong one is
     refused here."""
     if t is None or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
-            (shape is not None and t.shape != shape):
-        _refuse(what, t, dtype, shape)
+            (numel is not None and t.numel() != numel):
+        _refuse(what, dtype, numel)
     return t.data_ptr()
 
 
@@ -527,11 +529,11 @@ def paged_kv_write_i4(k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta, page
     [slots, Hkv, D / 2] uint8 and (s, m) pairs [slots, Hkv, 2] bf16."""
     torch = _torch()
     what, dev = "paged_kv_write_i4", _device()
-    T, Hkv, D = shape = k.shape
+    T, Hkv, D = k.shape
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     _check(lib().paged_kv_write_i4(
-        _typed(k, torch.bfloat16, what, dev), _typed(v, torch.bfloat16, what, dev, shape), T, Hkv,
-        D, _typed(slot_mapping, torch.int32, what, dev, (T,)), *ptrs, num_blocks, page_size,
+        _typed(k, torch.bfloat16, what, dev), _typed(v, torch.bfloat16, what, dev, T * Hkv * D), T,
+        Hkv, D, _typed(slot_mapping, torch.int32, what, dev, T), *ptrs, num_blocks, page_size,
         _raw_stream(stream, dev)))
 
 
@@ -544,14 +546,14 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     Hkv, D = k_codes.shape[-2], 2 * k_codes.shape[-1]
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
-    shape = (T, Hkv, D)
     if out is None:
-        both = torch.empty((2, *shape), dtype=torch.bfloat16, device=k_codes.device)
+        both = torch.empty((2, T, Hkv, D), dtype=torch.bfloat16, device=k_codes.device)
         out = both[0], both[1]
     k, v = out
     _check(lib().paged_kv_read_i4(
-        *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, (T,)), T, Hkv, D,
-        _typed(k, torch.bfloat16, what, dev, shape), _typed(v, torch.bfloat16, what, dev, shape),
+        *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, T), T, Hkv, D,
+        _typed(k, torch.bfloat16, what, dev, T * Hkv * D),
+        _typed(v, torch.bfloat16, what, dev, T * Hkv * D),
         _raw_stream(stream, dev)))
     return k, v
 
@@ -566,7 +568,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     pairs [slots, Hkv, 2] bf16), in float32, narrowed to bf16 once."""
     torch = _torch()
     what, dev = "paged_decode_attention_i4kv", _device()
-    B, Hq, D = shape = q.shape
+    B, Hq, D = q.shape
     Hkv = k_codes.shape[-2]
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     max_blocks = block_table.shape[-1]
@@ -579,9 +581,9 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     o = out if out is not None else torch.empty_like(q)
     _check(L.paged_decode_attention_i4kv(
         _typed(q, torch.bfloat16, what, dev), *ptrs,
-        _typed(block_table, torch.int32, what, dev, (B, max_blocks)),
-        _typed(ctx_lens, torch.int32, what, dev, (B,)), B, Hq, Hkv, D, page_size, max_blocks,
-        num_blocks, scale, _typed(o, torch.bfloat16, what, dev, shape),
+        _typed(block_table, torch.int32, what, dev, B * max_blocks),
+        _typed(ctx_lens, torch.int32, what, dev, B), B, Hq, Hkv, D, page_size, max_blocks,
+        num_blocks, scale, _typed(o, torch.bfloat16, what, dev, B * Hq * D),
         None if ws is None else _typed(ws, torch.uint8, what, dev), 0 if ws is None else ws.numel(),
         _raw_stream(stream, dev)))
     return o
@@ -624,8 +626,8 @@ class PagePool:
             raise A8W8Error(ERR_INVALID_ARG, f"{what}: block_table is [B, max_blocks]")
         B, max_blocks = block_table.shape
         return (_typed(block_table, i32, what, dev),
-                None if ctx_lens is None else _typed(ctx_lens, i32, what, dev, (B,)),
-                _typed(refcount, i32, what, dev, (self.num_blocks,)), B, max_blocks)
+                None if ctx_lens is None else _typed(ctx_lens, i32, what, dev, B),
+                _typed(refcount, i32, what, dev, self.num_blocks), B, max_blocks)
 
 
 def pages_workspace_bytes(num_blocks: int, B: int, n: int) -> int:
@@ -644,8 +646,8 @@ def paged_copy_pages(pool, src, dst, stream=None):
     """Copy page src[i] to page dst[i] (int32 [n] on the device) in every cache of the pool."""
     what = "paged_copy_pages"
     i32, dev, n = _torch().int32, pool._here(what), src.numel()
-    _check(lib().paged_copy_pages(*pool._args, pool.num_blocks, _typed(src, i32, what, dev, (n,)),
-                                  _typed(dst, i32, what, dev, (n,)), n, _raw_stream(stream, dev)))
+    _check(lib().paged_copy_pages(*pool._args, pool.num_blocks, _typed(src, i32, what, dev, n),
+                                  _typed(dst, i32, what, dev, n), n, _raw_stream(stream, dev)))
 
 
 def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None, stream=None):
@@ -655,8 +657,8 @@ def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None
     i32, dev, n = _torch().int32, pool._here(what), parents.numel()
     bt, cl, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount, ctx_lens)
     _check(lib().paged_fork(*pool._args, pool.num_blocks, pool.page_size, bt, cl, rc, B,
-                            max_blocks, _typed(parents, i32, what, dev, (n,)),
-                            _typed(children, i32, what, dev, (n,)), n,
+                            max_blocks, _typed(parents, i32, what, dev, n),
+                            _typed(children, i32, what, dev, n), n,
                             *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
 
 
@@ -667,8 +669,8 @@ def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=Non
     i32, dev, n = _torch().int32, pool._here(what), rows.numel()
     bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     _check(lib().paged_reserve(bt, rc, B, max_blocks, pool.num_blocks, pool.page_size,
-                               _typed(rows, i32, what, dev, (n,)),
-                               _typed(tokens, i32, what, dev, (n,)), n,
+                               _typed(rows, i32, what, dev, n),
+                               _typed(tokens, i32, what, dev, n), n,
                                *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
 
 
@@ -679,7 +681,7 @@ def paged_free(pool, block_table, ctx_lens, refcount, rows, stream=None):
     i32, dev, n = _torch().int32, pool._here(what), rows.numel()
     bt, cl, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount, ctx_lens)
     _check(lib().paged_free(bt, cl, rc, B, max_blocks, pool.num_blocks,
-                            _typed(rows, i32, what, dev, (n,)), n, _raw_stream(stream, dev)))
+                            _typed(rows, i32, what, dev, n), n, _raw_stream(stream, dev)))
 
 
 def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=None):
@@ -692,7 +694,7 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
     if num_live is None:
         num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
     _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
-                               _typed(num_live, torch.int32, what, dev, (1,)),
+                               _typed(num_live, torch.int32, what, dev, 1),
                                *_pages_ws(pool, B, 0, ws, what, dev), _raw_stream(stream, dev)))
     return num_live
 

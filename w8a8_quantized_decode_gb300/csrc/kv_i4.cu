@@ -59,24 +59,33 @@ __device__ __forceinline__ unsigned quant_row_i4(const int4& raw, unsigned& code
     if (s == 0.0f) return meta;
     float x[8];
     unpack8(raw, x);
+    if (!(s >= 7.9e-31f && s <= 1.2e30f)) {   // about 2^-100, 2^100: see below
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = __float2int_rn(fminf(__fdiv_rn(__fsub_rn(x[e], m), s), 15.0f));
+            codes |= (unsigned)c << (4 * e);
+        }
+        return meta;
+    }
     // x / s without a division: the float quotient by R = RN(1 / s) and one
     // correction by the exact remainder (as quant_code in common.cuh), where
-    // neither R nor the remainder leaves the normal range; the division else
+    // neither R nor the remainder leaves the normal range. The quotient is at
+    // most 15 (1 + 2^-8) there, so its rounding needs no clamp: adding 2^23
+    // leaves rne(q) in the low bits, and eight of them join by multiply-adds,
+    // the exponents' bits adding up to a constant.
     const float R = __frcp_rn(s);
-    const bool plain = !(s >= 7.9e-31f && s <= 1.2e30f);   // about 2^-100, 2^100
+    const f32x2 ms = pair(-m, -m), ns = pair(-s, -s), Rs = pair(R, R),
+                big = pair(8388608.0f, 8388608.0f);
+    unsigned acc = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float d = __fsub_rn(x[e], m);
-        float q;
-        if (plain) {
-            q = __fdiv_rn(d, s);
-        } else {
-            const float q0 = __fmul_rn(d, R);
-            q = __fmaf_rn(__fmaf_rn(-q0, s, d), R, q0);
-        }
-        const int c = max(0, min(15, __float2int_rn(q)));
-        codes |= (unsigned)c << (4 * e);
+    for (int e = 6; e >= 0; e -= 2) {
+        const f32x2 d = add2(pair(x[e], x[e + 1]), ms);
+        const f32x2 q0 = mul2(d, Rs);
+        float lo, hi;
+        split(add2(fma2(fma2(q0, ns, d), Rs, q0), big), lo, hi);
+        acc = (acc * 16u + __float_as_uint(hi)) * 16u + __float_as_uint(lo);
     }
+    codes = acc - 0xFB000000u;
     return meta;
 }
 
