@@ -547,9 +547,10 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        both = torch.empty((2, T, Hkv, D), dtype=torch.bfloat16, device=k_codes.device)
-        out = both[0], both[1]
-    k, v = out
+        k = k_meta.new_empty((T, Hkv, D))
+        v = torch.empty_like(k)
+    else:
+        k, v = out
     _check(lib().paged_kv_read_i4(
         *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, T), T, Hkv, D,
         _typed(k, torch.bfloat16, what, dev, T * Hkv * D),

@@ -13,10 +13,12 @@
 // s = m = NaN and codes 0: it reads as NaN.
 //
 // Both kernels are bound by HBM: a (token, head) pair of rows is 4 D bytes of
-// BF16 and D + 8 of cache. A row belongs to D / 8 lanes of 16 BF16 bytes and
-// one 32-bit word of codes each, so every access is a full vector and a
-// warp's stores of one row are contiguous; K and V of the row are in flight
-// together.
+// BF16 and D + 8 of cache. What stands against it is the issue rate of the
+// per-row work (s and its reciprocal, the reduction), which all lanes of a row
+// do: a row belongs to D / 16 lanes of 16 values, half the lanes that 16-byte
+// loads would need and twice the values per row's work (write of 16384 tokens
+// of 8 heads: 294 warp instructions per 16 rows' values with D / 8 lanes, XXX
+// with D / 16). K and V of the row are in flight together.
 #include "kernels.cuh"
 
 namespace a8w8 {
@@ -32,18 +34,20 @@ __device__ __forceinline__ unsigned as_u32(__nv_bfloat162 h) {
     return *reinterpret_cast<unsigned*>(&h);
 }
 
-// The row's (s, m) word and the lane's eight codes. LPR lanes hold the row,
-// eight values each; every lane of the warp calls this.
+// The row's (s, m) word and the lane's sixteen codes. LPR lanes hold the row,
+// sixteen values each; every lane of the warp calls this.
 template <int LPR>
-__device__ __forceinline__ unsigned quant_row_i4(const int4& raw, unsigned& codes) {
-    const __nv_bfloat162 h0 = as_bf162(raw.x), h1 = as_bf162(raw.y), h2 = as_bf162(raw.z),
-                         h3 = as_bf162(raw.w);
+__device__ __forceinline__ unsigned quant_row_i4(const int4 (&raw)[2], unsigned (&codes)[2]) {
     // maximum and negated minimum side by side, NaN taken over
-    const __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(h0, h1), __hmax2_nan(h2, h3));
-    const __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(h0, h1), __hmin2_nan(h2, h3));
-    const __nv_bfloat16 hi = __hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx));
-    const __nv_bfloat16 lo = __hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn));
-    __nv_bfloat162 r = __halves2bfloat162(hi, __hneg(lo));
+    __nv_bfloat162 mx = as_bf162(raw[0].x), mn = mx;
+    const int w[7] = {raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        mx = __hmax2_nan(mx, as_bf162(w[i]));
+        mn = __hmin2_nan(mn, as_bf162(w[i]));
+    }
+    __nv_bfloat162 r = __halves2bfloat162(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx)),
+                                          __hneg(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn))));
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1)
         r = __hmax2_nan(r, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
@@ -51,41 +55,54 @@ __device__ __forceinline__ unsigned quant_row_i4(const int4& raw, unsigned& code
     const __nv_bfloat16 mb = __hneg(__high2bfloat16(r));
     const float m = __bfloat162float(mb);
     const float range = __fsub_rn(top, m);
-    codes = 0u;
+    codes[0] = codes[1] = 0u;
     if (!isfinite(range)) return 0x7FC07FC0u;   // NaN, NaN
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.0f));
+    // Quotients without a division: the float product with R = RN(1 / y) and
+    // one correction by the exact remainder (as quant_code in common.cuh),
+    // where neither R nor the remainder leaves the normal range.
+    constexpr float kR15 = 1.0f / 15.0f;
+    const bool plain = !(range >= 1.6e-29f && range <= 1.2e30f);   // about 2^-96, 2^100
+    float sf;
+    if (plain) {
+        sf = __fdiv_rn(range, 15.0f);
+    } else {
+        sf = __fmul_rn(range, kR15);
+        sf = __fmaf_rn(__fmaf_rn(-sf, 15.0f, range), kR15, sf);
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(sf);
     const float s = __bfloat162float(sb);
     const unsigned meta = as_u32(__halves2bfloat162(sb, mb));
     if (s == 0.0f) return meta;
-    float x[8];
-    unpack8(raw, x);
-    if (!(s >= 7.9e-31f && s <= 1.2e30f)) {   // about 2^-100, 2^100: see below
+    float x[2][8];
+    unpack8(raw[0], x[0]);
+    unpack8(raw[1], x[1]);
+    if (plain) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = __float2int_rn(fminf(__fdiv_rn(__fsub_rn(x[e], m), s), 15.0f));
-            codes |= (unsigned)c << (4 * e);
+        for (int e = 0; e < 16; ++e) {
+            const float q = fminf(__fdiv_rn(__fsub_rn(x[e / 8][e % 8], m), s), 15.0f);
+            codes[e / 8] |= (unsigned)__float2int_rn(q) << (4 * (e % 8));
         }
         return meta;
     }
-    // x / s without a division: the float quotient by R = RN(1 / s) and one
-    // correction by the exact remainder (as quant_code in common.cuh), where
-    // neither R nor the remainder leaves the normal range. The quotient is at
-    // most 15 (1 + 2^-8) there, so its rounding needs no clamp: adding 2^23
-    // leaves rne(q) in the low bits, and eight of them join by multiply-adds,
-    // the exponents' bits adding up to a constant.
+    // The quotient is at most 15 (1 + 2^-8) here, so its rounding needs no
+    // clamp: adding 2^23 leaves rne(q) in the low bits, and eight of them join
+    // by multiply-adds, the exponents' bits adding up to a constant.
     const float R = __frcp_rn(s);
     const f32x2 ms = pair(-m, -m), ns = pair(-s, -s), Rs = pair(R, R),
                 big = pair(8388608.0f, 8388608.0f);
-    unsigned acc = 0u;
+    unsigned acc[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 6; e >= 0; e -= 2) {
-        const f32x2 d = add2(pair(x[e], x[e + 1]), ms);
-        const f32x2 q0 = mul2(d, Rs);
-        float lo, hi;
-        split(add2(fma2(fma2(q0, ns, d), Rs, q0), big), lo, hi);
-        acc = (acc * 16u + __float_as_uint(hi)) * 16u + __float_as_uint(lo);
-    }
-    codes = acc - 0xFB000000u;
+    for (int e = 6; e >= 0; e -= 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x2 d = add2(pair(x[h][e], x[h][e + 1]), ms);
+            const f32x2 q0 = mul2(d, Rs);
+            float lo, hi;
+            split(add2(fma2(fma2(q0, ns, d), Rs, q0), big), lo, hi);
+            acc[h] = (acc[h] * 16u + __float_as_uint(hi)) * 16u + __float_as_uint(lo);
+        }
+    codes[0] = acc[0] - 0xFB000000u;
+    codes[1] = acc[1] - 0xFB000000u;
     return meta;
 }
 
@@ -95,31 +112,37 @@ __global__ void __launch_bounds__(kI4Threads)
                        const int32_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_codes,
                        uint8_t* __restrict__ v_codes, bf16* __restrict__ k_meta,
                        bf16* __restrict__ v_meta, long num_slots, unsigned* err) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 16;
     pdl_wait();
     pdl_trigger();
-    const long row = ((long)blockIdx.x * kI4Threads + threadIdx.x) / LPR;   // token * Hkv + head
+    // token * Hkv + head, at most 2^31 and some
+    const unsigned row = blockIdx.x * (kI4Threads / LPR) + threadIdx.x / LPR;
     const int j = threadIdx.x % LPR;
-    const bool in = row < (long)T * Hkv;
-    const long t = in ? row / Hkv : 0;
-    const int hh = (int)(in ? row - t * Hkv : 0);
-    long slot = in ? (long)__ldg(slot_mapping + t) : -1;
+    const unsigned t = row / (unsigned)Hkv, hh = row - t * Hkv;
+    long slot = t < (unsigned)T ? (long)__ldg(slot_mapping + t) : -1;
+    int4 kr[2], vr[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        kr[i] = vr[i] = make_int4(0, 0, 0, 0);
+        if (t < (unsigned)T) {
+            kr[i] = ld_stream_v4(k + (size_t)row * D + 8 * (j + LPR * i));
+            vr[i] = ld_stream_v4(v + (size_t)row * D + 8 * (j + LPR * i));
+        }
+    }
     if (slot >= num_slots) {
         if (j == 0 && hh == 0) set_error(err, 0x1u);
         slot = -1;
     }
-    int4 kr = make_int4(0, 0, 0, 0), vr = kr;
-    if (slot >= 0) {
-        kr = ld_stream_v4(k + (size_t)row * D + 8 * j);
-        vr = ld_stream_v4(v + (size_t)row * D + 8 * j);
-    }
-    unsigned kc, vc;
+    unsigned kc[2], vc[2];
     const unsigned km = quant_row_i4<LPR>(kr, kc);
     const unsigned vm = quant_row_i4<LPR>(vr, vc);
     if (slot < 0) return;
     const size_t dst = (size_t)slot * Hkv + hh;
-    reinterpret_cast<unsigned*>(k_codes)[dst * LPR + j] = kc;
-    reinterpret_cast<unsigned*>(v_codes)[dst * LPR + j] = vc;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        reinterpret_cast<unsigned*>(k_codes)[dst * 2 * LPR + j + LPR * i] = kc[i];
+        reinterpret_cast<unsigned*>(v_codes)[dst * 2 * LPR + j + LPR * i] = vc[i];
+    }
     if (j == 0) {
         reinterpret_cast<unsigned*>(k_meta)[dst] = km;
         reinterpret_cast<unsigned*>(v_meta)[dst] = vm;
@@ -127,15 +150,19 @@ __global__ void __launch_bounds__(kI4Threads)
 }
 
 // Eight values of a row from their codes: c s + m rounded to BF16 once (the
-// float32 sum is the one rounding before it; c s is exact).
+// float32 sum is the one rounding before it; c s is exact). A code joins the
+// exponent of 2^23, of which it is the lowest bits.
 __device__ __forceinline__ int4 dequant8(unsigned codes, unsigned meta) {
     const float s = __uint_as_float(meta << 16), m = __uint_as_float(meta & 0xFFFF0000u);
+    const f32x2 ss = pair(s, s), mm = pair(m, m), big = pair(-8388608.0f, -8388608.0f);
     unsigned o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float a = __fmaf_rn((float)((codes >> (8 * e)) & 15u), s, m);
-        const float b = __fmaf_rn((float)((codes >> (8 * e + 4)) & 15u), s, m);
-        o[e] = as_u32(__floats2bfloat162_rn(a, b));
+        const float a = __uint_as_float((codes >> (8 * e) & 15u) | 0x4B000000u);
+        const float b = __uint_as_float((codes >> (8 * e + 4) & 15u) | 0x4B000000u);
+        float lo, hi;
+        split(fma2(add2(pair(a, b), big), ss, mm), lo, hi);
+        o[e] = as_u32(__floats2bfloat162_rn(lo, hi));
     }
     return make_int4(o[0], o[1], o[2], o[3]);
 }
@@ -146,34 +173,44 @@ __global__ void __launch_bounds__(kI4Threads)
                       const bf16* __restrict__ k_meta, const bf16* __restrict__ v_meta,
                       long num_slots, const int32_t* __restrict__ slot_mapping, int T, int Hkv,
                       bf16* __restrict__ k, bf16* __restrict__ v, unsigned* err) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 16;
     pdl_wait();
     pdl_trigger();
-    const long row = ((long)blockIdx.x * kI4Threads + threadIdx.x) / LPR;
+    const unsigned row = blockIdx.x * (kI4Threads / LPR) + threadIdx.x / LPR;
     const int j = threadIdx.x % LPR;
-    if (row >= (long)T * Hkv) return;
-    const long t = row / Hkv;
-    const int hh = (int)(row - t * Hkv);
+    const unsigned t = row / (unsigned)Hkv, hh = row - t * Hkv;
+    if (t >= (unsigned)T) return;
     const long slot = __ldg(slot_mapping + t);
-    int4 ko = make_int4(0, 0, 0, 0), vo = ko;
+    int4 ko[2], vo[2];
+    ko[0] = ko[1] = vo[0] = vo[1] = make_int4(0, 0, 0, 0);
     if (slot >= num_slots) {
         if (j == 0 && hh == 0) set_error(err, 0x1u);
     } else if (slot >= 0) {
         const size_t src = (size_t)slot * Hkv + hh;
-        const unsigned kc = __ldcg(reinterpret_cast<const unsigned*>(k_codes) + src * LPR + j);
-        const unsigned vc = __ldcg(reinterpret_cast<const unsigned*>(v_codes) + src * LPR + j);
+        unsigned kc[2], vc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            kc[i] = __ldcg(reinterpret_cast<const unsigned*>(k_codes) + src * 2 * LPR + j + LPR * i);
+            vc[i] = __ldcg(reinterpret_cast<const unsigned*>(v_codes) + src * 2 * LPR + j + LPR * i);
+        }
         const unsigned km = __ldcg(reinterpret_cast<const unsigned*>(k_meta) + src);
         const unsigned vm = __ldcg(reinterpret_cast<const unsigned*>(v_meta) + src);
-        ko = dequant8(kc, km);
-        vo = dequant8(vc, vm);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            ko[i] = dequant8(kc[i], km);
+            vo[i] = dequant8(vc[i], vm);
+        }
     }
-    *reinterpret_cast<int4*>(k + (size_t)row * D + 8 * j) = ko;
-    *reinterpret_cast<int4*>(v + (size_t)row * D + 8 * j) = vo;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<int4*>(k + (size_t)row * D + 8 * (j + LPR * i)) = ko[i];
+        *reinterpret_cast<int4*>(v + (size_t)row * D + 8 * (j + LPR * i)) = vo[i];
+    }
 }
 
 template <typename Kern, typename... Args>
 cudaError_t launch_rows_i4(Kern kern, long rows, int D, const Launch& L, Args... args) {
-    const long per = kI4Threads / (D / 8);
+    const long per = kI4Threads / (D / 16);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
     cfg.blockDim = dim3(kI4Threads);

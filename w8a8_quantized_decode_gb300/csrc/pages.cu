@@ -23,7 +23,10 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr unsigned kUnitBytes = 16384;   // a copy unit: 4 vectors of 16 bytes per thread
-constexpr int kCopyCtasPerSm = 4;
+// CTAs per SM: 4 for whole pages (copy 172 us for 1.07 GB, 180 at 6 or 8); 8
+// for forks, whose partial pages leave some of a CTA's units empty (fork of 64
+// children 68 us, 75 at 4).
+constexpr int kCopyCtasPerSm = 4, kForkCtasPerSm = 8;
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kErrBlock = 0x2u, kErrCtx = 0x4u, kErrRow = 0x40u, kErrPages = 0x80u,
                    kErrAlias = 0x100u;
@@ -563,8 +566,8 @@ cudaError_t launch_pages(Kern kern, int grid, int block, const Launch& L, Args..
 }
 
 // CTAs for `units` copy units of kUnitBytes at most.
-int copy_grid(long units, const Launch& L) {
-    return (int)std::max(1L, std::min(units, (long)L.num_sms * kCopyCtasPerSm));
+int copy_grid(long units, int per_sm, const Launch& L) {
+    return (int)std::max(1L, std::min(units, (long)L.num_sms * per_sm));
 }
 
 constexpr size_t kPart = 256;
@@ -603,7 +606,7 @@ size_t pages_workspace_bytes(int num_blocks, int B, int n) {
 cudaError_t launch_copy_pages(const CacheList& c, const int32_t* src, const int32_t* dst, int n,
                               unsigned* err, const Launch& L) {
     const long units = (long)n * c.first_unit[c.num_caches];
-    return launch_pages(copy_pages_kernel, copy_grid(units, L), kCopyThreads, L, c, src, dst, n,
+    return launch_pages(copy_pages_kernel, copy_grid(units, kCopyCtasPerSm, L), kCopyThreads, L, c, src, dst, n,
                         err);
 }
 
@@ -617,7 +620,7 @@ cudaError_t launch_fork(const CacheList& c, const PageTables& t, const int32_t* 
                                  reinterpret_cast<int*>(p + w.first), err);
     if (e != cudaSuccess) return e;
     const long units = (long)n * c.first_unit[c.num_caches];
-    return launch_pages(fork_apply_kernel, copy_grid(units, L), kCopyThreads, L, c, t, parents,
+    return launch_pages(fork_apply_kernel, copy_grid(units, kForkCtasPerSm, L), kCopyThreads, L, c, t, parents,
                         children, n, (const ForkPlan*)plan);
 }
 
