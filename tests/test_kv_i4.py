@@ -199,6 +199,25 @@ def test_write_and_read_exact(T, Hkv, D, page):
 
 
 @gpu
+@pytest.mark.parametrize("exponent", [0, -60, 50])
+def test_write_many_rows_exact(exponent):
+    """200,000 rows: every code at or next to a rounding boundary as the definition has it."""
+    T, Hkv, D, page = 25000, 4, 64, 50
+    rng, std = np.random.default_rng(exponent + 100), 2.0 ** exponent
+    k = synth.bf16_normal(1, (T, Hkv, D), std=std)
+    # rows of small integers times a power of two: quotients that are exact halves
+    v = _bf(rng.integers(-30, 31, (T, Hkv, D)) * std)
+    host = [np.zeros((T, Hkv, w), t) for w, t in
+            ((D // 2, np.uint8), (D // 2, np.uint8), (2, np.uint16), (2, np.uint16))]
+    dev = [to_dev(a) for a in host]
+    a8w8.paged_kv_write_i4(to_dev(k), to_dev(v), to_dev(np.arange(T, dtype=np.int32)), *dev, page)
+    for x, c, m in ((k, dev[0], dev[2]), (v, dev[1], dev[3])):
+        wc, wm = kv_i4.quant_rows(x)
+        assert np.array_equal(to_host(c), wc)
+        assert np.array_equal(kv_i4.bf16_to_f64(to_host(m)), kv_i4.bf16_to_f64(wm))
+
+
+@gpu
 def test_slots_out_of_range_are_flagged_and_skipped():
     Hkv, D, page, nblk = 2, 64, 16, 2
     k = synth.bf16_normal(5, (3, Hkv, D))
@@ -229,7 +248,8 @@ def _check(got, want, bound):
     """Within the derived bound plus the BF16 rounding of the result (half a step: 2^-8)."""
     g = kv_i4.bf16_to_f64(to_host(got))
     tol = bound + (np.abs(want) + bound) * 2.0 ** -8
-    assert np.array_equal(np.isnan(g), np.isnan(want))
+    odd = np.argwhere(np.isnan(g) != np.isnan(want))
+    assert not odd.size, f"NaN in one alone at {odd[:4].tolist()}"
     ok = np.isnan(want) | (np.abs(g - want) <= tol)
     worst = np.nanmax(np.abs(g - want) / np.maximum(tol, 1e-300))
     assert ok.all(), f"{(~ok).sum()} of {ok.size} elements off, worst {worst:.3g} of the bound"
@@ -340,6 +360,78 @@ def test_attention_bad_tables_and_nan_rows():
     _check(a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page), want,
            bound)
     assert a8w8.read_device_errors() == 0 and not np.isnan(want).any()
+
+
+@gpu
+@pytest.mark.parametrize("B,lo,hi,Hq,Hkv,D,page", [
+    (300, 0, 40, 6, 6, 64, 16),          # more requests than threads, many in one run
+    (140, 0, 700, 12, 3, 64, 32),
+    (1, 20011, 20011, 8, 1, 128, 24),    # one request in as many parts as there are runs
+    (2, 9000, 9001, 14, 2, 64, 128),
+    (5, 250, 258, 40, 8, 128, 129),      # tables just past what one CTA takes whole
+])
+def test_attention_runs(B, lo, hi, Hq, Hkv, D, page):
+    ctx = np.random.default_rng(B).integers(lo, hi + 1, B)
+    q, cache, bt, ctx = _case(B, ctx, Hq, Hkv, D, page)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page)
+    _check(got, want, bound)
+    assert not to_host(got)[ctx == 0].any()
+
+
+@gpu
+def test_attention_wide_tables_and_no_tokens_at_all():
+    """A table far wider than the contexts; then every request empty."""
+    page, Hq, Hkv, D = 16, 20, 4, 128
+    q, cache, bt, ctx = _case(11, [5, 0, 33, 17], Hq, Hkv, D, page)
+    wide = np.full((4, 4000), -1, np.int32)
+    wide[:, :bt.shape[1]] = bt
+    want, bound = kv_i4.attention(q, *cache, wide, ctx, page)
+    a8w8.read_device_errors()
+    dev = [to_dev(a) for a in (q, *cache, wide, ctx)]
+    _check(a8w8.paged_decode_attention_i4kv(*dev, page), want, bound)
+    dev[6].zero_()
+    assert not to_host(a8w8.paged_decode_attention_i4kv(*dev, page)).any()
+    dev[5] = dev[5][:, :4].contiguous()
+    assert not to_host(a8w8.paged_decode_attention_i4kv(*dev, page)).any()
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+def test_attention_queries_out_of_range():
+    """A query head with a NaN, an infinity or 2^118 and more gives NaN, its neighbours none of
+    it; the largest and smallest queries below that are exact."""
+    page, Hq, Hkv, D = 16, 8, 2, 64
+    q, cache, bt, ctx = _case(12, [40], Hq, Hkv, D, page)
+    q[0, 1, 3], q[0, 2, 0], q[0, 5, 63] = _bf(np.nan), _bf(np.inf), _bf(2.0 ** 118)
+    q[0, 3] = _bf(kv_i4.bf16_to_f64(q[0, 3]) * 2.0 ** -120)
+    q[0, 6] = 0
+    q[0, 7, 0] = _bf(2.0 ** 117)
+    q[0, 7, 1:] = 0
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page, scale=2.0 ** -118)
+    want[0, [1, 2, 5]] = np.nan
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page,
+                                           softmax_scale=2.0 ** -118)
+    _check(got, want, bound)
+
+
+@gpu
+def test_attention_calls_at_once_on_two_streams():
+    import torch
+    page, Hq, Hkv, D = 32, 40, 8, 128
+    cases, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for k in range(2):
+        q, cache, bt, ctx = _case(20 + k, [3000, 17, 900 + k], Hq, Hkv, D, page)
+        cases.append(([to_dev(a) for a in (q, *cache, bt, ctx)],
+                      kv_i4.attention(q, *cache, bt, ctx, page)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for (dev, _w), st in zip(cases, streams):
+            outs.append(a8w8.paged_decode_attention_i4kv(*dev, page, stream=st))
+        torch.cuda.synchronize()
+        for got, (_d, (want, bound)) in zip(outs, cases):
+            _check(got, want, bound)
 
 
 @gpu

@@ -320,6 +320,21 @@ def test_reserve_many_rows():
 
 
 @gpu
+@pytest.mark.parametrize("n", [1, 40, 1500])
+def test_reserve_far_more_than_the_pool(n):
+    page, B, M, N = 1, 2000, 5000, 37
+    s = State(n, B, M, N, page, (1,)).on_gpu()
+    rows = s.rng.permutation(B)[:n]
+    tokens = np.full(n, M)
+    tokens[n // 2:] = 30
+    a8w8.read_device_errors()
+    a8w8.paged_reserve(s.handle, s.g[0], s.g[2], _i32(rows), _i32(tokens))
+    err = pages.reserve(page, s.bt, s.ref, rows, tokens)
+    assert err == ({"PAGES"} if n > 1 else set()) and (n > 1 or s.ref.sum() == 30)
+    s.check(err)
+
+
+@gpu
 def test_free():
     page, B, M = 4, 20, 40
     s = State(5, B, M, 400, page)

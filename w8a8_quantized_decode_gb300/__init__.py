@@ -507,6 +507,14 @@ def _raw_stream(stream, dev):
     return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _kept(t, stream):
+    """A tensor allocated here for a call on `stream`: its memory is not handed out again while
+    that stream (when it is not the current one) may still use it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
     """Pointers and page count of a 4-bit cache: codes [slots, Hkv, D / 2] uint8 and (s, m)
     pairs [slots, Hkv, 2] bfloat16, in whole pages."""
@@ -547,8 +555,8 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        k = k_meta.new_empty((T, Hkv, D))
-        v = torch.empty_like(k)
+        k = _kept(k_meta.new_empty((T, Hkv, D)), stream)
+        v = _kept(torch.empty_like(k), stream)
     else:
         k, v = out
     _check(lib().paged_kv_read_i4(
@@ -578,8 +586,8 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     if ws is None:
         need = L.a8w8_attention_i4_workspace_bytes(B, Hq, Hkv, D, max_blocks * page_size)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    o = out if out is not None else torch.empty_like(q)
+            ws = _kept(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+    o = out if out is not None else _kept(torch.empty_like(q), stream)
     _check(L.paged_decode_attention_i4kv(
         _typed(q, torch.bfloat16, what, dev), *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
@@ -635,11 +643,11 @@ def pages_workspace_bytes(num_blocks: int, B: int, n: int) -> int:
     return lib().a8w8_pages_workspace_bytes(num_blocks, B, n)
 
 
-def _pages_ws(pool, B, n, ws, what, dev):
+def _pages_ws(pool, B, n, ws, what, dev, stream):
     torch = _torch()
     if ws is None:
-        ws = torch.empty(pages_workspace_bytes(pool.num_blocks, B, n), dtype=torch.uint8,
-                         device=pool.device)
+        ws = _kept(torch.empty(pages_workspace_bytes(pool.num_blocks, B, n), dtype=torch.uint8,
+                               device=pool.device), stream)
     return _typed(ws, torch.uint8, what, dev), ws.numel()
 
 
@@ -660,7 +668,7 @@ def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None
     _check(lib().paged_fork(*pool._args, pool.num_blocks, pool.page_size, bt, cl, rc, B,
                             max_blocks, _typed(parents, i32, what, dev, n),
                             _typed(children, i32, what, dev, n), n,
-                            *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
+                            *_pages_ws(pool, B, n, ws, what, dev, stream), _raw_stream(stream, dev)))
 
 
 def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=None):
@@ -672,7 +680,7 @@ def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=Non
     _check(lib().paged_reserve(bt, rc, B, max_blocks, pool.num_blocks, pool.page_size,
                                _typed(rows, i32, what, dev, n),
                                _typed(tokens, i32, what, dev, n), n,
-                               *_pages_ws(pool, B, n, ws, what, dev), _raw_stream(stream, dev)))
+                               *_pages_ws(pool, B, n, ws, what, dev, stream), _raw_stream(stream, dev)))
 
 
 def paged_free(pool, block_table, ctx_lens, refcount, rows, stream=None):
@@ -693,10 +701,10 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
     dev = pool._here(what)
     bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+        num_live = _kept(torch.empty(1, dtype=torch.int32, device=pool.device), stream)
     _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
                                _typed(num_live, torch.int32, what, dev, 1),
-                               *_pages_ws(pool, B, 0, ws, what, dev), _raw_stream(stream, dev)))
+                               *_pages_ws(pool, B, 0, ws, what, dev, stream), _raw_stream(stream, dev)))
     return num_live
 
 

@@ -366,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             }
-            // 2^e takes the largest |q| into [2^10, 2^11)
-            const int e = max(-107, min(126, 137 - (int)(__float_as_uint(top) >> 23)));
+            // 2^e takes the largest |q| into [2^10, 2^11) (16 2^e stays finite; the
+            // smallest BF16, 2^-133, is a normal FP16 then)
+            const int e = max(-107, min(123, 137 - (int)(__float_as_uint(top) >> 23)));
             const float up = __uint_as_float((unsigned)(127 + e) << 23);
             const float sc = p.scale * 1.4426950408889634f;
             float f = __uint_as_float((unsigned)(127 + 20 - e) << 23) * sc;
