@@ -494,3 +494,34 @@ def test_offsets_past_32_bits():
     gk, _ = a8w8.paged_kv_read_i4(*dev, to_dev(slots), page)
     x = kv_i4.dequant_rows(small[0][:T], small[2][:T]).astype(np.float32)
     assert np.array_equal(to_host(gk), _bf(x))
+
+
+@gpu
+def test_attention_full_server():
+    """64 requests of up to 16384 tokens over 4.1 GB of pages in random order; five of them
+    against the oracle, and a second call bit for bit."""
+    import torch
+    B, Hq, Hkv, D, page = 64, 40, 8, 128, 128
+    rng = np.random.default_rng(8)
+    ctx = rng.integers(64, 16385, B).astype(np.int32)
+    ctx[[3, 40]] = 16384, 0
+    bt, nblk = synth.paged_layout(8, np.maximum(ctx, 1), page, spare_blocks=3)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randint(0, 256, (nblk * page, Hkv, D // 2), dtype=torch.uint8, device="cuda",
+                            generator=g) for _ in range(2))
+    meta = []
+    for _ in range(2):
+        s = 0.25 + 0.2 * torch.rand((nblk * page, Hkv), device="cuda", generator=g)
+        meta.append(torch.stack((s, -7.5 * s), dim=-1).to(torch.bfloat16))
+    q = synth.bf16_normal(9, (B, Hq, D), std=1.5)
+    dev = [to_dev(q), kc, vc, *meta, to_dev(bt), to_dev(ctx)]
+    got = a8w8.paged_decode_attention_i4kv(*dev, page)
+    assert torch.equal(got, a8w8.paged_decode_attention_i4kv(*dev, page))
+    for b in (3, 40, int(ctx.argsort()[1]), 17, 63):
+        n = -(-int(ctx[b]) // page)
+        rows = (to_dev(bt[b, :n].astype(np.int64))[:, None] * page
+                + torch.arange(page, device="cuda")).reshape(-1)
+        own = [to_host(c[rows]) for c in (kc, vc, *meta)] if n else [to_host(c[:page]) for c in
+                                                                     (kc, vc, *meta)]
+        want, bound = kv_i4.attention(q[b:b + 1], *own, np.arange(max(n, 1))[None], ctx[b:b + 1], page)
+        _check(got[b:b + 1], want, bound)

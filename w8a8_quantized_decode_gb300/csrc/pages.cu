@@ -363,24 +363,18 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 __global__ void __launch_bounds__(kPlanThreads)
     reserve_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ rows,
-                   const int32_t* __restrict__ tokens, int n, int* need_ws, int* first_ws,
+                   const int32_t* __restrict__ tokens, int n, int2* need_ws, int* first_ws,
                    int* fresh, unsigned* err) {
     __shared__ int s[32];
-    __shared__ int s_need[kSharedList], s_first[kSharedRows];
+    __shared__ int2 s_need[kSharedList];      // pages needed, first rank
+    __shared__ int s_first[kSharedRows];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* need = n <= kSharedList ? s_need : need_ws;
+    int2* need = n <= kSharedList ? s_need : need_ws;
     int* first = t.B <= kSharedRows ? s_first : first_ws;
     const unsigned mask = first_mask(t.refcount, num_blocks);
     first_entries(first, t.B, n, [&](int i) { return rows[i] < t.B ? rows[i] : -1; });
-    // entries of the row that need a page: those of the first `entries` that
-    // are negative
-    auto empties = [&](const int32_t* row, int entries) {
-        int count = 0;
-        for (int j = lane; j < entries; j += 32) count += __ldcg(row + j) < 0;
-        return warp_sum_i(count);
-    };
     for (int i = warp; i < n; i += kPlanThreads / 32) {
         const int r = rows[i], tok = tokens[i];
         int count = 0;
@@ -389,23 +383,27 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (r >= t.B) bad = kErrRow;
             else if (first[r] != i) bad = kErrAlias;
             else if (tok < 0 || tok > t.max_blocks * t.page) bad = kErrCtx;
-            if (!bad) count = empties(t.block_table + (size_t)r * t.max_blocks, ceil_div(tok, t.page));
-            else if (lane == 0) set_error(err, bad);
+            if (!bad) {
+                const int32_t* row = t.block_table + (size_t)r * t.max_blocks;
+                for (int j = lane; j < ceil_div(tok, t.page); j += 32) count += __ldcg(row + j) < 0;
+                count = warp_sum_i(count);
+            } else if (lane == 0) {
+                set_error(err, bad);
+            }
         }
-        if (lane == 0) need[i] = count;
+        if (lane == 0) need[i].x = count;
     }
     __syncthreads();
-    // need[i] becomes the row's first rank (-1: nothing to give). A row is
-    // served if its last rank is below the number of free pages; a rank past
-    // the pool is held at its size, and one row's need too (1024 needs below
-    // 2^21 add up in 32 bits).
+    // A row is served if its last rank is below the number of free pages; a
+    // rank past the pool is held at its size, and one row's need too (1024
+    // needs below 2^21 add up in 32 bits).
     int want = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
         const int i = i0 + (int)threadIdx.x;
-        const int v = i < n ? min(need[i], num_blocks) : 0;
+        const int v = i < n ? min(need[i].x, num_blocks) : 0;
         int total;
         const int rank = min(want + block_exclusive(v, s, total), num_blocks);
-        if (i < n) need[i] = v == 0 ? -1 : rank;
+        if (i < n) need[i].y = rank;
         want = min(want + min(total, num_blocks), num_blocks);
     }
     __syncthreads();
@@ -413,15 +411,15 @@ __global__ void __launch_bounds__(kPlanThreads)
                                   [&](int rank, int page) { fresh[rank] = page; });
     __syncthreads();
     for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int base = need[i];
-        if (base < 0) continue;
-        int32_t* row = t.block_table + (size_t)rows[i] * t.max_blocks;
-        const int entries = ceil_div(tokens[i], t.page);
-        if (empties(row, entries) > found - base) {
+        const int2 want_at = need[i];
+        if (want_at.x == 0) continue;
+        if (want_at.x > found - want_at.y) {
             if (lane == 0) set_error(err, kErrPages);
             continue;
         }
-        int at = base;
+        int32_t* row = t.block_table + (size_t)rows[i] * t.max_blocks;
+        const int entries = ceil_div(tokens[i], t.page);
+        int at = want_at.y;
         for (int j0 = 0; j0 < entries; j0 += 32) {
             const int j = j0 + lane;
             const bool empty = j < entries && __ldcg(row + j) < 0;
@@ -573,7 +571,7 @@ int copy_grid(long units, int per_sm, const Launch& L) {
 constexpr size_t kPart = 256;
 size_t up(size_t x) { return (x + kPart - 1) / kPart * kPart; }
 
-// The workspace: plans [n], need [n], first [B], then three lists of
+// The workspace: plans [n], needs [n], first [B], then three lists of
 // num_blocks page numbers, and a head.
 struct PageWs {
     size_t plan, need, first, list, total;
@@ -582,7 +580,7 @@ PageWs page_ws(int num_blocks, int B, int n) {
     PageWs w;
     w.plan = kPart;
     w.need = w.plan + up((size_t)n * sizeof(ForkPlan));
-    w.first = w.need + up((size_t)n * 4);
+    w.first = w.need + up((size_t)n * 8);
     w.list = w.first + up((size_t)B * 4);
     w.total = w.list + 3 * up((size_t)num_blocks * 4);
     return w;
@@ -629,7 +627,7 @@ cudaError_t launch_reserve(const PageTables& t, int num_blocks, const int32_t* r
     const PageWs w = page_ws(num_blocks, t.B, n);
     unsigned char* p = static_cast<unsigned char*>(ws);
     return launch_pages(reserve_kernel, 1, kPlanThreads, L, t, num_blocks, rows, tokens, n,
-                        reinterpret_cast<int*>(p + w.need), reinterpret_cast<int*>(p + w.first),
+                        reinterpret_cast<int2*>(p + w.need), reinterpret_cast<int*>(p + w.first),
                         reinterpret_cast<int*>(p + w.list), err);
 }
 
