@@ -498,8 +498,8 @@ def test_offsets_past_32_bits():
 
 @gpu
 def test_attention_full_server():
-    """64 requests of up to 16384 tokens over 4.1 GB of pages in random order; five of them
-    against the oracle, and a second call bit for bit."""
+    """64 requests of up to 16384 tokens (some 570 MB of rows) over pages in random order; five of
+    them against the oracle, and a second call bit for bit."""
     import torch
     B, Hq, Hkv, D, page = 64, 40, 8, 128, 128
     rng = np.random.default_rng(8)

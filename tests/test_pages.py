@@ -469,6 +469,35 @@ def test_captured_on_another_stream_with_shared_workspace():
 
 
 @gpu
+def test_copy_and_compact_all_layers():
+    """The 160 caches of a 40-layer 4-bit pool: 96 page copies, then a compaction."""
+    import torch
+    L, N, page, Hkv, D = 40, 256, 128, 8, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (2 * L, N, page, Hkv, D // 2), dtype=torch.uint8, device="cuda",
+                          generator=g)
+    meta = torch.randint(-2 ** 15, 2 ** 15, (2 * L, N, page, Hkv, 2), dtype=torch.int16,
+                         device="cuda", generator=g)
+    pool = a8w8.PagePool([c[i] for i in range(2 * L) for c in (codes, meta)], N, page)
+    p = torch.randperm(N, device="cuda", generator=g).to(torch.int32)
+    src, dst = p[:96].contiguous(), p[96:192].contiguous()
+    want = codes.clone(), meta.clone()
+    a8w8.read_device_errors()
+    a8w8.paged_copy_pages(pool, src, dst)
+    for c, w in zip((codes, meta), want):
+        w[:, dst.long()] = w[:, src.long()]
+        assert torch.equal(c, w)
+    ref = torch.zeros(N, dtype=torch.int32, device="cuda")
+    bt = p[:100].reshape(10, 10).clone()
+    ref[p[:100].long()] = 1
+    live = a8w8.paged_compact(pool, bt, ref)
+    assert int(live) == 100 and int(ref[:100].sum()) == 100 and int(bt.max()) == 99
+    for c, w in zip((codes, meta), want):
+        assert torch.equal(c[:, bt.reshape(-1).long()], w[:, p[:100].long()])
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
 def test_pages_past_4_gib():
     import torch
     page_bytes, N = 1 << 20, 4200

@@ -557,13 +557,14 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     if out is None:
         k = _kept(k_meta.new_empty((T, Hkv, D)), stream)
         v = _kept(torch.empty_like(k), stream)
+        kv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
+        kv = (_typed(k, torch.bfloat16, what, dev, T * Hkv * D),
+              _typed(v, torch.bfloat16, what, dev, T * Hkv * D))
     _check(lib().paged_kv_read_i4(
         *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, T), T, Hkv, D,
-        _typed(k, torch.bfloat16, what, dev, T * Hkv * D),
-        _typed(v, torch.bfloat16, what, dev, T * Hkv * D),
-        _raw_stream(stream, dev)))
+        *kv, _raw_stream(stream, dev)))
     return k, v
 
 
@@ -587,12 +588,14 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         need = L.a8w8_attention_i4_workspace_bytes(B, Hq, Hkv, D, max_blocks * page_size)
         if need:
             ws = _kept(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
-    o = out if out is not None else _kept(torch.empty_like(q), stream)
+    qp = _typed(q, torch.bfloat16, what, dev)
+    o = _kept(torch.empty_like(q), stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
-        _typed(q, torch.bfloat16, what, dev), *ptrs,
+        qp, *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
         _typed(ctx_lens, torch.int32, what, dev, B), B, Hq, Hkv, D, page_size, max_blocks,
-        num_blocks, scale, _typed(o, torch.bfloat16, what, dev, B * Hq * D),
+        num_blocks, scale,
+        o.data_ptr() if out is None else _typed(o, torch.bfloat16, what, dev, B * Hq * D),
         None if ws is None else _typed(ws, torch.uint8, what, dev), 0 if ws is None else ws.numel(),
         _raw_stream(stream, dev)))
     return o

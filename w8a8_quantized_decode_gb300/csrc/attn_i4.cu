@@ -14,11 +14,12 @@
 // (mma.sync m16n8k16 f16, 600 TFLOP/s here: 64 of the 190 cycles) and codes
 // become operands without a conversion: an integer 0..15 in the lowest
 // mantissa bits of an FP16 is the subnormal c 2^-24, in the next four bits c
-// 2^-20, both exact, so a word of eight codes is four operand registers after
-// four masks and a shift. (mma.sync on e4m3 bytes, where a nibble is exact
-// too, compiles to conversions and f16 instructions on sm_103a: 1131
-// instructions per tile and head against 440 here, 221 us against XXX at batch
-// 64.) The power of two is taken back in the other operand or the result:
+// 2^-20, a whole byte c + 16 c' likewise, all exact, so a word of eight codes
+// is four operand registers after four or five integer instructions.
+// (mma.sync on e4m3 bytes, where a nibble is exact too, compiles to
+// conversions and f16 instructions on sm_103a: 1131 instructions per tile of
+// 32 tokens, 400 here.) The powers of two are taken back in the other operand
+// or the result:
 //   * q, scaled per head by a power of two to a maximum in [2^10, 2^11) (times
 //     16 beside the low nibbles): the eight significant bits of a BF16 are
 //     exact in FP16 down to 2^-35 of the head's largest |q|. Tokens are the
@@ -26,18 +27,34 @@
 //     instruction per 16 tokens and 16 dimensions.
 //   * the weights p_t s_t, rounded to FP16: 2^-11 relative, beside the 2^-8 of
 //     the BF16 result. ref keeps the largest between 2^10 and 2^15, so that
-//     what FP16 cannot hold lies 2^-35 below it. One 8 x 8 transpose
+//     what FP16 cannot hold lies 2^-34 below it. One 8 x 8 transpose
 //     (movmatrix) per 8 tokens takes them from the score's layout into the
 //     operand's.
 // For V the contraction runs over tokens: a lane reads four tokens' bytes for
 // its 16 dimensions per 16 tokens and pairs the halves of two words by one
-// permute each.
+// permute each; of a pair of dimensions it sums the low nibbles and the whole
+// bytes, whose difference is 16 times the high nibbles' sum.
 //
-// Work is cut into tiles of 32 tokens of one (request, KV head), numbered
-// through all requests; a CTA takes an equal run of them, whatever the
-// contexts, and its four warps take the run's tiles in turn, each with a
-// private cp.async ring (no CTA barrier inside a run). Runs that end inside a
-// (request, KV head) leave their (ref, sum, o) to a second kernel.
+// Work is cut into tiles of 32 tokens of a request, numbered through all
+// requests. A run is an equal share of the tiles, whatever the contexts; it
+// is taken by the CTAs of all KV heads, a warp per head and four heads to a
+// CTA where their number allows it, so that the rows of one token, which lie
+// side by side, are read together (heads one after the other: 27 % more bytes
+// from HBM, and 206 us against 140 for 64 requests of up to 16384 tokens). A
+// warp copies its tiles with cp.async into a private ring, without a barrier.
+// Runs that end inside a request leave (ref, sum, o) to a second kernel.
+// Three CTAs of four warps fill an SM at 168 registers; four at 128 were
+// slower (117 against 114 us, spills), and so were deeper rings (3 or 4
+// stages: 113, 117), more and shorter runs (117 at twice as many), the next
+// tile's scores ahead of this one's weights (114), and barriers that keep an
+// SM's CTAs in step (116 to 129).
+//
+// Measured (40 query and 8 KV heads of 128, pages of 128 tokens): 64 requests
+// of 64 to 16384 tokens, 574 MB, 106 us (5.4 TB/s, 0.81 of the copy rate; the
+// copies alone take 94, the arithmetic alone about 109, and neither the
+// integer pipe, 49 % busy, nor HBM, 70 %, is full: their waits do not hide
+// each other entirely with three warps per scheduler); 16 requests of 64 to
+// 4096 tokens, 37 MB, 16 us; one of 256 tokens 3 us.
 #include <limits.h>
 
 #include <algorithm>

@@ -15,10 +15,13 @@
 // Both kernels are bound by HBM: a (token, head) pair of rows is 4 D bytes of
 // BF16 and D + 8 of cache. What stands against it is the issue rate of the
 // per-row work (s and its reciprocal, the reduction), which all lanes of a row
-// do: a row belongs to D / 16 lanes of 16 values, half the lanes that 16-byte
-// loads would need and twice the values per row's work (write of 16384 tokens
-// of 8 heads: 294 warp instructions per 16 rows' values with D / 8 lanes, XXX
-// with D / 16). K and V of the row are in flight together.
+// do: a row belongs to D / 16 lanes of 16 values in two 16-byte pieces, half
+// the lanes that one piece each would take (95 warp instructions per pair of
+// rows of 128 values instead of 147), and the pieces of one load or store lie
+// side by side (a lane's two pieces together made half sectors: read 22.8
+// against 15.6 us). K and V of the row are in flight together. 16384 tokens of
+// 8 heads of 128: write 17 us and read 14 us in turn, 170 MB in 31 us (5.4
+// TB/s, 0.81 of the copy rate).
 #include "kernels.cuh"
 
 namespace a8w8 {

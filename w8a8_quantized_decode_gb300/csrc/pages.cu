@@ -8,11 +8,15 @@
 // order of the request lists, so a call's result is a function of its inputs.
 //
 // The data moves are bound by HBM (each byte read and written once); the
-// bookkeeping is a few passes over the counts and tables. fork and compact run
-// a one-CTA plan that decides every move (the decisions are ordered: ranks
-// among the free pages), then one kernel that carries the moves out over all
-// SMs. The plan starts the second kernel early by programmatic dependent
-// launch, so that only its wait remains between them.
+// bookkeeping is a few passes over the counts and tables, latency alone. fork
+// and compact run a one-CTA plan that decides every move (the decisions are
+// ordered: ranks among the free pages), then one kernel that carries the moves
+// out over all SMs. The plan starts the second kernel early by programmatic
+// dependent launch, so that only its wait remains between them.
+// Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page): 96
+// copies 164 us (6.5 TB/s read and written, 0.98 of the copy rate);
+// compaction of some 150 of 260 live pages 251 us; 64 forks of 16 parents,
+// half a page each, 48 us after a plan of 8.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -217,8 +221,8 @@ struct ForkPlan {
 };
 
 // Lists of up to this many entries, and tables of up to this many rows, are
-// planned in shared memory (a round trip to L2 less at each of the plan's
-// steps: 5.6 against 9.2 us for 64 forks); longer ones in the workspace.
+// planned in shared memory, a round trip to L2 less at each of the plan's
+// steps (fork of 64: 7.8 against 9.2 us); longer ones in the workspace.
 constexpr int kSharedList = 1024, kSharedRows = 2048;
 
 // The lowest entry of the list that names each row, for the rows named by
