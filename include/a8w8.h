@@ -9,7 +9,9 @@
  * as a replayable CUDA graph (optionally decoding on the device, greedily or
  * with sampling inside the graph); also a prefill chunk, the
  * prompt-to-first-token step, sampling beyond greedy, and two variants: the
- * INT8 KV cache with FP32 row scales and the BF16 (unquantised) layer.
+ * INT8 KV cache with FP32 row scales and the BF16 (unquantised) layer; beside
+ * them a 4-bit KV cache with its decode attention, and the pages of a cache
+ * copied, forked, reserved, freed and compacted on the device.
  *
  * Sources, cited by page title and section:
  *   [LIB-810] "perf(qwen3-a8w8): optimize decode scheduling and data paths"
