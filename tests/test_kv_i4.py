@@ -309,8 +309,8 @@ def test_attention_groups(G):
 
 
 @gpu
-@pytest.mark.parametrize("what", ["peaked", "tiny v", "mixed v", "zero s", "huge v", "rising",
-                                  "scale 0", "negative scale"])
+@pytest.mark.parametrize("what", ["peaked", "tiny v", "tiniest v", "mixed v", "zero s", "huge v",
+                                  "constant v", "rising", "falling", "scale 0", "negative scale"])
 def test_attention_ranges(what):
     """Weights, scales and maxima over wide ranges: one token that takes all, V rows of tiny,
     mixed (10 decades) or zero s, scores that rise along the context."""
@@ -318,7 +318,7 @@ def test_attention_ranges(what):
     rng = np.random.default_rng(3)
     gain = 30.0 if what == "peaked" else 1.5
     sc = {"scale 0": 0.0, "negative scale": -0.2}.get(what)
-    v_scale = {"tiny v": 1e-9, "huge v": 1e30}.get(what, 0.35)
+    v_scale = {"tiny v": 1e-9, "tiniest v": 2.0 ** -70, "huge v": 1e30}.get(what, 0.35)
     q, cache, bt, ctx = _case(9, [n, 1, 77], 10, 2, 128, page, gain=gain, v_scale=v_scale)
     kc, vc, km, vm = cache
     if what == "mixed v":
@@ -327,10 +327,14 @@ def test_attention_ranges(what):
     if what == "zero s":
         vm[::2, :, 0] = 0                                  # constant rows, every other slot
         km[1::3, :, 0] = 0
-    if what == "rising":
-        for t in range(n):                                 # K grows with the position
+    if what == "constant v":                               # s = 0 throughout, up to 2^36
+        vm[..., 0] = 0
+        vm[..., 1] = _bf(rng.choice([-1.0, 1.0], vm.shape[:2]) * 2.0 ** rng.integers(-60, 37, vm.shape[:2]))
+    if what in ("rising", "falling"):
+        for t in range(n):                                 # K grows (falls) with the position
             slot = bt[0][t // page] * page + t % page
-            km[slot] = _bf(kv_i4.bf16_to_f64(km[slot]) * (t / 60.0))
+            f = t / 60.0 if what == "rising" else (n - t) / 60.0
+            km[slot] = _bf(kv_i4.bf16_to_f64(km[slot]) * f)
     cache = (kc, vc, km, vm)
     want, bound = kv_i4.attention(q, *cache, bt, ctx, page, scale=sc)
     got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page,

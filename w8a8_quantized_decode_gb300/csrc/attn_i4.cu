@@ -115,9 +115,13 @@ __device__ __forceinline__ void cp4z(unsigned s, const void* g, unsigned n) {
 __device__ __forceinline__ float bf_lo(unsigned w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(unsigned w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Tiles of request b: none where the context is out of range.
+// Tokens of request b: none where the context is out of range. Contexts and
+// tables are read by plain loads, which see what the kernels before this one
+// wrote (the read-only path need not, as such a kernel may still run when this
+// one starts), and mostly from L1: a table entry from L2 comes back behind the
+// copies under way, 129 us against 109 for 64 long requests.
 __device__ __forceinline__ int tokens_of(const AttnI4Params& p, int b) {
-    const int c = __ldg(p.ctx_lens + b);
+    const int c = p.ctx_lens[b];
     return c < 0 || c > p.max_blocks * p.page ? 0 : c;
 }
 __device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kTile - 1) / kTile; }
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ unsigned s_scan[kWarps];
     __shared__ unsigned s_first;
-    __shared__ int s_b;
+    __shared__ int s_b, s_tokens;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv;
@@ -232,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int per = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
         unsigned mine = 0;
+        int last = 0;                           // tokens of the thread's last request
         for (int i = b0; i < b1; ++i) {
-            const int n = tokens_of(p, i);
+            const int n = last = tokens_of(p, i);
             if (blockIdx.x == 0 && n == 0) {
                 plan[i] = make_int2(-1, -1);
                 if (p.ctx_lens[i] != 0) set_error(p.err, 0x4u);
@@ -249,18 +254,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const unsigned x0 = runs.start(r), x1 = runs.start(r + 1);
         if (mine > 0 && x0 >= before && x0 - before < mine) {
             unsigned at = before;
-            int i = b0;
-            for (;; ++i) {
-                const unsigned n = tiles_of(tokens_of(p, i));
-                if (x0 - at < n) break;
-                at += n;
-            }
+            int i = b0, n = last;
+            if (per > 1)
+                for (; n = tokens_of(p, i), x0 - at >= (unsigned)tiles_of(n); ++i) at += tiles_of(n);
             s_b = i;
             s_first = at;
+            s_tokens = n;
         }
         __syncthreads();
         b = s_b;
-        tokens = tokens_of(p, b);
+        tokens = s_tokens;
         j = x0 - s_first;
         left = x1 - x0;
         // the requests that begin in this run: which runs hold their parts
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 ++q;
                 r -= p.page;
             }
-            blk = __ldg(table + q);
+            blk = table[q];
             in_page = (int)r;
         }
     };
@@ -471,10 +474,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
             // ---- weights -----------------------------------------------------------
             // ref is raised only where the tile's largest p times its largest s
-            // passes 2^15, which bounds every weight (s counts 2^-75 at least, so
-            // that p stays below 2^90); the raise takes the largest p s to 2^10
+            // passes 2^15, which bounds every weight; the raise takes the largest
+            // p s to 2^10. s counts 2^-45 here and 2^-50 there at least, so that p
+            // stays below 2^60 where rows are constant (s = 0): below s = 2^-74
+            // the weights leave FP16's normal range, and sums of p m overflow
+            // only for constant rows past 2^40
             float p0[4], p1[4];
-            float bigp = 0.0f, bigs = 2.7e-23f;
+            float bigp = 0.0f, bigs = 0x1p-45f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 p0[k] = ex2(y0[k]);
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float z0 = kNoRef, z1 = kNoRef;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float ls = log2f(fmaxf(fabsf(sv[k]), 8.3e-25f));
+                    const float ls = log2f(fmaxf(fabsf(sv[k]), 0x1p-50f));
                     z0 = fmaxf(z0, y0[k] + ls);
                     z1 = fmaxf(z1, y1[k] + ls);
                 }

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kI4Threads)
     const unsigned row = blockIdx.x * (kI4Threads / LPR) + threadIdx.x / LPR;
     const int j = threadIdx.x % LPR;
     const unsigned t = row / (unsigned)Hkv, hh = row - t * Hkv;
-    long slot = t < (unsigned)T ? (long)__ldg(slot_mapping + t) : -1;
+    long slot = t < (unsigned)T ? (long)__ldcg(slot_mapping + t) : -1;
     int4 kr[2], vr[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kI4Threads)
     const int j = threadIdx.x % LPR;
     const unsigned t = row / (unsigned)Hkv, hh = row - t * Hkv;
     if (t >= (unsigned)T) return;
-    const long slot = __ldg(slot_mapping + t);
+    const long slot = __ldcg(slot_mapping + t);
     int4 ko[2], vo[2];
     ko[0] = ko[1] = vo[0] = vo[1] = make_int4(0, 0, 0, 0);
     if (slot >= num_slots) {

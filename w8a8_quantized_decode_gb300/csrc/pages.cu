@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kCopyThreads)
         for (int j = threadIdx.x; j < t.max_blocks; j += kCopyThreads) {
             int e = -1;
             if (j < f.full) {
-                e = from[j];
+                // from L2: a line of the table may hold rows that other SMs write
+                e = __ldcg(from + j);
                 atomicAdd(t.refcount + e, 1);
             } else if (j == f.full && f.part > 0) {
                 e = f.fresh;
