@@ -499,12 +499,21 @@ def _typed(t, dtype, what, dev, numel=None):
 
 
 def _device() -> int:
-    return _torch().cuda.current_device()
+    """Index of the current CUDA device."""
+    return _torch()._C._cuda_getDevice()
 
 
 def _raw_stream(stream, dev):
     """The cudaStream_t of `stream`, or of the current stream of device dev."""
     return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _new_rows(a, b, c):
+    """An uninitialised bf16 tensor [a, b, c] on the current CUDA device, by the allocation entry
+    that torch's own generated code uses: one call without the dispatcher (a call of an operator
+    costs the host several microseconds between kernel launches)."""
+    torch = _torch()
+    return torch._C._dynamo.guards._empty_strided_cuda((a, b, c), (b * c, c, 1), torch.bfloat16)
 
 
 def _kept(t, stream):
@@ -519,6 +528,7 @@ def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
     """Pointers and page count of a 4-bit cache: codes [slots, Hkv, D / 2] uint8 and (s, m)
     pairs [slots, Hkv, 2] bfloat16, in whole pages."""
     torch = _torch()
+    u8, bf = torch.uint8, torch.bfloat16
     pairs = k_meta.numel()
     slots = pairs // (2 * Hkv)
     codes = slots * Hkv * D // 2
@@ -526,9 +536,14 @@ def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
             v_meta.numel() != pairs or k_codes.numel() != codes or v_codes.numel() != codes:
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: codes [slots, {Hkv}, {D // 2}] and meta "
                         f"[slots, {Hkv}, 2] of whole pages of {page_size} tokens expected")
-    u8, bf = torch.uint8, torch.bfloat16
-    return (_typed(k_codes, u8, what, dev), _typed(v_codes, u8, what, dev),
-            _typed(k_meta, bf, what, dev), _typed(v_meta, bf, what, dev)), slots // page_size
+    if not (k_codes.dtype is v_codes.dtype is u8 and k_meta.dtype is v_meta.dtype is bf
+            and k_codes.get_device() == v_codes.get_device() == dev
+            and k_meta.get_device() == v_meta.get_device() == dev
+            and k_codes.is_contiguous() and v_codes.is_contiguous()
+            and k_meta.is_contiguous() and v_meta.is_contiguous()):
+        _refuse(what, f"{u8} (codes), {bf} (meta)", None)
+    return (k_codes.data_ptr(), v_codes.data_ptr(), k_meta.data_ptr(),
+            v_meta.data_ptr()), slots // page_size
 
 
 def paged_kv_write_i4(k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta, page_size,
@@ -555,8 +570,7 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        k = _kept(k_meta.new_empty((T, Hkv, D)), stream)
-        v = _kept(torch.empty_like(k), stream)
+        k, v = _kept(_new_rows(T, Hkv, D), stream), _kept(_new_rows(T, Hkv, D), stream)
         kv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -589,7 +603,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         if need:
             ws = _kept(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
     qp = _typed(q, torch.bfloat16, what, dev)
-    o = _kept(torch.empty_like(q), stream) if out is None else out
+    o = _kept(_new_rows(B, Hq, D), stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
         qp, *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
