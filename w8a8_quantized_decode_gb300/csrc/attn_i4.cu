@@ -353,10 +353,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int s = 0; s < kStages; ++s) lookup(j + tw + s * TW, blk[s], in_page[s]);
     };
     int4 raw[KW];                           // the query head's values, as loaded
+    // The first tile is copied ahead, the ring's others once the query heads
+    // stand ready: every warp's first tile comes before any warp's second.
     auto copy_first = [&] {
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) fetch(j + tw + s * TW, s, blk[s], in_page[s]);
-        lookup(j + tw + kStages * TW, nblk, nin);
+        fetch(j + tw, 0, blk[0], in_page[0]);
         const bf16* q = p.q + ((size_t)b * p.Hq + (size_t)h * G + (g < G ? g : 0)) * D + t * (D / 4);
 #pragma unroll
         for (int w = 0; w < KW; ++w) raw[w] = g < G ? ld_cg_v4(q + 8 * w) : make_int4(0, 0, 0, 0);
@@ -420,6 +420,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         float ref0 = 0.0f, ref1 = 0.0f, l0 = 0.0f, l1 = 0.0f, om0 = 0.0f, om1 = 0.0f;
         bool fresh = true;                      // no tile yet
 
+#pragma unroll
+        for (int s = 1; s < kStages; ++s) fetch(j + tw + s * TW, s, blk[s], in_page[s]);
+        lookup(j + tw + kStages * TW, nblk, nin);
         int st = 0;
         for (int i = j + tw; i < j1; i += TW) {
             cp_async_wait_group<kStages - 1>();
