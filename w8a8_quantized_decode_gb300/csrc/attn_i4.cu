@@ -72,6 +72,7 @@ constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 152 * kCtasPerSm;
 constexpr int kMinTiles = 4;         // tiles per run at least
 constexpr int kCombineThreads = 128;
+constexpr int kJoin = 2;             // parts a warp of the second kernel loads at once
 constexpr float kNoRef = -1e30f;     // ref of a warp that has seen no token
 
 constexpr int code_bytes(int D) { return kTile * D / 2; }
@@ -696,8 +697,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 // Joins the parts of each (request, query head) that several CTAs share, and
 // writes the zeros of requests without tokens. One CTA per query head and
-// request; its warps take the parts in turn, each with a running ref, so that
-// a part is one round of loads, and then join theirs.
+// request; its warps take the parts two at a time, each
+// with a running ref, and then join theirs.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const AttnI4Params p) {
     constexpr int NW = kCombineThreads / 32, EL = D / 32;
@@ -720,17 +721,30 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
     float ref = kNoRef, L = 0.0f, o[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) o[e] = 0.0f;
-    for (int c = c0 + warp; c <= c1; c += NW) {
-        const float* po = part.o(2u * (c * p.Hkv + h) + (c == c0 ? plan.x & 1 : 0), hd);
-        const float2 rl = __ldcg(reinterpret_cast<const float2*>(po + D));
-        float v[EL];
+    for (int c = c0 + warp; c <= c1; c += kJoin * NW) {
+        float2 rl[kJoin];
+        float v[kJoin][EL];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = __ldcg(po + lane + 32 * e);
-        const float up = fmaxf(ref, rl.x), f = ex2(ref - up), g = ex2(rl.x - up);
-        ref = up;
-        L = __fmaf_rn(L, f, rl.y * g);
+        for (int k = 0; k < kJoin; ++k) {
+            const int ck = c + k * NW;
+            rl[k] = make_float2(kNoRef, 0.0f);
 #pragma unroll
-        for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(o[e], f, v[e] * g);
+            for (int e = 0; e < EL; ++e) v[k][e] = 0.0f;
+            if (ck <= c1) {
+                const float* po = part.o(2u * (ck * p.Hkv + h) + (ck == c0 ? plan.x & 1 : 0), hd);
+                rl[k] = __ldcg(reinterpret_cast<const float2*>(po + D));
+#pragma unroll
+                for (int e = 0; e < EL; ++e) v[k][e] = __ldcg(po + lane + 32 * e);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+            const float up = fmaxf(ref, rl[k].x), f = ex2(ref - up), g = ex2(rl[k].x - up);
+            ref = up;
+            L = __fmaf_rn(L, f, rl[k].y * g);
+#pragma unroll
+            for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(o[e], f, v[k][e] * g);
+        }
     }
 #pragma unroll
     for (int e = 0; e < EL; ++e) so[warp][lane + 32 * e] = o[e];
