@@ -16,7 +16,8 @@
 // Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page): 96
 // copies 164 us (6.5 TB/s read and written, 0.98 of the copy rate);
 // compaction of some 150 of 260 live pages 251 us; 64 forks of 16 parents,
-// half a page each, 48 us after a plan of 8.
+// half a page each, 45 us after a plan of 5 (their 225 MB take 34 at the copy
+// rate).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -27,10 +28,10 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr unsigned kUnitBytes = 16384;   // a copy unit: 4 vectors of 16 bytes per thread
-// CTAs per SM: 4 for whole pages (copy 172 us for 1.07 GB, 180 at 6 or 8); 8
-// for forks, whose partial pages leave some of a CTA's units empty (fork of 64
-// children 68 us, 75 at 4).
-constexpr int kCopyCtasPerSm = 4, kForkCtasPerSm = 8;
+// CTAs per SM: 4 for whole pages (copy 172 us for 1.07 GB, 180 at 6 or 8); 6
+// for forks, whose partial pages leave some of a CTA's items empty (fork of 64
+// children and reserve 60.2 us, 61.6 at 8, 64.1 at 4).
+constexpr int kCopyCtasPerSm = 4, kForkCtasPerSm = 6;
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kErrBlock = 0x2u, kErrCtx = 0x4u, kErrRow = 0x40u, kErrPages = 0x80u,
                    kErrAlias = 0x100u;
@@ -72,17 +73,12 @@ __device__ __forceinline__ int unit_cache(const CacheList& c, unsigned u) {
     return lo;
 }
 
-// Copies unit u of page `from` to page `to`, of the first tokens / page_size
-// of the page when `tokens` is below page_size.
-__device__ __forceinline__ void copy_page_unit(const CacheList& c, unsigned u, int from, int to,
-                                               int tokens, int page_size) {
+// Copies unit u of page `from` to page `to`.
+__device__ __forceinline__ void copy_page_unit(const CacheList& c, unsigned u, int from, int to) {
     const int k = unit_cache(c, u);
-    const unsigned pb = c.page_bytes[k];
-    const unsigned used = tokens >= page_size ? pb : pb / (unsigned)page_size * (unsigned)tokens;
-    const unsigned off = (u - c.first_unit[k]) * kUnitBytes;
-    if (off >= used) return;
+    const unsigned pb = c.page_bytes[k], off = (u - c.first_unit[k]) * kUnitBytes;
     copy_unit(c.base[k] + (size_t)to * pb + off, c.base[k] + (size_t)from * pb + off,
-              min(kUnitBytes, used - off));
+              min(kUnitBytes, pb - off));
 }
 
 // Exclusive prefix sum of v over the CTA's kPlanThreads threads; the total in
@@ -203,7 +199,7 @@ __global__ void __launch_bounds__(kCopyThreads)
         for (long u = a; u < b; ++u) {
             const int i = (int)(u / U) - p0;
             if (sbad[i]) continue;
-            copy_page_unit(c, (unsigned)(u - (long)(p0 + i) * U), sfrom[i], sto[i], 1, 1);
+            copy_page_unit(c, (unsigned)(u - (long)(p0 + i) * U), sfrom[i], sto[i]);
         }
         __syncthreads();   // the batch is read until here
     }
@@ -318,15 +314,26 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
 }
 
-// The (unit, fork) pairs dealt out in turn, forks fastest: children of one
-// parent read its page from L2 together, and forks that use little of their
-// page leave no CTA idle. The tables and counts of fork i by CTA i mod grid.
+// Items (cache, chunk of its page, fork) dealt out in turn, forks fastest:
+// children of one parent read its page from L2 together, and forks that use
+// little of their page leave no CTA idle. Every cache counts as many chunks as
+// the largest page has (a power of two, 1 << shift): an empty item costs a few
+// instructions, where finding the cache of a unit costs every thread a search
+// through the list (159 warp instructions per unit and 53 us for 64 forks of a
+// 40-layer pool, 46 here). The tables and counts of fork i by CTA i mod grid.
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const __grid_constant__ CacheList c, const PageTables t,
                       const int32_t* __restrict__ parents, const int32_t* __restrict__ children,
-                      int n, const ForkPlan* plan) {
+                      int n, const ForkPlan* plan, int shift) {
+    __shared__ unsigned char* s_base[kMaxCaches];
+    __shared__ unsigned s_token[kMaxCaches];    // bytes of a token
+    for (int k = threadIdx.x; k < c.num_caches; k += kCopyThreads) {
+        s_base[k] = c.base[k];
+        s_token[k] = c.page_bytes[k] / (unsigned)t.page;
+    }
     pdl_wait();
     pdl_trigger();
+    __syncthreads();
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const ForkPlan f = plan[i];
         if (f.full < 0) continue;
@@ -346,13 +353,20 @@ __global__ void __launch_bounds__(kCopyThreads)
         }
         if (threadIdx.x == 0) t.ctx_lens[children[i]] = f.full * t.page + f.part;
     }
-    const unsigned U = c.first_unit[c.num_caches];
+    const unsigned items = (unsigned)c.num_caches << shift;
     const int du = gridDim.x / n, di = gridDim.x % n;
     unsigned u = blockIdx.x / n;
     int i = blockIdx.x % n;
-    while (u < U) {
+    while (u < items) {
         const ForkPlan f = plan[i];
-        if (f.src >= 0) copy_page_unit(c, u, f.src, f.fresh, f.part, t.page);
+        const unsigned tb = s_token[u >> shift], off = (u & ((1u << shift) - 1u)) * kUnitBytes;
+        const unsigned used = f.src >= 0 ? tb * (unsigned)f.part : 0u;
+        if (off < used) {
+            const unsigned pb = tb * (unsigned)t.page;
+            unsigned char* base = s_base[u >> shift] + off;
+            copy_unit(base + (size_t)f.fresh * pb, base + (size_t)f.src * pb,
+                      min(kUnitBytes, used - off));
+        }
         u += du;
         i += di;
         if (i >= n) {
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     const long total = (long)moves * U;
     for (long u = blockIdx.x; u < total; u += gridDim.x) {
         const int k = (int)(u / U);
-        copy_page_unit(c, (unsigned)(u - (long)k * U), from[k], to[k], 1, 1);
+        copy_page_unit(c, (unsigned)(u - (long)k * U), from[k], to[k]);
     }
 }
 
@@ -609,8 +623,8 @@ size_t pages_workspace_bytes(int num_blocks, int B, int n) {
 cudaError_t launch_copy_pages(const CacheList& c, const int32_t* src, const int32_t* dst, int n,
                               unsigned* err, const Launch& L) {
     const long units = (long)n * c.first_unit[c.num_caches];
-    return launch_pages(copy_pages_kernel, copy_grid(units, kCopyCtasPerSm, L), kCopyThreads, L, c, src, dst, n,
-                        err);
+    return launch_pages(copy_pages_kernel, copy_grid(units, kCopyCtasPerSm, L), kCopyThreads, L, c,
+                        src, dst, n, err);
 }
 
 cudaError_t launch_fork(const CacheList& c, const PageTables& t, const int32_t* parents,
@@ -622,9 +636,13 @@ cudaError_t launch_fork(const CacheList& c, const PageTables& t, const int32_t* 
                                  children, n, plan, reinterpret_cast<int*>(p + w.need),
                                  reinterpret_cast<int*>(p + w.first), err);
     if (e != cudaSuccess) return e;
-    const long units = (long)n * c.first_unit[c.num_caches];
-    return launch_pages(fork_apply_kernel, copy_grid(units, kForkCtasPerSm, L), kCopyThreads, L, c, t, parents,
-                        children, n, (const ForkPlan*)plan);
+    unsigned largest = 0;
+    for (int k = 0; k < c.num_caches; ++k) largest = std::max(largest, c.page_bytes[k]);
+    int shift = 0;
+    while (((size_t)kUnitBytes << shift) < largest) ++shift;
+    const long items = ((long)n * c.num_caches) << shift;
+    return launch_pages(fork_apply_kernel, copy_grid(items, kForkCtasPerSm, L), kCopyThreads, L, c,
+                        t, parents, children, n, (const ForkPlan*)plan, shift);
 }
 
 cudaError_t launch_reserve(const PageTables& t, int num_blocks, const int32_t* rows,
