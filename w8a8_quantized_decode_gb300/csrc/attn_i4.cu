@@ -54,7 +54,7 @@
 // copies alone take 94, the arithmetic alone about 109, and neither the
 // integer pipe, 49 % busy, nor HBM, 70 %, is full: their waits do not hide
 // each other entirely with three warps per scheduler); 16 requests of 64 to
-// 4096 tokens, 37 MB, 16 us; one of 256 tokens 3 us.
+// 4096 tokens, 37 MB, 14 us; one of 256 tokens 3 us.
 #include <limits.h>
 
 #include <algorithm>
