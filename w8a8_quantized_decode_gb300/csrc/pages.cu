@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 // fork
 // ---------------------------------------------------------------------------
 
-struct ForkPlan {
+struct __align__(16) ForkPlan {
     int src;        // the parent's page in part, -1: none
     int fresh;      // the page that takes its copy
     int full;       // shared pages, -1: the fork is not carried out
