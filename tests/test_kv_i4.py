@@ -373,6 +373,8 @@ def test_attention_bad_tables_and_nan_rows():
     (1, 20011, 20011, 8, 1, 128, 24),    # one request in as many parts as there are runs
     (2, 9000, 9001, 14, 2, 64, 128),
     (5, 250, 258, 40, 8, 128, 129),      # tables just past what one CTA takes whole
+    (2, 290, 310, 1900, 1900, 64, 16),   # more KV heads than CTAs at once: one run
+    (3, 700, 900, 130, 26, 128, 64),
 ])
 def test_attention_runs(B, lo, hi, Hq, Hkv, D, page):
     ctx = np.random.default_rng(B).integers(lo, hi + 1, B)
