@@ -395,8 +395,9 @@ a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
  * flags A8W8_DEVERR_BLOCK; a NaN row makes the heads that attend to it NaN,
  * and so does a query head with a NaN, an infinity or a value of 2^118 or
  * more. V rows with 0 < s < 2^-74 lose precision; constant rows (s = 0) of
- * 2^40 and more may overflow the sums. B is at most 65535, B * Hq at most 2^24, num_blocks * page_size below
- * 2^31 and B * max_blocks * page_size at most 2^35. */
+ * 2^40 and more may overflow the sums. B is at most 65535, B * Hq at most
+ * 2^24, num_blocks * page_size below 2^31 and B * max_blocks * page_size at
+ * most 2^35. */
 a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
                                         const uint8_t* v_codes, const a8w8_bf16* k_meta,
                                         const a8w8_bf16* v_meta, const int32_t* block_table,

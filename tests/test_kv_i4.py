@@ -143,6 +143,14 @@ def test_binding_refuses_wrong_tensors():
         a8w8._cache_i4(z, z, m, m[:31], 2, 64, 16, "x", -1)
 
 
+def test_binding_refuses_a_cache_of_no_heads():
+    import torch
+    z = torch.zeros((32, 0, 32), dtype=torch.uint8)
+    m = torch.zeros((32, 0, 2), dtype=torch.bfloat16)
+    with pytest.raises(a8w8.A8W8Error, match="codes"):
+        a8w8._cache_i4(z, z, m, m, 0, 64, 16, "x", -1)
+
+
 # ---------------------------------------------------------------------------
 # write and read (GPU)
 # ---------------------------------------------------------------------------

@@ -530,9 +530,9 @@ def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
     torch = _torch()
     u8, bf = torch.uint8, torch.bfloat16
     pairs = k_meta.numel()
-    slots = pairs // (2 * Hkv)
+    slots = pairs // (2 * Hkv) if Hkv > 0 else -1
     codes = slots * Hkv * D // 2
-    if page_size <= 0 or slots % page_size or pairs != slots * Hkv * 2 or \
+    if slots < 0 or page_size <= 0 or slots % page_size or pairs != slots * Hkv * 2 or \
             v_meta.numel() != pairs or k_codes.numel() != codes or v_codes.numel() != codes:
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: codes [slots, {Hkv}, {D // 2}] and meta "
                         f"[slots, {Hkv}, 2] of whole pages of {page_size} tokens expected")
