@@ -137,3 +137,9 @@ def test_measured_path_wrappers(rec):
                           ws, _t((2,), torch.int32))
     assert rec.calls == ["a8w8_rmsnorm_gate_up_swiglu", "a8w8_matmul_i8", "a8w8_decode_layer",
                          "a8w8_prefill_layer", "a8w8_decode_step"]
+
+
+def test_binding_uses_public_torch_names_only():
+    """torch's private modules change with any release."""
+    src = open(a8w8.__file__).read()
+    assert "torch._" not in src and "_torch()._" not in src and "._C" not in src

@@ -500,20 +500,7 @@ def _typed(t, dtype, what, dev, numel=None):
 
 def _device() -> int:
     """Index of the current CUDA device."""
-    return _torch()._C._cuda_getDevice()
-
-
-def _raw_stream(stream, dev):
-    """The cudaStream_t of `stream`, or of the current stream of device dev."""
-    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _new_rows(a, b, c):
-    """An uninitialised bf16 tensor [a, b, c] on the current CUDA device, by the allocation entry
-    that torch's own generated code uses: one call without the dispatcher (a call of an operator
-    costs the host several microseconds between kernel launches)."""
-    torch = _torch()
-    return torch._C._dynamo.guards._empty_strided_cuda((a, b, c), (b * c, c, 1), torch.bfloat16)
+    return _torch().cuda.current_device()
 
 
 def _kept(t, stream):
@@ -557,7 +544,7 @@ def paged_kv_write_i4(k, v, slot_mapping, k_codes, v_codes, k_meta, v_meta, page
     _check(lib().paged_kv_write_i4(
         _typed(k, torch.bfloat16, what, dev), _typed(v, torch.bfloat16, what, dev, T * Hkv * D), T,
         Hkv, D, _typed(slot_mapping, torch.int32, what, dev, T), *ptrs, num_blocks, page_size,
-        _raw_stream(stream, dev)))
+        _stream(stream)))
 
 
 def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, out=None,
@@ -570,7 +557,7 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        k, v = _kept(_new_rows(T, Hkv, D), stream), _kept(_new_rows(T, Hkv, D), stream)
+        k, v = (_kept(k_meta.new_empty((T, Hkv, D)), stream) for _ in range(2))
         kv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -578,7 +565,7 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
               _typed(v, torch.bfloat16, what, dev, T * Hkv * D))
     _check(lib().paged_kv_read_i4(
         *ptrs, num_blocks, page_size, _typed(slot_mapping, torch.int32, what, dev, T), T, Hkv, D,
-        *kv, _raw_stream(stream, dev)))
+        *kv, _stream(stream)))
     return k, v
 
 
@@ -603,7 +590,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         if need:
             ws = _kept(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
     qp = _typed(q, torch.bfloat16, what, dev)
-    o = _kept(_new_rows(B, Hq, D), stream) if out is None else out
+    o = _kept(torch.empty_like(q), stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
         qp, *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
@@ -611,7 +598,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         num_blocks, scale,
         o.data_ptr() if out is None else _typed(o, torch.bfloat16, what, dev, B * Hq * D),
         None if ws is None else _typed(ws, torch.uint8, what, dev), 0 if ws is None else ws.numel(),
-        _raw_stream(stream, dev)))
+        _stream(stream)))
     return o
 
 
@@ -673,7 +660,7 @@ def paged_copy_pages(pool, src, dst, stream=None):
     what = "paged_copy_pages"
     i32, dev, n = _torch().int32, pool._here(what), src.numel()
     _check(lib().paged_copy_pages(*pool._args, pool.num_blocks, _typed(src, i32, what, dev, n),
-                                  _typed(dst, i32, what, dev, n), n, _raw_stream(stream, dev)))
+                                  _typed(dst, i32, what, dev, n), n, _stream(stream)))
 
 
 def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None, stream=None):
@@ -685,7 +672,7 @@ def paged_fork(pool, block_table, ctx_lens, refcount, parents, children, ws=None
     _check(lib().paged_fork(*pool._args, pool.num_blocks, pool.page_size, bt, cl, rc, B,
                             max_blocks, _typed(parents, i32, what, dev, n),
                             _typed(children, i32, what, dev, n), n,
-                            *_pages_ws(pool, B, n, ws, what, dev, stream), _raw_stream(stream, dev)))
+                            *_pages_ws(pool, B, n, ws, what, dev, stream), _stream(stream)))
 
 
 def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=None):
@@ -697,7 +684,7 @@ def paged_reserve(pool, block_table, refcount, rows, tokens, ws=None, stream=Non
     _check(lib().paged_reserve(bt, rc, B, max_blocks, pool.num_blocks, pool.page_size,
                                _typed(rows, i32, what, dev, n),
                                _typed(tokens, i32, what, dev, n), n,
-                               *_pages_ws(pool, B, n, ws, what, dev, stream), _raw_stream(stream, dev)))
+                               *_pages_ws(pool, B, n, ws, what, dev, stream), _stream(stream)))
 
 
 def paged_free(pool, block_table, ctx_lens, refcount, rows, stream=None):
@@ -707,7 +694,7 @@ def paged_free(pool, block_table, ctx_lens, refcount, rows, stream=None):
     i32, dev, n = _torch().int32, pool._here(what), rows.numel()
     bt, cl, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount, ctx_lens)
     _check(lib().paged_free(bt, cl, rc, B, max_blocks, pool.num_blocks,
-                            _typed(rows, i32, what, dev, n), n, _raw_stream(stream, dev)))
+                            _typed(rows, i32, what, dev, n), n, _stream(stream)))
 
 
 def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=None):
@@ -721,7 +708,7 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
         num_live = _kept(torch.empty(1, dtype=torch.int32, device=pool.device), stream)
     _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
                                _typed(num_live, torch.int32, what, dev, 1),
-                               *_pages_ws(pool, B, 0, ws, what, dev, stream), _raw_stream(stream, dev)))
+                               *_pages_ws(pool, B, 0, ws, what, dev, stream), _stream(stream)))
     return num_live
 
 
