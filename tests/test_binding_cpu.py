@@ -143,3 +143,71 @@ def test_binding_uses_public_torch_names_only():
     """torch's private modules change with any release."""
     src = open(a8w8.__file__).read()
     assert "torch._" not in src and "_torch()._" not in src and "._C" not in src
+
+
+class _FakeStreams:
+    """What _alloc uses of torch: streams, one of them current, and tensors that note the stream
+    they were allocated on and those recorded as users."""
+
+    class Stream:
+        def __init__(self, n):
+            self.cuda_stream = n
+
+    def __init__(self):
+        self.now, self.cuda = self.Stream(1), self
+
+    def current_stream(self):
+        return self.now
+
+    def stream(self, s):
+        import contextlib
+
+        @contextlib.contextmanager
+        def switch():
+            before, self.now = self.now, s
+            yield
+            self.now = before
+        return switch()
+
+    def tensor(self):
+        t = type("T", (), {})()
+        t.home, t.users = self.now, []
+        t.record_stream = t.users.append
+        return t
+
+
+def test_memory_of_a_call_belongs_to_its_stream(monkeypatch):
+    fake = _FakeStreams()
+    monkeypatch.setattr(a8w8, "_torch", lambda: fake)
+    here, side = fake.now, fake.Stream(2)
+    t = a8w8._alloc(fake.tensor, side)
+    assert t.home is side and t.users == [here] and fake.now is here
+    for s in (None, here, fake.Stream(1)):
+        t = a8w8._alloc(fake.tensor, s)
+        assert t.home is here and not t.users
+
+
+def _bare_allocations(names):
+    """(function, line) of tensors that the named functions allocate outside of _alloc."""
+    import ast
+    tree = ast.parse(open(a8w8.__file__).read())
+    found = []
+    for f in tree.body:
+        if not isinstance(f, ast.FunctionDef) or not names(f):
+            continue
+        inside = {id(n) for c in ast.walk(f) if isinstance(c, ast.Call)
+                  and getattr(c.func, "id", "") == "_alloc" for n in ast.walk(c)}
+        found += [(f.name, n.lineno) for n in ast.walk(f) if isinstance(n, ast.Call)
+                  and getattr(n.func, "attr", "").startswith(("empty", "new_empty", "zeros", "full"))
+                  and id(n) not in inside]
+    return found
+
+
+def _takes_stream(f):
+    return "stream" in [a.arg for a in f.args.args]
+
+
+def test_4_bit_and_page_entries_allocate_on_their_stream():
+    new = lambda f: _takes_stream(f) and ("i4" in f.name or "page" in f.name)  # noqa: E731
+    assert _bare_allocations(lambda f: new(f) and f.name != "paged_decode_attention_i8kv"
+                             and not f.name.startswith("paged_decode_attention_bf16")) == []

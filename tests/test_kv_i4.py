@@ -539,3 +539,34 @@ def test_attention_full_server():
                                                                      (kc, vc, *meta)]
         want, bound = kv_i4.attention(q[b:b + 1], *own, np.arange(max(n, 1))[None], ctx[b:b + 1], page)
         _check(got[b:b + 1], want, bound)
+
+
+@gpu
+def test_calls_on_another_stream_with_work_pending_on_the_current_one():
+    """The current stream gives back blocks of just the sizes that the calls allocate, with a kernel
+    still queued that writes them; the calls on another stream must not be handed those."""
+    import torch
+    page, Hq, Hkv, D, T = 32, 40, 8, 128, 6000
+    q, cache, bt, ctx = _case(41, [3000, 17, 900, 2500] * 8, Hq, Hkv, D, page)
+    want, bound = kv_i4.attention(q[:4], *cache, bt[:4], ctx[:4], page)
+    dev = [to_dev(a) for a in (q, *cache, bt, ctx)]
+    slots = to_dev(np.random.default_rng(2).integers(0, cache[0].shape[0], T).astype(np.int32))
+    ref = a8w8.paged_kv_read_i4(*dev[1:5], slots, page)
+    need = a8w8.attention_i4_workspace_bytes(len(ctx), Hq, Hkv, D, bt.shape[1] * page)
+    a = torch.randn((8192, 8192), device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        left = [torch.empty_like(dev[0]), torch.empty(need, dtype=torch.uint8, device="cuda"),
+                torch.empty_like(ref[0]), torch.empty_like(ref[1])]
+        for _k in range(20):                               # some 10 ms on the current stream
+            a @ a
+        for x in left:
+            x.fill_(0)
+        del left, x
+        got = a8w8.paged_decode_attention_i4kv(*dev, page, stream=side)
+        k, v = a8w8.paged_kv_read_i4(*dev[1:5], slots, page, stream=side)
+        torch.cuda.synchronize()
+        _check(got[:4], want, bound)
+        assert torch.equal(k, ref[0]) and torch.equal(v, ref[1])
+        del got, k, v

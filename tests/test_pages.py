@@ -584,3 +584,35 @@ def test_serving_run_over_the_4_bit_cache():
     assert np.array_equal(before, check())             # moved pages, the same bits
     assert np.array_equal(np.bincount(held, minlength=N), to_host(ref))
     assert a8w8.read_device_errors() == 0
+
+
+@gpu
+def test_calls_on_another_stream_with_work_pending_on_the_current_one():
+    """Workspaces and counts of calls on another stream are not taken from what the current stream
+    gave back with a kernel still queued that writes it."""
+    import torch
+    page = 8
+    s = State(14, 16, 6, 64, page)
+    _fill(s, [0, 1], [20, 33])
+    s.on_gpu()
+    a = torch.randn((8192, 8192), device="cuda", dtype=torch.bfloat16)
+    p, c, tok = [_i32(v) for v in ([0, 1, 0], [4, 5, 6], [30, 48, 21])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a8w8.read_device_errors()
+    left = [torch.empty(a8w8.pages_workspace_bytes(64, 16, n), dtype=torch.uint8, device="cuda")
+            for n in (3, 3, 0)] + [torch.empty(1, dtype=torch.int32, device="cuda")]
+    for _ in range(20):                                    # some 10 ms on the current stream
+        a @ a
+    for x in left:
+        x.fill_(1)
+    del left, x
+    a8w8.paged_fork(s.handle, *s.g, p, c, stream=side)
+    a8w8.paged_reserve(s.handle, s.g[0], s.g[2], c, tok, stream=side)
+    live = a8w8.paged_compact(s.handle, s.g[0], s.g[2], stream=side)
+    torch.cuda.synchronize()
+    err = pages.fork(s.pool, page, s.bt, s.ctx, s.ref, [0, 1, 0], [4, 5, 6])
+    err |= pages.reserve(page, s.bt, s.ref, [4, 5, 6], [30, 48, 21])
+    e, n = pages.compact(s.pool, s.bt, s.ref)
+    assert int(live) == n
+    s.check(err | e)

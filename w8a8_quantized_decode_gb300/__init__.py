@@ -3,7 +3,10 @@
 Argument marshalling only: every operation runs in the CUDA kernels behind the
 C ABI declared in include/a8w8.h, with the same entry-point names. PyTorch
 supplies device memory and streams. BF16 tensors are passed as
-``torch.bfloat16``; all tensors must be contiguous CUDA tensors.
+``torch.bfloat16``; all tensors must be contiguous CUDA tensors. A call runs on
+``stream`` (None: the current stream), in order with that stream's work only;
+tensors that it shares with other streams are the caller's to order, as with
+torch's own operators.
 
 There is no CPU fallback: if the library is missing or fails to load, every
 call raises.
@@ -198,6 +201,24 @@ def _stream(stream=None):
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _alloc(make, stream):
+    """The tensor that make() allocates, for a call on `stream`. A given stream's memory comes from
+    that stream's own pool: what the current stream gave back last may still be read or written by
+    kernels queued there, for which `stream` does not wait. The current stream, where the caller goes
+    on to use the tensor, is recorded as a user of it, so that its memory is not handed out again
+    before that stream is done."""
+    if stream is None:
+        return make()
+    torch = _torch()
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
+    return t
 
 
 def make_config(cfg: dict) -> Config:
@@ -503,14 +524,6 @@ def _device() -> int:
     return _torch().cuda.current_device()
 
 
-def _kept(t, stream):
-    """A tensor allocated here for a call on `stream`: its memory is not handed out again while
-    that stream (when it is not the current one) may still use it."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
     """Pointers and page count of a 4-bit cache: codes [slots, Hkv, D / 2] uint8 and (s, m)
     pairs [slots, Hkv, 2] bfloat16, in whole pages."""
@@ -557,7 +570,7 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        k, v = (_kept(k_meta.new_empty((T, Hkv, D)), stream) for _ in range(2))
+        k, v = (_alloc(lambda: k_meta.new_empty((T, Hkv, D)), stream) for _ in range(2))
         kv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -588,9 +601,9 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     if ws is None:
         need = L.a8w8_attention_i4_workspace_bytes(B, Hq, Hkv, D, max_blocks * page_size)
         if need:
-            ws = _kept(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+            ws = _alloc(lambda: torch.empty(need, dtype=torch.uint8, device=q.device), stream)
     qp = _typed(q, torch.bfloat16, what, dev)
-    o = _kept(torch.empty_like(q), stream) if out is None else out
+    o = _alloc(lambda: torch.empty_like(q), stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
         qp, *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
@@ -650,8 +663,8 @@ def pages_workspace_bytes(num_blocks: int, B: int, n: int) -> int:
 def _pages_ws(pool, B, n, ws, what, dev, stream):
     torch = _torch()
     if ws is None:
-        ws = _kept(torch.empty(pages_workspace_bytes(pool.num_blocks, B, n), dtype=torch.uint8,
-                               device=pool.device), stream)
+        need = pages_workspace_bytes(pool.num_blocks, B, n)
+        ws = _alloc(lambda: torch.empty(need, dtype=torch.uint8, device=pool.device), stream)
     return _typed(ws, torch.uint8, what, dev), ws.numel()
 
 
@@ -705,7 +718,7 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
     dev = pool._here(what)
     bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     if num_live is None:
-        num_live = _kept(torch.empty(1, dtype=torch.int32, device=pool.device), stream)
+        num_live = _alloc(lambda: torch.empty(1, dtype=torch.int32, device=pool.device), stream)
     _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
                                _typed(num_live, torch.int32, what, dev, 1),
                                *_pages_ws(pool, B, 0, ws, what, dev, stream), _stream(stream)))
