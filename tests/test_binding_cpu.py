@@ -211,3 +211,7 @@ def test_4_bit_and_page_entries_allocate_on_their_stream():
     new = lambda f: _takes_stream(f) and ("i4" in f.name or "page" in f.name)  # noqa: E731
     assert _bare_allocations(lambda f: new(f) and f.name != "paged_decode_attention_i8kv"
                              and not f.name.startswith("paged_decode_attention_bf16")) == []
+
+
+def test_every_entry_allocates_on_its_stream():
+    assert _bare_allocations(_takes_stream) == []

@@ -221,6 +221,11 @@ def _alloc(make, stream):
     return t
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on `stream`."""
+    return _alloc(lambda: _torch().empty(shape, dtype=dtype, device=device), stream)
+
+
 def make_config(cfg: dict) -> Config:
     return Config(cfg["hidden"], cfg["num_q_heads"], cfg["num_kv_heads"], cfg["head_dim"],
                   cfg["intermediate"], cfg.get("num_layers", 1), cfg.get("vocab", 0),
@@ -252,8 +257,8 @@ def read_device_errors(stream=None) -> int:
 def a8w8_quant_rows(x, stream=None):
     torch = _torch()
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    s = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    q = _empty((rows, cols), torch.int8, x.device, stream)
+    s = _empty((rows,), torch.float32, x.device, stream)
     _check(lib().a8w8_quant_rows(_ptr(x), rows, cols, cols, _ptr(q), _ptr(s), _stream(stream)))
     return q, s
 
@@ -263,8 +268,8 @@ def a8w8_linear(xq, x_scale, W, w_scale, k_splits=1, residual=None, acc_out=Fals
     torch = _torch()
     M, K = xq.shape
     N = W.shape[0]
-    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
-    acc = torch.empty((M, N), dtype=torch.int32, device=xq.device) if acc_out else None
+    y = out if out is not None else _empty((M, N), torch.bfloat16, xq.device, stream)
+    acc = _empty((M, N), torch.int32, xq.device, stream) if acc_out else None
     _check(lib().a8w8_linear(_ptr(xq), _ptr(x_scale), M, K, _ptr(W), _ptr(w_scale), N, k_splits,
                              _ptr(residual), _ptr(y), _ptr(acc), _stream(stream)))
     return (y, acc) if acc_out else y
@@ -274,8 +279,8 @@ def a8w8_gate_up_swiglu(xq, x_scale, W_gu, s_gu, acc_out=False, stream=None):
     torch = _torch()
     M, K = xq.shape
     I = W_gu.shape[0] // 2
-    act = torch.empty((M, I), dtype=torch.bfloat16, device=xq.device)
-    acc = torch.empty((M, 2 * I), dtype=torch.int32, device=xq.device) if acc_out else None
+    act = _empty((M, I), torch.bfloat16, xq.device, stream)
+    acc = _empty((M, 2 * I), torch.int32, xq.device, stream) if acc_out else None
     _check(lib().a8w8_gate_up_swiglu(_ptr(xq), _ptr(x_scale), M, K, _ptr(W_gu), _ptr(s_gu), I,
                                      _ptr(act), _ptr(acc), _stream(stream)))
     return (act, acc) if acc_out else act
@@ -289,9 +294,9 @@ def a8w8_matmul_i8(xq, W, k0=0, k1=None, out=None, scratch=None, stream=None):
     M, K = xq.shape
     N = W.shape[0]
     k1 = K if k1 is None else k1
-    acc = out if out is not None else torch.empty((M, N), dtype=torch.int32, device=xq.device)
+    acc = out if out is not None else _empty((M, N), torch.int32, xq.device, stream)
     if scratch is None:
-        scratch = torch.empty((max(M * K, 1),), dtype=torch.float16, device=xq.device)
+        scratch = _empty((max(M * K, 1),), torch.float16, xq.device, stream)
     _check(lib().a8w8_matmul_i8(_ptr(xq), M, K, _ptr(W), N, int(k0), int(k1), _ptr(acc),
                                 _ptr(scratch), _stream(stream)))
     return acc
@@ -303,7 +308,7 @@ def a8w8_rmsnorm_gate_up_swiglu(x, norm_w, eps, W_gu, s_gu, out=None, stream=Non
     torch = _torch()
     M, K = x.shape
     I = W_gu.shape[0] // 2
-    act = out if out is not None else torch.empty((M, I), dtype=torch.bfloat16, device=x.device)
+    act = out if out is not None else _empty((M, I), torch.bfloat16, x.device, stream)
     _check(lib().a8w8_rmsnorm_gate_up_swiglu(_ptr(x), M, K, _ptr(norm_w), float(eps), _ptr(W_gu),
                                              _ptr(s_gu), I, _ptr(act), _stream(stream)))
     return act
@@ -330,8 +335,8 @@ def paged_decode_attention_bf16(q, k_cache, v_cache, block_table, ctx_lens, page
     scale = (1.0 / D ** 0.5) if softmax_scale is None else softmax_scale
     need = attention_workspace_bytes(B, Hq, D, max_blocks * page_size)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    o = out if out is not None else torch.empty_like(q)
+        ws = _empty(need, torch.uint8, q.device, stream)
+    o = out if out is not None else _alloc(lambda: _torch().empty_like(q), stream)
     _check(lib().paged_decode_attention_bf16(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens), B, Hq, Hkv, D,
         page_size, max_blocks, num_blocks, scale, _ptr(o), _ptr(ws),
@@ -355,7 +360,7 @@ def paged_decode_attention_bf16_noalloc(q, k_cache, v_cache, block_table, ctx_le
     Hkv = k_cache.shape[-2]
     num_blocks = k_cache.numel() // (Hkv * D * page_size)
     scale = (1.0 / D ** 0.5) if softmax_scale is None else softmax_scale
-    o = out if out is not None else _torch().empty_like(q)
+    o = out if out is not None else _alloc(lambda: _torch().empty_like(q), stream)
     _check(lib().paged_decode_attention_bf16_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(ctx_lens), B, Hq, Hkv, D,
         page_size, block_table.shape[1], num_blocks, scale, _ptr(o), _stream(stream)))
@@ -364,7 +369,7 @@ def paged_decode_attention_bf16_noalloc(q, k_cache, v_cache, block_table, ctx_le
 
 def a8w8_rope_table(max_pos, D, theta, device="cuda", stream=None):
     torch = _torch()
-    t = torch.empty((max_pos, 2 * D), dtype=torch.float32, device=device)
+    t = _empty((max_pos, 2 * D), torch.float32, device, stream)
     _check(lib().a8w8_rope_table(_ptr(t), max_pos, D, float(theta), _stream(stream)))
     return t
 
@@ -376,10 +381,10 @@ def a8w8_sample(logits, temperature: float, top_p: float, seed: int, step: int, 
     Gumbel-max rule with Philox4x32-10 noise keyed by (seed, step)."""
     torch = _torch()
     B, V = logits.shape
-    o = out if out is not None else torch.empty(B, dtype=torch.int32, device=logits.device)
+    o = out if out is not None else _empty(B, torch.int32, logits.device, stream)
     need = lib().a8w8_sample_workspace_bytes(B, V)
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        ws = _empty(need, torch.uint8, logits.device, stream)
     _check(lib().a8w8_sample(_ptr(logits), B, V, logits.stride(0), float(temperature), float(top_p),
                              int(seed) & (2 ** 64 - 1), int(step) & (2 ** 64 - 1), _ptr(o), _ptr(ws),
                              0 if ws is None else ws.numel(), _stream(stream)))
@@ -451,8 +456,8 @@ def paged_decode_attention_i8kv(q, k_codes, v_codes, k_scale, v_scale, block_tab
     scale = (1.0 / D ** 0.5) if softmax_scale is None else softmax_scale
     need = attention_workspace_bytes(B, Hq, D, max_blocks * page_size)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    o = out if out is not None else torch.empty_like(q)
+        ws = _empty(need, torch.uint8, q.device, stream)
+    o = out if out is not None else _alloc(lambda: _torch().empty_like(q), stream)
     _check(lib().paged_decode_attention_i8kv(
         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
         _ptr(ctx_lens), B, Hq, Hkv, D, page_size, max_blocks, num_blocks, scale, _ptr(o),
@@ -601,7 +606,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
     if ws is None:
         need = L.a8w8_attention_i4_workspace_bytes(B, Hq, Hkv, D, max_blocks * page_size)
         if need:
-            ws = _alloc(lambda: torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+            ws = _empty(need, torch.uint8, q.device, stream)
     qp = _typed(q, torch.bfloat16, what, dev)
     o = _alloc(lambda: torch.empty_like(q), stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
@@ -664,7 +669,7 @@ def _pages_ws(pool, B, n, ws, what, dev, stream):
     torch = _torch()
     if ws is None:
         need = pages_workspace_bytes(pool.num_blocks, B, n)
-        ws = _alloc(lambda: torch.empty(need, dtype=torch.uint8, device=pool.device), stream)
+        ws = _empty(need, torch.uint8, pool.device, stream)
     return _typed(ws, torch.uint8, what, dev), ws.numel()
 
 
@@ -718,7 +723,7 @@ def paged_compact(pool, block_table, refcount, num_live=None, ws=None, stream=No
     dev = pool._here(what)
     bt, _, rc, B, max_blocks = pool._tables(what, dev, block_table, refcount)
     if num_live is None:
-        num_live = _alloc(lambda: torch.empty(1, dtype=torch.int32, device=pool.device), stream)
+        num_live = _empty(1, torch.int32, pool.device, stream)
     _check(lib().paged_compact(*pool._args, pool.num_blocks, bt, rc, B, max_blocks,
                                _typed(num_live, torch.int32, what, dev, 1),
                                *_pages_ws(pool, B, 0, ws, what, dev, stream), _stream(stream)))
@@ -730,7 +735,7 @@ def bf16_linear(x, W, residual=None, out=None, stream=None):
     torch = _torch()
     M, K = x.shape
     N = W.shape[0]
-    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    y = out if out is not None else _empty((M, N), torch.bfloat16, x.device, stream)
     _check(lib().bf16_linear(_ptr(x), M, K, _ptr(W), N, _ptr(residual), _ptr(y), _stream(stream)))
     return y
 
@@ -740,7 +745,7 @@ def bf16_gate_up_swiglu(x, W_gu, stream=None):
     torch = _torch()
     M, K = x.shape
     I = W_gu.shape[0] // 2
-    act = torch.empty((M, I), dtype=torch.bfloat16, device=x.device)
+    act = _empty((M, I), torch.bfloat16, x.device, stream)
     _check(lib().bf16_gate_up_swiglu(_ptr(x), M, K, _ptr(W_gu), I, _ptr(act), _stream(stream)))
     return act
 
