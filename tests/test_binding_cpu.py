@@ -139,10 +139,33 @@ def test_measured_path_wrappers(rec):
                          "a8w8_prefill_layer", "a8w8_decode_step"]
 
 
-def test_binding_uses_public_torch_names_only():
-    """torch's private modules change with any release."""
-    src = open(a8w8.__file__).read()
-    assert "torch._" not in src and "_torch()._" not in src and "._C" not in src
+@pytest.mark.parametrize("what", ["absent", "changed", "raises", "there"])
+def test_private_torch_entries_have_public_stand_ins(what):
+    """torch's private entries change with any release: whatever is there in their place, the calls
+    get the current stream and rows of the shape they ask for."""
+    from types import SimpleNamespace as NS
+    public, calls = object(), []
+
+    def fail(*a):
+        raise TypeError("another signature")
+
+    def private(shape, strides, dtype):
+        calls.append(shape)
+        t = torch.empty_strided(shape, strides, dtype=dtype)
+        return NS(dtype=t.dtype, shape=t.shape, is_contiguous=t.is_contiguous,
+                  get_device=lambda: 3 if what == "there" else 0)
+
+    own = {"absent": NS(), "raises": NS(_dynamo=NS(guards=NS(_empty_strided_cuda=fail)),
+                                        _cuda_getCurrentRawStream=fail)}.get(what, NS(
+        _dynamo=NS(guards=NS(_empty_strided_cuda=private)),
+        _cuda_getCurrentRawStream=lambda dev: 77 if what == "there" else 0))
+    fake = NS(_C=own, bfloat16=torch.bfloat16, empty_strided=lambda *a, **k: public,
+              cuda=NS(current_device=lambda: 3, current_stream=lambda *a: NS(cuda_stream=77)))
+    h = a8w8._HostPath(fake)
+    assert h.stream(3) == 77
+    rows = h.rows(5, 6, 7)
+    assert (rows is public) == (what != "there")
+    assert calls[1:] == ([(5, 6, 7)] if what == "there" else [])
 
 
 class _FakeStreams:
