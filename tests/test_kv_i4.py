@@ -570,3 +570,44 @@ def test_calls_on_another_stream_with_work_pending_on_the_current_one():
         _check(got[:4], want, bound)
         assert torch.equal(k, ref[0]) and torch.equal(v, ref[1])
         del got, k, v
+
+
+@pytest.mark.parametrize("name", ["kv_i4.cu", "attn_i4.cu", "pages.cu"])
+def test_kernels_that_start_early_read_nothing_through_the_read_only_path(name):
+    """These grids may stand beside the kernel that writes their inputs (programmatic launch); a
+    read-only (non-coherent) load is for data that stays as it is for the grid's whole time. The
+    compiler takes one for a `const __restrict__` argument."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(a8w8.__file__), "csrc", name)).read()
+    code = re.sub(r"//[^\n]*|/\*.*?\*/", "", src, flags=re.S)
+    for word in ("__restrict__", "__ldg(", "ld_nc_v4", "ld_stream_v4", ".nc."):
+        assert word not in code, word
+
+
+@gpu
+def test_rows_written_by_the_kernel_just_before():
+    """Rows read back from one cache into two buffers that are used again and again, and from there
+    into another cache, with nothing between the calls."""
+    import torch
+    T, Hkv, D, page, rounds = 700, 4, 128, 32, 40
+    rng = np.random.default_rng(12)
+    n = 40 * page
+    host = _cache(rng, n, Hkv, D)
+    src = [to_dev(a) for a in host]
+    dst = [torch.zeros((rounds * T + 32, *a.shape[1:]), dtype=a.dtype, device="cuda") for a in src]
+    dst = [d[:(d.shape[0] // page) * page] for d in dst]
+    kv = [torch.empty((T, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    at = rng.integers(0, n, (rounds, T)).astype(np.int32)
+    to = rng.permutation(rounds * T).reshape(rounds, T).astype(np.int32)
+    at_d, to_d = to_dev(at), to_dev(to)
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        a8w8.paged_kv_read_i4(*src, at_d[i], page, out=kv)
+        a8w8.paged_kv_write_i4(*kv, to_d[i], *dst, page)
+    assert a8w8.read_device_errors() == 0
+    for c, m, gc, gm in ((host[0], host[2], dst[0], dst[2]), (host[1], host[3], dst[1], dst[3])):
+        x = _bf(kv_i4.dequant_rows(c, m).astype(np.float32))
+        wc, wm = kv_i4.quant_rows(x)
+        assert np.array_equal(to_host(gc)[to], wc[at])
+        assert np.array_equal(kv_i4.bf16_to_f64(to_host(gm)[to]), kv_i4.bf16_to_f64(wm[at]))

@@ -616,3 +616,27 @@ def test_calls_on_another_stream_with_work_pending_on_the_current_one():
     e, n = pages.compact(s.pool, s.bt, s.ref)
     assert int(live) == n
     s.check(err | e)
+
+
+@gpu
+def test_lists_written_by_the_kernel_just_before():
+    """Page lists drawn by the sampler (one logit far above the others) into a buffer that is used
+    again and again, and copied from at once."""
+    import torch
+    N, n, rounds, page = 200, 24, 30, 4
+    s = State(21, 2, 2, N, page, (16,)).on_gpu()
+    src = s.rng.integers(0, 100, (rounds, n)).astype(np.int32)
+    logits = torch.zeros((rounds, n, N), dtype=torch.float32, device="cuda")
+    logits.scatter_(2, to_dev(src.astype(np.int64))[:, :, None], 100.0)
+    dst = _i32(100 + s.rng.permutation(100)[:n])
+    out = torch.empty(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(a8w8.lib().a8w8_sample_workspace_bytes(n, N), dtype=torch.uint8, device="cuda")
+    got = torch.zeros((rounds, n, page, 16), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    a8w8.read_device_errors()
+    for i in range(rounds):
+        a8w8.a8w8_sample(logits[i], 1.0, 1.0, 3, i, out=out, ws=ws)
+        a8w8.paged_copy_pages(s.handle, out, dst)
+        got[i] = s.gp[0][dst.long()]
+    assert a8w8.read_device_errors() == 0
+    assert np.array_equal(to_host(got), s.pool[0][src])

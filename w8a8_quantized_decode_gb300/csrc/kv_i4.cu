@@ -37,6 +37,12 @@ __device__ __forceinline__ unsigned as_u32(__nv_bfloat162 h) {
     return *reinterpret_cast<unsigned*>(&h);
 }
 
+// Sixteen bytes of a row that is read once. Not by the read-only path: the
+// kernel that writes the rows may still run when this grid starts.
+__device__ __forceinline__ int4 ld_row_v4(const bf16* p) {
+    return __ldcs(reinterpret_cast<const int4*>(p));
+}
+
 // The row's (s, m) word and the lane's sixteen codes. LPR lanes hold the row,
 // sixteen values each; every lane of the warp calls this.
 template <int LPR>
@@ -111,10 +117,9 @@ __device__ __forceinline__ unsigned quant_row_i4(const int4 (&raw)[2], unsigned 
 
 template <int D>
 __global__ void __launch_bounds__(kI4Threads)
-    kv_write_i4_kernel(const bf16* __restrict__ k, const bf16* __restrict__ v, int T, int Hkv,
-                       const int32_t* __restrict__ slot_mapping, uint8_t* __restrict__ k_codes,
-                       uint8_t* __restrict__ v_codes, bf16* __restrict__ k_meta,
-                       bf16* __restrict__ v_meta, long num_slots, unsigned* err) {
+    kv_write_i4_kernel(const bf16* k, const bf16* v, int T, int Hkv, const int32_t* slot_mapping,
+                       uint8_t* k_codes, uint8_t* v_codes, bf16* k_meta, bf16* v_meta,
+                       long num_slots, unsigned* err) {
     constexpr int LPR = D / 16;
     pdl_wait();
     pdl_trigger();
@@ -128,8 +133,8 @@ __global__ void __launch_bounds__(kI4Threads)
     for (int i = 0; i < 2; ++i) {
         kr[i] = vr[i] = make_int4(0, 0, 0, 0);
         if (t < (unsigned)T) {
-            kr[i] = ld_stream_v4(k + (size_t)row * D + 8 * (j + LPR * i));
-            vr[i] = ld_stream_v4(v + (size_t)row * D + 8 * (j + LPR * i));
+            kr[i] = ld_row_v4(k + (size_t)row * D + 8 * (j + LPR * i));
+            vr[i] = ld_row_v4(v + (size_t)row * D + 8 * (j + LPR * i));
         }
     }
     if (slot >= num_slots) {
@@ -172,10 +177,9 @@ __device__ __forceinline__ int4 dequant8(unsigned codes, unsigned meta) {
 
 template <int D>
 __global__ void __launch_bounds__(kI4Threads)
-    kv_read_i4_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
-                      const bf16* __restrict__ k_meta, const bf16* __restrict__ v_meta,
-                      long num_slots, const int32_t* __restrict__ slot_mapping, int T, int Hkv,
-                      bf16* __restrict__ k, bf16* __restrict__ v, unsigned* err) {
+    kv_read_i4_kernel(const uint8_t* k_codes, const uint8_t* v_codes, const bf16* k_meta,
+                      const bf16* v_meta, long num_slots, const int32_t* slot_mapping, int T,
+                      int Hkv, bf16* k, bf16* v, unsigned* err) {
     constexpr int LPR = D / 16;
     pdl_wait();
     pdl_trigger();

@@ -12,7 +12,11 @@
 // and compact run a one-CTA plan that decides every move (the decisions are
 // ordered: ranks among the free pages), then one kernel that carries the moves
 // out over all SMs. The plan starts the second kernel early by programmatic
-// dependent launch, so that only its wait remains between them.
+// dependent launch, so that only its wait remains between them. A grid can so
+// be there while the kernel before it writes the lists, tables and counts that
+// it takes: they are read by plain loads or from L2 after the wait, never by
+// the read-only path (no `const ... __restrict__` here), which asks for data
+// that nothing writes as long as the grid is there.
 // Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page): 96
 // copies 164 us (6.5 TB/s read and written, 0.98 of the copy rate);
 // compaction of some 150 of 260 live pages 251 us; 64 forks of 16 parents,
@@ -164,8 +168,8 @@ constexpr int kPairBatch = 64;
 // earlier pair or the source of another one; a pair counts if both pages are
 // in range and differ.
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_pages_kernel(const __grid_constant__ CacheList c, const int32_t* __restrict__ src,
-                      const int32_t* __restrict__ dst, int n, unsigned* err) {
+    copy_pages_kernel(const __grid_constant__ CacheList c, const int32_t* src, const int32_t* dst,
+                      int n, unsigned* err) {
     __shared__ int sfrom[kPairBatch], sto[kPairBatch], sbad[kPairBatch];
     pdl_wait();
     pdl_trigger();
@@ -235,9 +239,9 @@ __device__ __forceinline__ void first_entries(int* first, int B, int n, Row row)
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-    fork_plan_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ parents,
-                     const int32_t* __restrict__ children, int n, ForkPlan* plan, int* need_ws,
-                     int* first_ws, unsigned* err) {
+    fork_plan_kernel(const PageTables t, int num_blocks, const int32_t* parents,
+                     const int32_t* children, int n, ForkPlan* plan, int* need_ws, int* first_ws,
+                     unsigned* err) {
     __shared__ int s[32];
     __shared__ int s_need[kSharedList], s_first[kSharedRows];
     __shared__ ForkPlan s_plan[kSharedList];
@@ -323,8 +327,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // 40-layer pool, 46 here). The tables and counts of fork i by CTA i mod grid.
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const __grid_constant__ CacheList c, const PageTables t,
-                      const int32_t* __restrict__ parents, const int32_t* __restrict__ children,
-                      int n, const ForkPlan* plan, int shift) {
+                      const int32_t* parents, const int32_t* children, int n,
+                      const ForkPlan* plan, int shift) {
     __shared__ unsigned char* s_base[kMaxCaches];
     __shared__ unsigned s_token[kMaxCaches];    // bytes of a token
     for (int k = threadIdx.x; k < c.num_caches; k += kCopyThreads) {
@@ -338,7 +342,8 @@ __global__ void __launch_bounds__(kCopyThreads)
         const ForkPlan f = plan[i];
         if (f.full < 0) continue;
         const int32_t* from = t.block_table + (size_t)parents[i] * t.max_blocks;
-        int32_t* to = t.block_table + (size_t)children[i] * t.max_blocks;
+        const int child = children[i];
+        int32_t* to = t.block_table + (size_t)child * t.max_blocks;
         for (int j = threadIdx.x; j < t.max_blocks; j += kCopyThreads) {
             int e = -1;
             if (j < f.full) {
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(kCopyThreads)
             }
             to[j] = e;
         }
-        if (threadIdx.x == 0) t.ctx_lens[children[i]] = f.full * t.page + f.part;
+        if (threadIdx.x == 0) t.ctx_lens[child] = f.full * t.page + f.part;
     }
     const unsigned items = (unsigned)c.num_caches << shift;
     const int du = gridDim.x / n, di = gridDim.x % n;
@@ -381,9 +386,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // ---------------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kPlanThreads)
-    reserve_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ rows,
-                   const int32_t* __restrict__ tokens, int n, int2* need_ws, int* first_ws,
-                   int* fresh, unsigned* err) {
+    reserve_kernel(const PageTables t, int num_blocks, const int32_t* rows, const int32_t* tokens,
+                   int n, int2* need_ws, int* first_ws, int* fresh, unsigned* err) {
     __shared__ int s[32];
     __shared__ int2 s_need[kSharedList];      // pages needed, first rank
     __shared__ int s_first[kSharedRows];
@@ -460,8 +464,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // One warp per listed row. Each entry is taken by an atomic exchange, so a row
 // named twice gives its pages back once.
 __global__ void __launch_bounds__(kCopyThreads)
-    free_kernel(const PageTables t, int num_blocks, const int32_t* __restrict__ rows, int n,
-                unsigned* err) {
+    free_kernel(const PageTables t, int num_blocks, const int32_t* rows, int n, unsigned* err) {
     pdl_wait();
     pdl_trigger();
     const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 // live page at or past head[0]) to page to[k] (the k-th free page below it);
 // remap[p - head[0]] for p >= head[0]: the page's new number, -1 if free.
 __global__ void __launch_bounds__(kPlanThreads)
-    compact_plan_kernel(const int32_t* __restrict__ refcount, int num_blocks, int* head, int* from,
+    compact_plan_kernel(const int32_t* refcount, int num_blocks, int* head, int* from,
                         int* to, int* remap, int32_t* num_live) {
     __shared__ int s[32];
     pdl_wait();
