@@ -163,7 +163,7 @@ def test_private_torch_entries_have_public_stand_ins(what):
               cuda=NS(current_device=lambda: 3, current_stream=lambda *a: NS(cuda_stream=77)))
     h = a8w8._HostPath(fake)
     assert h.stream(3) == 77
-    rows = h.rows(5, 6, 7)
+    rows = h.rows(5, 6, 7, None)
     assert (rows is public) == (what != "there")
     assert calls[1:] == ([(5, 6, 7)] if what == "there" else [])
 

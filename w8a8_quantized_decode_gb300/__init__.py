@@ -556,11 +556,14 @@ class _HostPath:
                 self.stream = f
         except Exception:
             pass
-        self._bf16 = torch.bfloat16
+        self._bf16, self.device = torch.bfloat16, torch.cuda.current_device
 
-    def rows(self, a, b, c):
-        """An uninitialised bf16 tensor [a, b, c] on the current CUDA device."""
-        return self._rows((a, b, c), (b * c, c, 1), self._bf16)
+    def rows(self, a, b, c, stream):
+        """An uninitialised bf16 tensor [a, b, c] on the current CUDA device, for a call on
+        `stream`."""
+        if stream is None:
+            return self._rows((a, b, c), (b * c, c, 1), self._bf16)
+        return _alloc(lambda: self._rows((a, b, c), (b * c, c, 1), self._bf16), stream)
 
 
 _host_path = None
@@ -575,12 +578,12 @@ def _host():
 
 def _device() -> int:
     """Index of the current CUDA device."""
-    return _torch().cuda.current_device()
+    return (_host_path or _host()).device()
 
 
 def _raw_stream(stream, dev):
     """The cudaStream_t of `stream`, or of the current stream of device dev."""
-    return _host().stream(dev) if stream is None else stream.cuda_stream
+    return (_host_path or _host()).stream(dev) if stream is None else stream.cuda_stream
 
 
 def _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev):
@@ -629,7 +632,8 @@ def paged_kv_read_i4(k_codes, v_codes, k_meta, v_meta, slot_mapping, page_size, 
     T = slot_mapping.numel()
     ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
     if out is None:
-        k, v = (_alloc(lambda: _host().rows(T, Hkv, D), stream) for _ in range(2))
+        h = _host()
+        k, v = h.rows(T, Hkv, D, stream), h.rows(T, Hkv, D, stream)
         kv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -662,7 +666,7 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         if need:
             ws = _empty(need, torch.uint8, q.device, stream)
     qp = _typed(q, torch.bfloat16, what, dev)
-    o = _alloc(lambda: _host().rows(B, Hq, D), stream) if out is None else out
+    o = _host().rows(B, Hq, D, stream) if out is None else out
     _check(L.paged_decode_attention_i4kv(
         qp, *ptrs,
         _typed(block_table, torch.int32, what, dev, B * max_blocks),
