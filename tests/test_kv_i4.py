@@ -611,3 +611,19 @@ def test_rows_written_by_the_kernel_just_before():
         wc, wm = kv_i4.quant_rows(x)
         assert np.array_equal(to_host(gc)[to], wc[at])
         assert np.array_equal(kv_i4.bf16_to_f64(to_host(gm)[to]), kv_i4.bf16_to_f64(wm[at]))
+
+
+@gpu
+def test_attention_largest_query():
+    """The largest BF16 below 2^118 is a query value like any other."""
+    page, Hq, Hkv, D = 16, 4, 2, 64
+    q, cache, bt, ctx = _case(13, [40, 300], Hq, Hkv, D, page)
+    q[:, 1] = 0
+    q[0, 1, 5] = q[1, 1, 60] = 0x7A7F                      # 1.9921875 * 2^117
+    assert kv_i4.bf16_to_f64(q[0, 1, 5]) == 2.0 ** 118 - 2.0 ** 110
+    q[0, 2, 7], q[1, 3, 0] = _bf(2.0 ** 118), _bf(-(2.0 ** 118))
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page, scale=2.0 ** -118)
+    want[0, 2] = want[1, 3] = np.nan
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page,
+                                           softmax_scale=2.0 ** -118)
+    _check(got, want, bound)

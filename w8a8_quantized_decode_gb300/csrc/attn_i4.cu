@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const float sc = p.scale * 1.4426950408889634f;
             float f = __uint_as_float((unsigned)(127 + 20 - e) << 23) * sc;
             // a NaN shows in the sum; from 2^118 on FP16 would overflow
-            if (!(fabsf(sum) <= 3e38f) || top >= 3.3e35f) f = __uint_as_float(0x7FC00000u);
+            if (!(fabsf(sum) <= 3e38f) || top >= 0x1p118f) f = __uint_as_float(0x7FC00000u);
             sum *= sc;
             ch = pair(__shfl_sync(0xffffffffu, f, 8 * t), __shfl_sync(0xffffffffu, f, 8 * t + 4));
             qs = pair(__shfl_sync(0xffffffffu, sum, 8 * t), __shfl_sync(0xffffffffu, sum, 8 * t + 4));
