@@ -627,3 +627,29 @@ def test_attention_largest_query():
     got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, *cache, bt, ctx)], page,
                                            softmax_scale=2.0 ** -118)
     _check(got, want, bound)
+
+
+@gpu
+@pytest.mark.parametrize("ctx", [[1, 40], [250], [5000, 33, 700]])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_attention_scores_far_from_zero(ctx, sign):
+    """Scores near +-2^113: equal ones share the weight, one above the others takes all of it."""
+    page, Hq, Hkv, D = 16, 4, 2, 64
+    q, cache, bt, ctx = _case(32, ctx, Hq, Hkv, D, page)
+    kc, vc, km, vm = cache
+    q[:] = _bf(2.0 ** 60)
+    km[..., 0], km[..., 1] = 0, _bf(sign * 2.0 ** 50)      # constant rows
+    want, bound = kv_i4.attention(q, kc, vc, km, vm, bt, ctx, page, scale=0.0)
+    dev = [to_dev(a) for a in (q, kc, vc, km, vm, bt, ctx)]
+    _check(a8w8.paged_decode_attention_i4kv(*dev, page), want, bound)
+    top = ctx // 2                                         # this token's score is 1/8 higher
+    for b, t in enumerate(top):
+        slot = bt[b][t // page] * page + t % page
+        km[slot, :, 1] = _bf(sign * 2.0 ** 50 + 2.0 ** 47)
+        for h in range(Hkv):
+            v = kv_i4.dequant_rows(vc[slot, h], vm[slot, h])
+            want[b, 2 * h:2 * h + 2] = v
+            bound[b, 2 * h:2 * h + 2] = 2.0 ** -10 * (15 * abs(kv_i4.bf16_to_f64(vm[slot, h, 0]))
+                                                      + abs(kv_i4.bf16_to_f64(vm[slot, h, 1])))
+    dev[3] = to_dev(km)
+    _check(a8w8.paged_decode_attention_i4kv(*dev, page), want, bound)

@@ -73,7 +73,7 @@ constexpr int kMaxCtas = 152 * kCtasPerSm;
 constexpr int kMinTiles = 4;         // tiles per run at least
 constexpr int kCombineThreads = 128;
 constexpr int kJoin = 2;             // parts a warp of the second kernel loads at once
-constexpr float kNoRef = -1e30f;     // ref of a warp that has seen no token
+constexpr float kNoRef = -3.4e38f;   // ref of a warp that has seen no token: below every score
 
 constexpr int code_bytes(int D) { return kTile * D / 2; }
 constexpr int stage_bytes(int D) { return 2 * code_bytes(D) + kTile * 8; }
