@@ -653,3 +653,25 @@ def test_attention_scores_far_from_zero(ctx, sign):
                                                       + abs(kv_i4.bf16_to_f64(vm[slot, h, 1])))
     dev[3] = to_dev(km)
     _check(a8w8.paged_decode_attention_i4kv(*dev, page), want, bound)
+
+
+@gpu
+@pytest.mark.parametrize("ctx", [[64], [192, 33], [3000, 100, 700]])
+@pytest.mark.parametrize("Hkv", [1, 2, 4])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+def test_attention_scales_far_apart(ctx, Hkv, order):
+    """V rows of ordinary size beside rows near the end of float32's range: their weights in the
+    softmax's sum count alike, whichever tile, warp or run they are in."""
+    page, D = 16, 64
+    q, cache, bt, ctx = _case(31, ctx, 2 * Hkv, Hkv, D, page, gain=0.3)
+    kc, vc, km, vm = cache
+    rng = np.random.default_rng(5)
+    for b, n in enumerate(ctx):
+        t = np.arange(n)
+        big = {"rising": t >= n // 2, "falling": t < n // 2, "mixed": rng.random(n) < 0.1}[order]
+        slot = bt[b][t // page] * page + t % page
+        f = np.where(big, 2.0 ** 120, 2.0 ** -12)[:, None, None]
+        vm[slot] = _bf(kv_i4.bf16_to_f64(vm[slot]) * f)
+    want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
+    got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, kc, vc, km, vm, bt, ctx)], page)
+    _check(got, want, bound)

@@ -107,6 +107,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Sums taken at one ref go to another, d higher, by the factor 2^-d, applied as
+// 2^(-d/2) twice: refs differ by up to 174 with the V rows' scales alone (2^124
+// to the 2^-50 that tiny ones count), past 2^-126, while the sum of the lower
+// ones' weights, up to 2^60 a token, weighs as much as the others'.
+__device__ __forceinline__ float half_step(float d) { return ex2(0.5f * d); }
 __device__ __forceinline__ void cp16(unsigned s, const void* g) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(g) : "memory");
 }
@@ -511,20 +516,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float d0 = fmaxf(low, z0 - 10.0f), d1 = fmaxf(low, z1 - 10.0f);
                 if (d0 <= kNoRef) d0 = 0.0f;
                 if (d1 <= kNoRef) d1 = 0.0f;
-                const float f0 = fresh ? 0.0f : ex2(-d0), f1 = fresh ? 0.0f : ex2(-d1);
+                const float f0 = fresh ? 0.0f : half_step(-d0), f1 = fresh ? 0.0f : half_step(-d1);
                 ref0 += d0;
                 ref1 += d1;
                 fresh = false;
-                l0 *= f0;
-                l1 *= f1;
-                om0 *= f0;
-                om1 *= f1;
+                l0 = l0 * f0 * f0;
+                l1 = l1 * f1 * f1;
+                om0 = om0 * f0 * f0;
+                om1 = om1 * f1 * f1;
+                const float a0 = f0 * f0, a1 = f1 * f1;
 #pragma unroll
                 for (int q = 0; q < 4 * VW; ++q) {
-                    acc[q][0] *= f0;
-                    acc[q][1] *= f1;
-                    acc[q][2] *= f0;
-                    acc[q][3] *= f1;
+                    acc[q][0] *= a0;
+                    acc[q][1] *= a1;
+                    acc[q][2] *= a0;
+                    acc[q][3] *= a1;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -674,9 +680,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                 for (int w = 0; w < TW; ++w) {
                     const int at = (w * HW + x) * 8 + hd;
-                    const float f = ex2(sref[at] - top);
-                    o = __fmaf_rn(f, so[at * (D + 4) + d], o);
-                    L = __fmaf_rn(f, sl[at], L);
+                    const float f = half_step(sref[at] - top);
+                    o = __fmaf_rn(f, f * so[at * (D + 4) + d], o);
+                    L = __fmaf_rn(f, f * sl[at], L);
                 }
                 const int hx = h - hw + x;
                 if (all) {
@@ -737,13 +743,20 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
                 for (int e = 0; e < EL; ++e) v[k][e] = __ldcg(po + lane + 32 * e);
             }
         }
+        float up = ref;
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) up = fmaxf(up, rl[k].x);
+        const float f = half_step(ref - up);
+        ref = up;
+        L = L * f * f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[e] = o[e] * f * f;
 #pragma unroll
         for (int k = 0; k < kJoin; ++k) {
-            const float up = fmaxf(ref, rl[k].x), f = ex2(ref - up), g = ex2(rl[k].x - up);
-            ref = up;
-            L = __fmaf_rn(L, f, rl[k].y * g);
+            const float g = half_step(rl[k].x - up);
+            L = __fmaf_rn(rl[k].y * g, g, L);
 #pragma unroll
-            for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(o[e], f, v[k][e] * g);
+            for (int e = 0; e < EL; ++e) o[e] = __fmaf_rn(v[k][e] * g, g, o[e]);
         }
     }
 #pragma unroll
@@ -759,9 +772,9 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
         for (int w = 0; w < NW; ++w) top = fmaxf(top, s_ref[w]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = ex2(s_ref[w] - top);
-            O = __fmaf_rn(f, so[w][d], O);
-            Ls = __fmaf_rn(f, s_l[w], Ls);
+            const float f = half_step(s_ref[w] - top);
+            O = __fmaf_rn(f, f * so[w][d], O);
+            Ls = __fmaf_rn(f, f * s_l[w], Ls);
         }
         out[d] = f2bf(__fdividef(O, Ls));
     }
