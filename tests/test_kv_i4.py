@@ -675,3 +675,49 @@ def test_attention_scales_far_apart(ctx, Hkv, order):
     want, bound = kv_i4.attention(q, *cache, bt, ctx, page)
     got = a8w8.paged_decode_attention_i4kv(*[to_dev(a) for a in (q, kc, vc, km, vm, bt, ctx)], page)
     _check(got, want, bound)
+
+
+@gpu
+def test_attention_sums_of_long_runs():
+    """64 requests of 2^24 tokens, equal scores and constant V rows c s of one code: 2^30 equal
+    weights in 456 runs. The sums' roundings stay below a quarter of BF16's half step, so the
+    result is c s itself (a BF16 value: c is a power of two). In one chain a lane adds 294,000
+    weights of which each is 2^-18 of the sum at last, and loses (a float32 model of that chain)
+    0.41 to 0.43 % for the scales taken here."""
+    page, B, Hkv, D = 4096, 64, 4, 64
+    scale = np.array([145, 129, 226, 156]) / 128.0
+    n = 2 * page
+    code = np.array([8, 4, 2, 1], np.uint8)
+    vc = np.broadcast_to((code | code << 4)[None, :, None], (n, Hkv, D // 2)).copy()
+    vm = np.broadcast_to(np.stack((_bf(scale), _bf(0 * scale)), -1)[None], (n, Hkv, 2)).copy()
+    q = np.zeros((B, Hkv, D), np.uint16)
+    bt = np.tile(np.array([0, 1], np.int32), (B, 2048))
+    ctx = np.full(B, 1 << 24, np.int32)
+    dev = [to_dev(a) for a in (q, np.zeros_like(vc), vc, np.zeros_like(vm), vm, bt, ctx)]
+    got = kv_i4.bf16_to_f64(to_host(a8w8.paged_decode_attention_i4kv(*dev, page)))
+    assert (got == (code * scale)[None, :, None]).all()
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("Hkv,D,heads", [(457, 64, (0, 228, 456)), (458, 64, (0, 1, 457)),
+                                         (1828, 64, (0, 3, 1827)), (201, 64, (0, 200)),
+                                         (402, 128, (1, 400)), (912, 128, (2, 911))])
+def test_attention_long_runs(Hkv, D, heads):
+    """So many KV heads that one run, or two, takes all tiles: segments of thousands of tiles,
+    summed piece by piece, that end with their request or inside it, against the oracle for some
+    of the heads; the same bits every time."""
+    page = 64
+    ctx = np.array([70001, 0, 140000, 90, 66000], np.int32)
+    nblk = 9
+    cache = _cache(np.random.default_rng(Hkv), nblk * page, Hkv, D)
+    bt = np.random.default_rng(1).integers(0, nblk, (len(ctx), 2200)).astype(np.int32)
+    q = synth.bf16_normal(Hkv, (len(ctx), 2 * Hkv, D), std=1.5)
+    dev = [to_dev(a) for a in (q, *cache, bt, ctx)]
+    a8w8.read_device_errors()
+    got = a8w8.paged_decode_attention_i4kv(*dev, page)
+    assert np.array_equal(to_host(got), to_host(a8w8.paged_decode_attention_i4kv(*dev, page)))
+    at = [2 * h + g for h in heads for g in (0, 1)]
+    want, bound = kv_i4.attention(q[:, at], *[c[:, list(heads)] for c in cache], bt, ctx, page)
+    _check(got[:, at], want, bound)
+    assert not to_host(got)[1].any() and a8w8.read_device_errors() == 0

@@ -71,6 +71,7 @@ constexpr int kStages = 2;           // ring depth per warp
 constexpr int kCtasPerSm = 3;
 constexpr int kMaxCtas = 152 * kCtasPerSm;
 constexpr int kMinTiles = 4;         // tiles per run at least
+constexpr int kPiece = 512;          // tiles a warp adds up before it joins them to its part
 constexpr int kCombineThreads = 128;
 constexpr int kJoin = 2;             // parts a warp of the second kernel loads at once
 constexpr float kNoRef = -3.4e38f;   // ref of a warp that has seen no token: below every score
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __shared__ unsigned s_scan[kWarps];
     __shared__ unsigned s_first;
     __shared__ int s_b, s_tokens;
+    __shared__ float2 s_was[HW * 8];           // (ref, sum) of the segment's pieces so far
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv;
@@ -310,8 +312,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const unsigned char* km = reinterpret_cast<const unsigned char*>(p.c.k_meta) + h * 4;
     const unsigned char* vm = reinterpret_cast<const unsigned char*>(p.c.v_meta) + h * 4;
 
-    // ---- a segment: the run's tiles of one request ---------------------------
-    int n_all, j1;                              // the request's tiles; the segment's end
+    // ---- a segment: the run's tiles of one request, in pieces -----------------
+    // A float32 sum of n like terms may be off by n 2^-24: where runs are long,
+    // a segment is summed in pieces of kPiece tiles a warp (2048 weights a lane)
+    // that are joined in its part's place in the workspace. At the largest size
+    // taken, 2^35 tokens, 4600 pieces: 2^-13 + 2^-11.9 in all, beside the 2^-8
+    // of the result's rounding. (One chain a run, 2^30 equal weights: 0.43 %.)
+    int n_all, j1;                              // the request's tiles; the piece's end
     const int32_t* table;
     int blk[kStages], in_page[kStages], nblk, nin = 0;
     // The page and the place in it of token `lane` of tile i, asked for one
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     auto open = [&] {
         n_all = tiles_of(tokens);
-        j1 = min(n_all, j + left);
+        j1 = min(min(n_all, j + left), j + kPiece * TW);
         table = p.block_table + (size_t)b * p.max_blocks;
 #pragma unroll
         for (int s = 0; s < kStages; ++s) lookup(j + tw + s * TW, blk[s], in_page[s]);
@@ -369,7 +376,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     open();
     copy_first();
-    for (bool first = true;; first = false) {
+    bool first = true;                          // the run's first segment
+    bool from0 = j == 0;                        // the segment begins with its request
+    bool joins = false, again = false;          // not the segment's, the run's first piece
+    for (;; again = true) {
         // ---- the query heads ------------------------------------------------------
         // head g's dimensions of chunk t: for word w, elements (0, 4) and (2, 6)
         // times 16 meet the low nibbles of the masks, (1, 5) and (3, 7) the high
@@ -589,19 +599,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             lookup(i + (kStages + 1) * TW, nblk, nin);
             st = st + 1 == kStages ? 0 : st + 1;
         }
-        // ---- the next segment's first copies, then this one's parts ---------------
+        // ---- the next piece's first copies, then what this one leaves -------------
         const int mb = b;
-        const bool all = j == 0 && j1 == n_all;
+        const unsigned slot = 2 * (r * p.Hkv + h) + (first ? 0 : 1);
+        const bool old = joins, ends = j1 == n_all, all = from0 && ends;
         left -= j1 - j;
-        j = 0;
         const bool more = left > 0;
+        joins = more && !ends;
+        j = joins ? j1 : 0;
         if (more) {
-            do {
-                tokens = tokens_of(p, ++b);
-            } while (tokens == 0);
+            if (!joins) {
+                first = false;
+                from0 = true;
+                do {
+                    tokens = tokens_of(p, ++b);
+                } while (tokens == 0);
+            }
             open();
         }
-        if (TW > 1 && !first) __syncthreads();  // the last segment's parts have been read
+        if (TW > 1 && again) __syncthreads();   // the last piece's parts have been read
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, o);
@@ -618,13 +634,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                          : __fmaf_rn(lo, 16777216.0f, e ? om1 : om0);
         };
         const PartView part = {p.part + plan_bytes(p.B) / 4, D, G};
-        const unsigned slot = 2 * (r * p.Hkv + h) + (first ? 0 : 1);
         if constexpr (TW == 1) {
+            float2 was[2];                      // (ref, sum) of the segment's pieces so far
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (old && 2 * t + e < G)
+                    was[e] = *reinterpret_cast<const float2*>(part.o(slot, 2 * t + e) + D);
+            __syncwarp();                       // read before lane g = 0 writes them again
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int hd = 2 * t + e;
                 if (hd >= G) continue;
-                const float L = e ? l1 : l0;
+                float L = e ? l1 : l0, ref = e ? ref1 : ref0, val[LD];
+#pragma unroll
+                for (int i = 0; i < LD; ++i) val[i] = value(e, i);
+                if (old) {
+                    const float* po = part.o(slot, hd);
+                    const float up = fmaxf(ref, was[e].x);
+                    const float f = half_step(ref - up), q = half_step(was[e].x - up);
+                    ref = up;
+                    L = __fmaf_rn(L * f, f, was[e].y * q * q);
+#pragma unroll
+                    for (int i = 0; i < LD; ++i)
+                        val[i] = __fmaf_rn(val[i] * f, f, po[LD * g + i] * q * q);
+                }
                 if (all) {
                     bf16* po = p.out + ((size_t)mb * p.Hq + (size_t)h * G + hd) * D + LD * g;
 #pragma unroll
@@ -633,8 +666,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const __nv_bfloat162 v = __floats2bfloat162_rn(
-                                __fdividef(value(e, i + 2 * k), L),
-                                __fdividef(value(e, i + 2 * k + 1), L));
+                                __fdividef(val[i + 2 * k], L), __fdividef(val[i + 2 * k + 1], L));
                             w[k] = *reinterpret_cast<const unsigned*>(&v);
                         }
                         *reinterpret_cast<int4*>(po + i) = make_int4(w[0], w[1], w[2], w[3]);
@@ -643,14 +675,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     float* po = part.o(slot, hd);
 #pragma unroll
                     for (int i = 0; i < LD; i += 4)
-                        *reinterpret_cast<float4*>(po + LD * g + i) = make_float4(
-                            value(e, i), value(e, i + 1), value(e, i + 2), value(e, i + 3));
+                        *reinterpret_cast<float4*>(po + LD * g + i) =
+                            make_float4(val[i], val[i + 1], val[i + 2], val[i + 3]);
                     if (g == 0) {
-                        po[D] = e ? ref1 : ref0;
+                        po[D] = ref;
                         po[D + 1] = L;
                     }
                 }
             }
+            __syncwarp();
             if (more) copy_first();
         } else {
             float* so = reinterpret_cast<float*>(smem + ring_bytes(D));   // [warp][8][D + 4]
@@ -669,6 +702,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     *reinterpret_cast<float4*>(po + i) = make_float4(
                         value(e, i), value(e, i + 1), value(e, i + 2), value(e, i + 3));
             }
+            if (old && threadIdx.x < HW * G) {
+                const int x = threadIdx.x / G, hd = threadIdx.x - x * G;
+                s_was[x * 8 + hd] =
+                    *reinterpret_cast<const float2*>(part.o(slot + 2 * (x - hw), hd) + D);
+            }
             if (more) copy_first();
             __syncthreads();
             for (int i = threadIdx.x; i < HW * G * D; i += kThreads) {
@@ -683,6 +721,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     const float f = half_step(sref[at] - top);
                     o = __fmaf_rn(f, f * so[at * (D + 4) + d], o);
                     L = __fmaf_rn(f, f * sl[at], L);
+                }
+                if (old) {
+                    const float2 was = s_was[x * 8 + hd];
+                    const float up = fmaxf(top, was.x);
+                    const float f = half_step(top - up), q = half_step(was.x - up);
+                    top = up;
+                    L = __fmaf_rn(L * f, f, was.y * q * q);
+                    o = __fmaf_rn(o * f, f, part.o(slot + 2 * (x - hw), hd)[d] * q * q);
                 }
                 const int hx = h - hw + x;
                 if (all) {
