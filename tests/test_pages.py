@@ -640,3 +640,39 @@ def test_lists_written_by_the_kernel_just_before():
         got[i] = s.gp[0][dst.long()]
     assert a8w8.read_device_errors() == 0
     assert np.array_equal(to_host(got), s.pool[0][src])
+
+
+class _FakeCache:
+    """What PagePool asks of a CUDA tensor."""
+
+    def __init__(self, page_bytes, blocks, ptr=FAKE):
+        self.bytes, self.ptr, self.device = page_bytes * blocks, ptr, "cuda:0"
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.bytes
+
+    def element_size(self):
+        return 1
+
+    def data_ptr(self):
+        return self.ptr
+
+
+def test_pool_refuses_what_its_operations_would(lib):
+    """Too many caches, pages that are not words, empty or misaligned caches and too many pages are
+    refused when the pool is made, not when an operation first meets them."""
+    c = lambda **k: _FakeCache(**{**dict(page_bytes=1024, blocks=8), **k})  # noqa: E731
+    assert len(a8w8.PagePool([c()] * 256, 8, 16).caches) == 256
+    a8w8.PagePool([c(page_bytes=20)], 8, 16)          # no whole words a token: refused by fork alone
+    for caches, blocks in (([c()] * 257, 8), ([c(), c(page_bytes=1022)], 8), ([c(page_bytes=0)], 8),
+                           ([c(ptr=FAKE + 4)], 8), ([c(ptr=0)], 8),
+                           ([c(page_bytes=1 << 31)], 8),
+                           ([c(page_bytes=4, blocks=1 << 21)], 1 << 21)):
+        with pytest.raises(a8w8.A8W8Error, match="PagePool: "):
+            a8w8.PagePool(caches, blocks, 16)

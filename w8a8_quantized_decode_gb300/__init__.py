@@ -680,9 +680,10 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
 
 class PagePool:
     """The caches that share one page numbering (K and V of every layer, or codes and scales):
-    each tensor of `caches` is num_blocks pages. Holds the caches and the arrays that the page
-    operations take; pages and counts live in the caller's tensors: block_table [B, max_blocks],
-    ctx_lens [B] and refcount [num_blocks], int32."""
+    each tensor of `caches` is num_blocks pages; at most 256 of them, each 16-byte aligned, with
+    pages of a multiple of 4 bytes (for paged_fork of 4 bytes a token). Holds the caches and the
+    arrays that the page operations take; pages and counts live in the caller's tensors:
+    block_table [B, max_blocks], ctx_lens [B] and refcount [num_blocks], int32."""
 
     def __init__(self, caches, num_blocks: int, page_size: int):
         self.caches = list(caches)
@@ -702,6 +703,10 @@ class PagePool:
         self.device = self.caches[0].device
         n = len(ptrs)
         self._args = ((_p * n)(*ptrs), (_sz * n)(*sizes), n)
+        # a copy of no pages: every rule that all page operations hold their caches to
+        status = lib().paged_copy_pages(*self._args, self.num_blocks, None, None, 0, None)
+        if status != OK:
+            raise A8W8Error(status, last_error().replace("paged_copy_pages", "PagePool"))
 
     def _here(self, what) -> int:
         dev = _device()
