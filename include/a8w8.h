@@ -432,7 +432,7 @@ size_t a8w8_attention_i4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_
  * carried out. ws: a8w8_pages_workspace_bytes(num_blocks, B, n) bytes of device
  * memory (n = 0 for paged_compact) that need no initialisation; calls that
  * share a workspace, or a pool, must not overlap on the GPU. num_blocks is
- * below 2^21 and max_blocks * page_size at most 2^24. */
+ * below 2^21, max_blocks * page_size at most 2^24 and n at most 2^30. */
 size_t a8w8_pages_workspace_bytes(int num_blocks, int B, int n);
 
 /* Copies page src[i] to page dst[i] in every cache, i < n. A pair with a

@@ -676,3 +676,33 @@ def test_pool_refuses_what_its_operations_would(lib):
                            ([c(page_bytes=4, blocks=1 << 21)], 1 << 21)):
         with pytest.raises(a8w8.A8W8Error, match="PagePool: "):
             a8w8.PagePool(caches, blocks, 16)
+
+
+def test_lists_too_long_are_refused(lib):
+    """Entries are counted in int with strides past the end, and copy units in 64 bits."""
+    n = (1 << 30) + 1
+    pool = ((ctypes.c_void_p * 1)(FAKE), (ctypes.c_size_t * 1)(1024), 1)
+    tables, ws = (FAKE, FAKE, FAKE), (FAKE, 1 << 50, None)
+    SHAPE = a8w8.ERR_UNSUPPORTED_SHAPE
+    assert lib.paged_copy_pages(*pool, 8, FAKE, FAKE, n, None) == SHAPE
+    assert lib.paged_fork(*pool, 8, 16, *tables, 4, 4, FAKE, FAKE, n, *ws) == SHAPE
+    assert lib.paged_reserve(FAKE, FAKE, 4, 4, 8, 16, FAKE, FAKE, n, *ws) == SHAPE
+    assert lib.paged_free(*tables, 4, 4, 8, FAKE, n, None) == SHAPE
+
+
+@gpu
+def test_copy_long_list():
+    """20,000 pairs of small pages, some in conflict, over many CTAs' shares."""
+    s = State(22, 2, 2, 50000, 1, (4, 1)).on_gpu()
+    p = s.rng.permutation(50000).astype(np.int32)
+    src, dst = p[:20000].copy(), p[20000:40000].copy()
+    dst[[17000, 9000, 19999]] = dst[[5, 3, 0]]             # destinations of earlier pairs
+    dst[4000] = src[15000]                                 # a page that is read
+    dst[7], src[8] = -1, 50000
+    a8w8.read_device_errors()
+    a8w8.paged_copy_pages(s.handle, _i32(src), _i32(dst))
+    ok = np.ones(20000, bool)
+    ok[[17000, 9000, 19999, 4000, 7, 8]] = False
+    for c in s.pool:
+        c[dst[ok]] = c[src[ok]]
+    s.check({"ALIAS", "BLOCK"})

@@ -288,6 +288,13 @@ a8w8_status cache_list(CacheList& c, void* const* caches, const size_t* page_byt
     return A8W8_OK;
 }
 
+// A request list's entries are counted in int, by strides past its end.
+a8w8_status check_list(int n, const char* what) {
+    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "%s: negative count", what);
+    if (n > (1 << 30)) return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: more than 2^30 entries", what);
+    return A8W8_OK;
+}
+
 a8w8_status check_pages_ws(int num_blocks, int B, int n, const void* ws, size_t ws_bytes,
                            const char* what) {
     const size_t need = pages_workspace_bytes(num_blocks, B, n);
@@ -1068,8 +1075,9 @@ a8w8_status paged_copy_pages(void* const* caches, const size_t* page_bytes, int 
                              int num_blocks, const int32_t* src, const int32_t* dst, int n,
                              void* stream) {
     CacheList c;
-    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_copy_pages: negative count");
-    a8w8_status s = cache_list(c, caches, page_bytes, num_caches, num_blocks, 1, "paged_copy_pages");
+    a8w8_status s = check_list(n, "paged_copy_pages");
+    if (s != A8W8_OK) return s;
+    s = cache_list(c, caches, page_bytes, num_caches, num_blocks, 1, "paged_copy_pages");
     if (s != A8W8_OK || n == 0) return s;
     if ((s = check_ptrs({src, dst}, "paged_copy_pages")) != A8W8_OK) return s;
     const Launch L = make_launch(stream, true);
@@ -1082,8 +1090,9 @@ a8w8_status paged_fork(void* const* caches, const size_t* page_bytes, int num_ca
                        int num_blocks, int page_size, int32_t* block_table, int32_t* ctx_lens,
                        int32_t* refcount, int B, int max_blocks, const int32_t* parents,
                        const int32_t* children, int n, void* ws, size_t ws_bytes, void* stream) {
-    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_fork: negative count");
-    a8w8_status s = check_pages(num_blocks, B, max_blocks, page_size, "paged_fork");
+    a8w8_status s = check_list(n, "paged_fork");
+    if (s != A8W8_OK) return s;
+    s = check_pages(num_blocks, B, max_blocks, page_size, "paged_fork");
     if (s != A8W8_OK) return s;
     CacheList c;
     s = cache_list(c, caches, page_bytes, num_caches, num_blocks, page_size, "paged_fork");
@@ -1101,8 +1110,9 @@ a8w8_status paged_fork(void* const* caches, const size_t* page_bytes, int num_ca
 a8w8_status paged_reserve(int32_t* block_table, int32_t* refcount, int B, int max_blocks,
                           int num_blocks, int page_size, const int32_t* rows,
                           const int32_t* tokens, int n, void* ws, size_t ws_bytes, void* stream) {
-    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_reserve: negative count");
-    a8w8_status s = check_pages(num_blocks, B, max_blocks, page_size, "paged_reserve");
+    a8w8_status s = check_list(n, "paged_reserve");
+    if (s != A8W8_OK) return s;
+    s = check_pages(num_blocks, B, max_blocks, page_size, "paged_reserve");
     if (s != A8W8_OK || n == 0) return s;
     if ((s = check_ptrs({block_table, refcount, rows, tokens}, "paged_reserve")) != A8W8_OK) return s;
     if ((s = check_pages_ws(num_blocks, B, n, ws, ws_bytes, "paged_reserve")) != A8W8_OK) return s;
@@ -1116,8 +1126,9 @@ a8w8_status paged_reserve(int32_t* block_table, int32_t* refcount, int B, int ma
 
 a8w8_status paged_free(int32_t* block_table, int32_t* ctx_lens, int32_t* refcount, int B,
                        int max_blocks, int num_blocks, const int32_t* rows, int n, void* stream) {
-    if (n < 0) return fail(A8W8_ERR_INVALID_ARG, "paged_free: negative count");
-    a8w8_status s = check_pages(num_blocks, B, max_blocks, 1, "paged_free");
+    a8w8_status s = check_list(n, "paged_free");
+    if (s != A8W8_OK) return s;
+    s = check_pages(num_blocks, B, max_blocks, 1, "paged_free");
     if (s != A8W8_OK || n == 0) return s;
     if ((s = check_ptrs({block_table, ctx_lens, refcount, rows}, "paged_free")) != A8W8_OK) return s;
     const Launch L = make_launch(stream, true);

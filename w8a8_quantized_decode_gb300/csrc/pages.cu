@@ -175,7 +175,9 @@ __global__ void __launch_bounds__(kCopyThreads)
     pdl_trigger();
     const unsigned U = c.first_unit[c.num_caches];
     const long total = (long)n * U;
-    const long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    const long share = total / gridDim.x, rest = total - share * gridDim.x;
+    const long u0 = share * blockIdx.x + min((long)blockIdx.x, rest);
+    const long u1 = u0 + share + (blockIdx.x < rest ? 1 : 0);
     if (u0 >= u1) return;
     const int p1 = (int)((u1 - 1) / U) + 1;
     for (int p0 = (int)(u0 / U); p0 < p1; p0 += kPairBatch) {
