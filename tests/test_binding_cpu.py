@@ -153,16 +153,18 @@ def test_private_torch_entries_have_public_stand_ins(what):
         calls.append(shape)
         t = torch.empty_strided(shape, strides, dtype=dtype)
         return NS(dtype=t.dtype, shape=t.shape, is_contiguous=t.is_contiguous,
-                  get_device=lambda: 3 if what == "there" else 0)
+                  get_device=lambda: 3 if there else 0)
 
+    there = what == "there"
     own = {"absent": NS(), "raises": NS(_dynamo=NS(guards=NS(_empty_strided_cuda=fail)),
-                                        _cuda_getCurrentRawStream=fail)}.get(what, NS(
-        _dynamo=NS(guards=NS(_empty_strided_cuda=private)),
-        _cuda_getCurrentRawStream=lambda dev: 77 if what == "there" else 0))
+                                        _cuda_getCurrentRawStream=fail, _cuda_getDevice=fail)}.get(
+        what, NS(_dynamo=NS(guards=NS(_empty_strided_cuda=private)),
+                 _cuda_getCurrentRawStream=lambda dev: 77 if there else 0,
+                 _cuda_getDevice=lambda: 3 if there else None))
     fake = NS(_C=own, bfloat16=torch.bfloat16, empty_strided=lambda *a, **k: public,
               cuda=NS(current_device=lambda: 3, current_stream=lambda *a: NS(cuda_stream=77)))
     h = a8w8._HostPath(fake)
-    assert h.stream(3) == 77
+    assert h.stream(3) == 77 and h.device() == 3
     rows = h.rows(5, 6, 7, None)
     assert (rows is public) == (what != "there")
     assert calls[1:] == ([(5, 6, 7)] if what == "there" else [])

@@ -526,10 +526,11 @@ def _typed(t, dtype, what, dev, numel=None):
 
 class _HostPath:
     """What a call of the 4-bit and page entries asks torch for between two kernel launches: the
-    current stream's handle and uninitialised bf16 rows. torch's own generated code has entries for
-    both that cost the host 0.1 and 0.9 us where the public ones cost 1.1 to 2.9 and 1.3 to 3.3
-    (write and read of one token: 18.5 us a pass, 35 by the public ones). They are not part of its
-    interface, so each is tried once, and the public way stands in where it is not what it was."""
+    current device, its stream's handle, and uninitialised bf16 rows. torch's own generated code has
+    entries for these that cost the host 0.1, 0.1 and 0.9 us where the public ones cost 0.2, 1.1 to
+    2.9 and 1.3 to 3.3 (write and read of one token: 18.5 us a pass, 35 by the public ones). They are
+    not part of its interface, so each is tried once, and the public way stands in where it is not
+    what it was."""
 
     def __init__(self, torch):
         own = getattr(torch, "_C", None)
@@ -556,7 +557,14 @@ class _HostPath:
                 self.stream = f
         except Exception:
             pass
-        self._bf16, self.device = torch.bfloat16, torch.cuda.current_device
+        self.device = torch.cuda.current_device
+        try:
+            f = own._cuda_getDevice
+            if f() == torch.cuda.current_device():
+                self.device = f
+        except Exception:
+            pass
+        self._bf16 = torch.bfloat16
 
     def rows(self, a, b, c, stream):
         """An uninitialised bf16 tensor [a, b, c] on the current CUDA device, for a call on
