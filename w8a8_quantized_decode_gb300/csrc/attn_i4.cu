@@ -188,6 +188,29 @@ struct PartView {
 };
 __host__ __device__ inline size_t plan_bytes(int B) { return ((size_t)B * 8 + 255) / 256 * 256; }
 
+// Adds a piece of a segment (o [D], ref, sum) to the part that holds the ones
+// before it, or writes the result of all: by one warp, where several share the
+// heads, and in a loop of its own. Within the CTA's join the same cost short
+// calls 2 to 4 % (64 requests of 256 tokens: 10.5 against 10.2 us).
+template <int D>
+__device__ __forceinline__ void add_piece(float* part, const float* piece, bf16* out, int lane) {
+    const float2 a = *reinterpret_cast<const float2*>(part + D);
+    const float2 b = *reinterpret_cast<const float2*>(piece + D);
+    const float up = fmaxf(a.x, b.x), f = half_step(a.x - up), q = half_step(b.x - up);
+    const float L = __fmaf_rn(a.y * f, f, b.y * q * q);
+    for (int d = lane; d < D; d += 32) {
+        const float o = __fmaf_rn(part[d] * f, f, piece[d] * q * q);
+        if (out) out[d] = f2bf(__fdividef(o, L));
+        else part[d] = o;
+    }
+    __syncwarp();                               // every lane has read (ref, sum)
+    if (lane == 0 && !out) {
+        part[D] = up;
+        part[D + 1] = L;
+    }
+    __syncwarp();
+}
+
 template <int D>
 struct Frag {
     static constexpr int KW = D / 32;   // 32-bit words of K codes per lane and token
@@ -207,7 +230,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __shared__ unsigned s_scan[kWarps];
     __shared__ unsigned s_first;
     __shared__ int s_b, s_tokens;
-    __shared__ float2 s_was[HW * 8];           // (ref, sum) of the segment's pieces so far
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv;
@@ -702,11 +724,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     *reinterpret_cast<float4*>(po + i) = make_float4(
                         value(e, i), value(e, i + 1), value(e, i + 2), value(e, i + 3));
             }
-            if (old && threadIdx.x < HW * G) {
-                const int x = threadIdx.x / G, hd = threadIdx.x - x * G;
-                s_was[x * 8 + hd] =
-                    *reinterpret_cast<const float2*>(part.o(slot + 2 * (x - hw), hd) + D);
-            }
             if (more) copy_first();
             __syncthreads();
             for (int i = threadIdx.x; i < HW * G * D; i += kThreads) {
@@ -722,24 +739,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     o = __fmaf_rn(f, f * so[at * (D + 4) + d], o);
                     L = __fmaf_rn(f, f * sl[at], L);
                 }
-                if (old) {
-                    const float2 was = s_was[x * 8 + hd];
-                    const float up = fmaxf(top, was.x);
-                    const float f = half_step(top - up), q = half_step(was.x - up);
-                    top = up;
-                    L = __fmaf_rn(L * f, f, was.y * q * q);
-                    o = __fmaf_rn(o * f, f, part.o(slot + 2 * (x - hw), hd)[d] * q * q);
-                }
                 const int hx = h - hw + x;
-                if (all) {
+                if (all && !old) {
                     p.out[((size_t)mb * p.Hq + (size_t)hx * G + hd) * D + d] = f2bf(__fdividef(o, L));
                 } else {
-                    float* po = part.o(slot + 2 * (x - hw), hd);
+                    float* po = old ? so + (x * 8 + hd) * (D + 4)   // this thread's own element
+                                    : part.o(slot + 2 * (x - hw), hd);
                     po[d] = o;
                     if (d == 0) {
                         po[D] = top;
                         po[D + 1] = L;
                     }
+                }
+            }
+            if (old) {
+                __syncthreads();
+#pragma unroll 1
+                for (int k = warp; k < HW * G; k += kWarps) {
+                    const int x = k / G, hd = k - x * G, hx = h - hw + x;
+                    bf16* out = all ? p.out + ((size_t)mb * p.Hq + (size_t)hx * G + hd) * D : nullptr;
+                    add_piece<D>(part.o(slot + 2 * (x - hw), hd), so + (x * 8 + hd) * (D + 4), out,
+                                 lane);
                 }
             }
         }
