@@ -222,11 +222,9 @@ struct __align__(16) ForkPlan {
     int part;       // tokens of the page in part
 };
 
-// Lists of up to this many entries, and tables of up to this many rows, are
-// planned in shared memory, a round trip to L2 less at each of the plan's
-// steps (fork of 64: 7.8 against 9.2 us); longer ones in the workspace.
-constexpr int kSharedList = 1024, kSharedRows = 2048;
-
+// The plan's lists stand in the workspace, whatever their length. In shared
+// memory (28 KB) each step is a round trip to L2 shorter, yet 64 forks with
+// their reserve took 58.9 us instead of 56.9.
 // The lowest entry of the list that names each row, for the rows named by
 // valid entries. All threads call it.
 template <typename Row>
@@ -242,18 +240,12 @@ __device__ __forceinline__ void first_entries(int* first, int B, int n, Row row)
 
 __global__ void __launch_bounds__(kPlanThreads)
     fork_plan_kernel(const PageTables t, int num_blocks, const int32_t* parents,
-                     const int32_t* children, int n, ForkPlan* plan, int* need_ws, int* first_ws,
+                     const int32_t* children, int n, ForkPlan* plan, int* need, int* first,
                      unsigned* err) {
     __shared__ int s[32];
-    __shared__ int s_need[kSharedList], s_first[kSharedRows];
-    __shared__ ForkPlan s_plan[kSharedList];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool small = n <= kSharedList;
-    int* need = small ? s_need : need_ws;
-    int* first = t.B <= kSharedRows ? s_first : first_ws;
-    ForkPlan* work = small ? s_plan : plan;
     const unsigned mask = first_mask(t.refcount, num_blocks);
     first_entries(first, t.B, n, [&](int i) {
         const int p = parents[i], c = children[i];
@@ -293,14 +285,14 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (bad && lane == 0) set_error(err, bad);
             if (bad || ctx == 0) f = {-1, -1, -1, 0};
         }
-        if (lane == 0) work[i] = f;
+        if (lane == 0) plan[i] = f;
     }
     __syncthreads();
     // ranks of the pages in part in list order, then the lowest free pages
     int want = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
         const int i = i0 + (int)threadIdx.x;
-        const bool w = i < n && work[i].src >= 0;
+        const bool w = i < n && plan[i].src >= 0;
         int total;
         const int rank = want + block_exclusive(w, s, total);
         if (w) need[rank] = i;
@@ -308,15 +300,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     __syncthreads();
     const int found = lowest_free(t.refcount, num_blocks, mask, want, s,
-                                  [&](int rank, int page) { work[need[rank]].fresh = page; });
+                                  [&](int rank, int page) { plan[need[rank]].fresh = page; });
     __syncthreads();
     for (int k = found + (int)threadIdx.x; k < want; k += kPlanThreads) {
-        work[need[k]] = {-1, -1, -1, 0};
+        plan[need[k]] = {-1, -1, -1, 0};
         if (k == found) set_error(err, kErrPages);
-    }
-    if (small) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kPlanThreads) plan[i] = work[i];
     }
 }
 
@@ -386,6 +374,11 @@ __global__ void __launch_bounds__(kCopyThreads)
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
+
+// Lists of up to this many entries, and tables of up to this many rows, are
+// planned in shared memory, a round trip to L2 less at each step (0.2 us of 59
+// for a fork of 64 and its reserve); longer ones in the workspace.
+constexpr int kSharedList = 1024, kSharedRows = 2048;
 
 __global__ void __launch_bounds__(kPlanThreads)
     reserve_kernel(const PageTables t, int num_blocks, const int32_t* rows, const int32_t* tokens,
