@@ -388,13 +388,17 @@ a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
  * and errors, with its own workspace (a8w8_attention_i4_workspace_bytes of
  * the same B, Hq, Hkv, D and max_blocks * page_size; its contents need no
  * initialisation), and in float32 arithmetic where the BF16 form is in
- * two-float: the scores are float32 sums of exact products, the softmax
- * weights times s are rounded to FP16 (2^-11 relative) before the products
- * with the codes, all sums are float32, and out is rounded to BF16 once. A
+ * two-float: q counts exactly except for elements below 2^-27 of the head's
+ * largest |q|, which are off by at most 2^-35 of that; the products of the
+ * scores are exact; the softmax weights times s are rounded to FP16 (2^-11
+ * relative) before the products with the codes; all sums are float32 (in
+ * pieces of at most 16384 tokens a warp, so that their roundings stay below
+ * 2^-11 of the terms at any size taken); and out is rounded to BF16 once. A
  * token whose block id is outside [0, num_blocks) counts as a row of zeros and
  * flags A8W8_DEVERR_BLOCK; a NaN row makes the heads that attend to it NaN,
  * and so does a query head with a NaN, an infinity or a value of 2^118 or
- * more. V rows with 0 < s < 2^-74 lose precision; constant rows (s = 0) of
+ * more; scores have to stay in float32's range, |softmax_scale| * |q| below
+ * 2^117. V rows with 0 < s < 2^-74 lose precision; constant rows (s = 0) of
  * 2^40 and more may overflow the sums. B is at most 65535, B * Hq at most
  * 2^24, num_blocks * page_size below 2^31 and B * max_blocks * page_size at
  * most 2^35. */

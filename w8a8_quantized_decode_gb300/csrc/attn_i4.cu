@@ -21,10 +21,11 @@
 // 32 tokens, 400 here.) The powers of two are taken back in the other operand
 // or the result:
 //   * q, scaled per head by a power of two to a maximum in [2^10, 2^11) (times
-//     16 beside the low nibbles): the eight significant bits of a BF16 are
-//     exact in FP16 down to 2^-35 of the head's largest |q|. Tokens are the
-//     rows, query heads the columns, so a group of up to 8 heads costs one
-//     instruction per 16 tokens and 16 dimensions.
+//     16 beside the low nibbles). FP16's last bit is 2^-24, so the eight
+//     significant bits of a BF16 are exact from 2^-17 up, 2^-27 of the head's
+//     largest |q|; a smaller value is off by at most 2^-25, 2^-35 of it. Tokens
+//     are the rows, query heads the columns, so a group of up to 8 heads costs
+//     one instruction per 16 tokens and 16 dimensions.
 //   * the weights p_t s_t, rounded to FP16: 2^-11 relative, beside the 2^-8 of
 //     the BF16 result. ref keeps the largest between 2^10 and 2^15, so that
 //     what FP16 cannot hold lies 2^-34 below it. One 8 x 8 transpose
@@ -49,12 +50,15 @@
 // tile's scores ahead of this one's weights (114), and barriers that keep an
 // SM's CTAs in step (116 to 129).
 //
-// Measured (40 query and 8 KV heads of 128, pages of 128 tokens): 64 requests
-// of 64 to 16384 tokens, 574 MB, 106 us (5.4 TB/s, 0.81 of the copy rate; the
-// copies alone take 94, the arithmetic alone about 109, and neither the
-// integer pipe, 49 % busy, nor HBM, 70 %, is full: their waits do not hide
-// each other entirely with three warps per scheduler); 16 requests of 64 to
-// 4096 tokens, 37 MB, 14 us; one of 256 tokens 3 us.
+// Measured (40 query and 8 KV heads of 128, pages of 128 tokens; a call queued
+// behind others): 64 requests of 64 to 16384 tokens, 574 MB, 106 us (5.4 TB/s,
+// 0.81 of the copy rate); 16 requests of 64 to 4096 tokens, 37 MB, 17 us. As
+// replayed graphs 108.7 and 18.7 us; there the same kernels without the
+// arithmetic take 99.5 and 15.5, without the copies behind the first two tiles
+// 86.1 and 18.5. So long calls are bound by their copies, and short ones by
+// the chain from the run search to the second kernel; neither the integer
+// pipe, 50 % busy, nor HBM, 69 %, is full with three warps per scheduler. One
+// request of 256 tokens: 4.5 us a kernel in a row of them.
 #include <limits.h>
 
 #include <algorithm>
@@ -156,9 +160,9 @@ __device__ __forceinline__ unsigned cta_exclusive(unsigned v, unsigned* s, unsig
 }
 
 // The runs: run r of E begins at tile floor(r T / E) of T = sum_b tiles(b),
-// request after request; the CTAs of a run's KV heads stand side by side (CTA
-// r Hkv + h), so that the sectors that hold several heads' (s, m) words and
-// the lines that hold their codes are read together.
+// request after request. Its HG = Hkv / HW CTAs stand side by side (CTA r HG +
+// k takes heads k HW to k HW + HW - 1), so that the sectors that hold several
+// heads' (s, m) words and the lines that hold their codes are read together.
 struct Runs {
     unsigned T, E, q, rem;   // T = q E + rem
     __device__ __forceinline__ Runs(unsigned tiles, unsigned runs) {
@@ -174,11 +178,12 @@ struct Runs {
 };
 
 // The workspace: what the second kernel has to join for each request, then
-// two parts per CTA of the first (a run ends inside at most two requests'
-// tiles), each G heads of o [D], ref and sum.
-//   plan.x = 2 (first run) + (0 if that run begins inside the request),
-//   plan.y = last run; the same run twice: nothing to join; plan.x = -1: no
-//   tokens.
+// two parts per run and KV head, each G heads of o [D], ref and sum: part 0 of
+// the run's first segment, part 1 of its last one, if that is another (those
+// between are whole requests, which only pass their pieces through part 1).
+//   plan.x = 2 (first run) + (0 if the request is that run's first segment,
+//   1 if it follows others), plan.y = last run; the same run twice: nothing to
+//   join; plan.x = -1: no tokens.
 struct PartView {
     float* base;
     int D, G;
@@ -846,7 +851,13 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
     }
 }
 
-// Contexts of at most this many tokens go to one CTA per (request, KV head).
+// Tables of at most this many tokens go to one CTA per (request, KV head),
+// without the run search and the second kernel. By the table's width, because
+// the contexts are on the device: a wider table may hold one long request
+// among short ones, which one CTA would take alone. Requests of 256 tokens, 40
+// query and 8 KV heads of 128: one 4.6 us against 7.3 by runs, 16 5.0 against
+// 8.3, 64 10.5 against 12.7, 256 29.8 against 29.3; at 1024 tokens each 8.6
+// against 7.6, 9.0 / 10.3, 21.5 / 21.9, 65.1 / 67.4.
 constexpr int kWholeCtx = 256;
 
 // KV heads that a CTA's warps stand for when it takes a run.
