@@ -393,7 +393,7 @@ a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
  * scores are exact; the softmax weights times s are rounded to FP16 (2^-11
  * relative) before the products with the codes; all sums are float32 (in
  * pieces of at most 16384 tokens a warp, so that their roundings stay below
- * 2^-11 of the terms at any size taken); and out is rounded to BF16 once. A
+ * 2^-10 of the terms at any size taken); and out is rounded to BF16 once. A
  * token whose block id is outside [0, num_blocks) counts as a row of zeros and
  * flags A8W8_DEVERR_BLOCK; a NaN row makes the heads that attend to it NaN,
  * and so does a query head with a NaN, an infinity or a value of 2^118 or
@@ -401,7 +401,8 @@ a8w8_status paged_kv_read_i4(const uint8_t* k_codes, const uint8_t* v_codes,
  * 2^117. V rows with 0 < s < 2^-74 lose precision; constant rows (s = 0) of
  * 2^40 and more may overflow the sums. B is at most 65535, B * Hq at most
  * 2^24, num_blocks * page_size below 2^31 and B * max_blocks * page_size at
- * most 2^35. */
+ * most 2^35, and at most 2^27 times max(1, 456 / n), n the first whole number
+ * of Hkv / 4, Hkv / 2 and Hkv (2^27 tokens for each part of the work). */
 a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
                                         const uint8_t* v_codes, const a8w8_bf16* k_meta,
                                         const a8w8_bf16* v_meta, const int32_t* block_table,

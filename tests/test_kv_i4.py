@@ -721,3 +721,14 @@ def test_attention_long_runs(Hkv, D, heads):
     want, bound = kv_i4.attention(q[:, at], *[c[:, list(heads)] for c in cache], bt, ctx, page)
     _check(got[:, at], want, bound)
     assert not to_host(got)[1].any() and a8w8.read_device_errors() == 0
+
+
+def test_attention_refuses_runs_that_are_too_long(lib):
+    """A run's sums are joined piece by piece: 2^27 tokens a run, of which there are as many as the
+    KV heads leave room for."""
+    def f(B, Hkv, max_blocks=4096, page=4096):
+        return lib.paged_decode_attention_i4kv(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, B, Hkv, Hkv,
+                                               64, page, max_blocks, 100, 0.1, FAKE, FAKE, 0, None)
+    for B, Hkv, ok in ((8, 1901, True), (9, 1901, False), (8, 1824, True), (9, 1824, False),
+                       (16, 912, True), (17, 912, False), (2048, 4, True), (2049, 4, False)):
+        assert f(B, Hkv) == (a8w8.ERR_WORKSPACE if ok else a8w8.ERR_UNSUPPORTED_SHAPE), (B, Hkv)

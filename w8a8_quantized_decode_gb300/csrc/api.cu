@@ -1038,6 +1038,8 @@ a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_cod
         return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
                     "more than 65535 requests, 2^24 (request, head) pairs, 2^31 - 1 slots or 2^35 "
                     "tokens");
+    if (attn_i4_run_tokens(B, Hkv, max_blocks * page_size) > (1L << 27) + 64)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "more than 2^27 tokens a run");
     a8w8_status s = check_ptrs({q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, out},
                                "paged_decode_attention_i4kv");
     if (s != A8W8_OK) return s;

@@ -135,7 +135,7 @@ __device__ __forceinline__ int tokens_of(const AttnI4Params& p, int b) {
     const int c = p.ctx_lens[b];
     return c < 0 || c > p.max_blocks * p.page ? 0 : c;
 }
-__device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kTile - 1) / kTile; }
+__host__ __device__ __forceinline__ int tiles_of(int tokens) { return (tokens + kTile - 1) / kTile; }
 
 // Exclusive sum of v over the CTA's threads (total in `total`); `s` is one
 // unsigned per warp.
@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- a segment: the run's tiles of one request, in pieces -----------------
     // A float32 sum of n like terms may be off by n 2^-24: where runs are long,
     // a segment is summed in pieces of kPiece tiles a warp (2048 weights a lane)
-    // that are joined in its part's place in the workspace. At the largest size
-    // taken, 2^35 tokens, 4600 pieces: 2^-13 + 2^-11.9 in all, beside the 2^-8
+    // that are joined in its part's place in the workspace. The longest run
+    // taken, 2^27 tokens, has 8192 pieces: 2^-13 + 2^-11 in all, beside the 2^-8
     // of the result's rounding. (One chain a run, 2^30 equal weights: 0.43 %.)
     int n_all, j1;                              // the request's tiles; the piece's end
     const int32_t* table;
@@ -863,7 +863,7 @@ constexpr int kWholeCtx = 256;
 // KV heads that a CTA's warps stand for when it takes a run.
 int heads_per_cta(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
 int runs_of(int B, int Hkv, int max_ctx) {
-    const long tiles = (long)B * ((max_ctx + kTile - 1) / kTile);
+    const long tiles = (long)B * tiles_of(max_ctx);
     const long fit = kMaxCtas / (Hkv / heads_per_cta(Hkv));
     return (int)std::max(1L, std::min((tiles + kMinTiles - 1) / kMinTiles, fit));
 }
@@ -908,6 +908,11 @@ cudaError_t launch_attention_i4_d(const AttnI4Params& p, const Launch& L) {
 }
 
 }  // namespace
+
+long attn_i4_run_tokens(int B, int Hkv, int max_ctx) {
+    const long tiles = (long)B * tiles_of(max_ctx);
+    return max_ctx <= kWholeCtx ? max_ctx : (tiles / runs_of(B, Hkv, max_ctx) + 1) * kTile;
+}
 
 size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx) {
     if (max_ctx <= kWholeCtx) return 0;

@@ -198,6 +198,8 @@ struct AttnI4Params {
     float* part;            // attn_i4_part_bytes
     unsigned* err;
 };
+// Tokens that one run may hold at most.
+long attn_i4_run_tokens(int B, int Hkv, int max_ctx);
 size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx);
 cudaError_t launch_attention_i4(const AttnI4Params& p, const Launch& L);
 
