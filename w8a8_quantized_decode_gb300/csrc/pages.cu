@@ -17,11 +17,11 @@
 // it takes: they are read by plain loads or from L2 after the wait, never by
 // the read-only path (no `const ... __restrict__` here), which asks for data
 // that nothing writes as long as the grid is there.
-// Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page): 96
-// copies 164 us (6.5 TB/s read and written, 0.98 of the copy rate);
-// compaction of some 150 of 260 live pages 251 us; 64 forks of 16 parents,
-// half a page each, 45 us after a plan of 5 (their 225 MB take 34 at the copy
-// rate).
+// Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page), each
+// launch by itself: 96 copies 164 us (6.5 TB/s read and written, 0.98 of the
+// copy rate); 64 forks of 16 parents, half a page each, 48.7 us (their 225 MB
+// take 34 at the copy rate) between a plan of 8 and a reserve of 9, 57 us for
+// all of them in a row.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -32,10 +32,12 @@ namespace {
 
 constexpr int kCopyThreads = 256;
 constexpr unsigned kUnitBytes = 16384;   // a copy unit: 4 vectors of 16 bytes per thread
-// CTAs per SM: 4 for whole pages (copy 172 us for 1.07 GB, 180 at 6 or 8); 6
-// for forks, whose partial pages leave some of a CTA's items empty (fork of 64
-// children and reserve 60.2 us, 61.6 at 8, 64.1 at 4).
-constexpr int kCopyCtasPerSm = 4, kForkCtasPerSm = 6;
+// CTAs per SM: 4 for whole pages (copy of 1.07 GB 170 us as a replayed graph,
+// 181 at 6 or 8; compaction 278, 290, 294); 8, all that fit, for forks, whose
+// partial pages leave some of a CTA's items empty (fork of 64 children and
+// reserve 57.7 us, 58.3 at 6, 65.9 at 4). Units of 8 KB: 198 and 69.8 us; of
+// 32 KB: 172 and 58.9.
+constexpr int kCopyCtasPerSm = 4, kForkCtasPerSm = 8;
 constexpr int kPlanThreads = 1024;
 constexpr unsigned kErrBlock = 0x2u, kErrCtx = 0x4u, kErrRow = 0x40u, kErrPages = 0x80u,
                    kErrAlias = 0x100u;
@@ -313,8 +315,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 // little of their page leave no CTA idle. Every cache counts as many chunks as
 // the largest page has (a power of two, 1 << shift): an empty item costs a few
 // instructions, where finding the cache of a unit costs every thread a search
-// through the list (159 warp instructions per unit and 53 us for 64 forks of a
-// 40-layer pool, 46 here). The tables and counts of fork i by CTA i mod grid.
+// through the list (159 warp instructions per unit: 64 forks of a 40-layer pool
+// took 7 us longer). The tables and counts of fork i by CTA i mod grid.
 __global__ void __launch_bounds__(kCopyThreads)
     fork_apply_kernel(const __grid_constant__ CacheList c, const PageTables t,
                       const int32_t* parents, const int32_t* children, int n,
