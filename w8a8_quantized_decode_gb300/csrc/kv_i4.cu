@@ -18,17 +18,19 @@
 // do: a row belongs to D / 16 lanes of 16 values in two 16-byte pieces, half
 // the lanes that one piece each would take (95 warp instructions per pair of
 // rows of 128 values instead of 147), and the pieces of one load or store lie
-// side by side (a lane's two pieces together made half sectors: read 22.8
-// against 15.6 us). K and V of the row are in flight together. 16384 tokens of
-// 8 heads of 128, write and read in turn: 170 MB in 28 us (6.1 TB/s, 0.91 of the
-// copy rate).
+// side by side (a lane's two pieces together made half sectors, and the read
+// half as long again). K and V of the row are in flight together. 16384 tokens
+// of 8 heads of 128, write and read in turn, calls queued: 170 MB in 28.2 us
+// (6.0 TB/s, 0.90 of the copy rate); as a replayed graph 30.8.
 #include "kernels.cuh"
 
 namespace a8w8 {
 
 namespace {
 
-constexpr int kI4Threads = 128;   // write + read of 16384 tokens 32.7 us; 33.6 at 256, 39 at 64
+// Write and read of 16384 tokens 30.8 us as a replayed graph, 32.8 at 256, 39 at
+// 64; of 2048 tokens 9.0, 10.3, 8.5.
+constexpr int kI4Threads = 128;
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(unsigned u) {
     return *reinterpret_cast<__nv_bfloat162*>(&u);
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kI4Threads)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         // streaming stores: the BF16 rows, four times the cache's bytes, leave L2
-        // to what is still to be read (32.7 -> 30.8 us)
+        // to what is still to be read (30.8 against 32.4 us)
         __stcs(reinterpret_cast<int4*>(k + (size_t)row * D + 8 * (j + LPR * i)), ko[i]);
         __stcs(reinterpret_cast<int4*>(v + (size_t)row * D + 8 * (j + LPR * i)), vo[i]);
     }
