@@ -732,3 +732,28 @@ def test_attention_refuses_runs_that_are_too_long(lib):
     for B, Hkv, ok in ((8, 1901, True), (9, 1901, False), (8, 1824, True), (9, 1824, False),
                        (16, 912, True), (17, 912, False), (2048, 4, True), (2049, 4, False)):
         assert f(B, Hkv) == (a8w8.ERR_WORKSPACE if ok else a8w8.ERR_UNSUPPORTED_SHAPE), (B, Hkv)
+
+
+@gpu
+def test_longest_chunk():
+    """16384 tokens of 8 heads of 128, pages in random order: codes, pairs and rows read back, bit
+    for bit."""
+    import torch
+    T, Hkv, D, page = 16384, 8, 128, 128
+    rng = np.random.default_rng(77)
+    k, v = synth.bf16_normal(78, (T, Hkv, D)), synth.bf16_normal(79, (T, Hkv, D), std=2.0)
+    blocks = rng.permutation(T // page + 3)
+    t = np.arange(T)
+    slots = (blocks[t // page] * page + t % page).astype(np.int32)
+    n = len(blocks) * page
+    dev = [torch.zeros((n, Hkv, w), dtype=dt, device="cuda") for w, dt in
+           ((D // 2, torch.uint8), (D // 2, torch.uint8), (2, torch.bfloat16), (2, torch.bfloat16))]
+    a8w8.read_device_errors()
+    a8w8.paged_kv_write_i4(to_dev(k), to_dev(v), to_dev(slots), *dev, page)
+    got = a8w8.paged_kv_read_i4(*dev, to_dev(slots), page)
+    assert a8w8.read_device_errors() == 0
+    for x, c, m, g in ((k, dev[0], dev[2], got[0]), (v, dev[1], dev[3], got[1])):
+        wc, wm = kv_i4.quant_rows(x)
+        assert np.array_equal(to_host(c)[slots], wc)
+        assert np.array_equal(kv_i4.bf16_to_f64(to_host(m)[slots]), kv_i4.bf16_to_f64(wm))
+        assert np.array_equal(to_host(g), _bf(kv_i4.dequant_rows(wc, wm).astype(np.float32)))

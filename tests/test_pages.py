@@ -706,3 +706,38 @@ def test_copy_long_list():
     for c in s.pool:
         c[dst[ok]] = c[src[ok]]
     s.check({"ALIAS", "BLOCK"})
+
+
+@gpu
+def test_fork_all_layers():
+    """64 forks of 16 rows through the 160 caches of a 40-layer 4-bit pool, then their pages for 160
+    more tokens: tables and counts as the oracle's, every child's tokens its parent's."""
+    import torch
+    L, N, page, Hkv, D, B, M = 40, 448, 128, 8, 128, 96, 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    codes = torch.randint(0, 256, (2 * L, N, page, Hkv, D // 2), dtype=torch.uint8, device="cuda",
+                          generator=g)
+    meta = torch.randint(-2 ** 15, 2 ** 15, (2 * L, N, page, Hkv, 2), dtype=torch.int16,
+                         device="cuda", generator=g)
+    pool = a8w8.PagePool([c[i] for i in range(2 * L) for c in (codes, meta)], N, page)
+    s = State(31, B, M, N, page, (1,))
+    _fill(s, np.arange(16), 100 + np.arange(16) * 173)
+    s.on_gpu()
+    p, c = np.arange(64, dtype=np.int32) % 16, 20 + np.arange(64, dtype=np.int32)
+    tokens = s.ctx[p] + 160
+    a8w8.read_device_errors()
+    a8w8.paged_fork(pool, *s.g, _i32(p), _i32(c))
+    a8w8.paged_reserve(pool, s.g[0], s.g[2], _i32(c), _i32(tokens))
+    assert pages.fork(s.pool, page, s.bt, s.ctx, s.ref, p, c) == set()
+    assert pages.reserve(page, s.bt, s.ref, c, tokens) == set()
+    for got, host in zip(s.g, (s.bt, s.ctx, s.ref)):
+        assert np.array_equal(to_host(got), host)
+    assert a8w8.read_device_errors() == 0 and s.counts_match()
+    for i in range(0, 64, 7):
+        n = int(s.ctx[c[i]])
+        if n % page == 0:
+            continue                                       # no page in part: all shared
+        own, of = s.bt[c[i]][n // page], s.bt[p[i]][n // page]
+        assert own != of
+        for x in (codes, meta):
+            assert torch.equal(x[:, int(own), :n % page], x[:, int(of), :n % page])

@@ -18,10 +18,10 @@
 // the read-only path (no `const ... __restrict__` here), which asks for data
 // that nothing writes as long as the grid is there.
 // Measured over the 160 caches of a 40-layer 4-bit pool (5.57 MB a page), each
-// launch by itself: 96 copies 164 us (6.5 TB/s read and written, 0.98 of the
-// copy rate); 64 forks of 16 parents, half a page each, 48.7 us (their 225 MB
-// take 34 at the copy rate) between a plan of 8 and a reserve of 9, 57 us for
-// all of them in a row.
+// launch by itself with cold caches: 96 copies 164 us (6.5 TB/s read and
+// written, 0.98 of the copy rate); 64 forks of 16 parents, half a page each, 45
+// us (their 214 MB take 32 at the copy rate) between a plan of 9 and a reserve
+// of 10; 57 for the three in a row.
 #include <algorithm>
 
 #include "kernels.cuh"
