@@ -50,10 +50,10 @@
 // tile's scores ahead of this one's weights (114), and barriers that keep an
 // SM's CTAs in step (116 to 129).
 //
-// Measured (40 query and 8 KV heads of 128, pages of 128 tokens; a call queued
-// behind others): 64 requests of 64 to 16384 tokens, 574 MB, 106 us (5.4 TB/s,
-// 0.81 of the copy rate); 16 requests of 64 to 4096 tokens, 37 MB, 17 us. As
-// replayed graphs 108.7 and 18.7 us; there the same kernels without the
+// Measured (40 query and 8 KV heads of 128, pages of 128 tokens; calls through
+// the binding one after the other): 64 requests of 64 to 16384 tokens, 574 MB,
+// 106 us (5.4 TB/s, 0.81 of the copy rate); 16 requests of 64 to 4096 tokens,
+// 37 MB, 18.5 us. As replayed graphs 108.7 and 18.7 us; there the same kernels without the
 // arithmetic take 99.5 and 15.5, without the copies behind the first two tiles
 // 86.1 and 18.5. So long calls are bound by their copies, and short ones by
 // the chain from the run search to the second kernel; neither the integer
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_i4_combine_kernel(const 
 // the contexts are on the device: a wider table may hold one long request
 // among short ones, which one CTA would take alone. Requests of 256 tokens, 40
 // query and 8 KV heads of 128: one 4.6 us against 7.3 by runs, 16 5.0 against
-// 8.3, 64 10.5 against 12.7, 256 29.8 against 29.3; at 1024 tokens each 8.6
+// 8.3, 64 10.2 against 12.7, 256 29.8 against 29.3; at 1024 tokens each 8.6
 // against 7.6, 9.0 / 10.3, 21.5 / 21.9, 65.1 / 67.4.
 constexpr int kWholeCtx = 256;
 
