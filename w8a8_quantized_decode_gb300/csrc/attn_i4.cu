@@ -53,12 +53,12 @@
 // Measured (40 query and 8 KV heads of 128, pages of 128 tokens; calls through
 // the binding one after the other): 64 requests of 64 to 16384 tokens, 574 MB,
 // 106 us (5.4 TB/s, 0.81 of the copy rate); 16 requests of 64 to 4096 tokens,
-// 37 MB, 18.5 us. As replayed graphs 108.7 and 18.7 us; there the same kernels without the
-// arithmetic take 99.5 and 15.5, without the copies behind the first two tiles
-// 86.1 and 18.5. So long calls are bound by their copies, and short ones by
-// the chain from the run search to the second kernel; neither the integer
-// pipe, 50 % busy, nor HBM, 69 %, is full with three warps per scheduler. One
-// request of 256 tokens: 4.5 us a kernel in a row of them.
+// 37 MB, 18.5 us. As replayed graphs 108.7 and 18.7 us; there the same kernels
+// without the arithmetic take 99.5 and 15.5, without the copies behind the
+// first two tiles 86.1 and 18.5. So long calls are bound by their copies, and
+// short ones by the chain from the run search to the second kernel; neither
+// the integer pipe, 50 % busy, nor HBM, 70 %, is full with three warps per
+// scheduler. One request of 256 tokens: 4.5 us a kernel in a row of them.
 #include <limits.h>
 
 #include <algorithm>
