@@ -414,6 +414,108 @@ a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_cod
 size_t a8w8_attention_i4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_ctx);
 
 /* ------------------------------------------------------------------------- */
+/* Chunks of new tokens                                                      */
+/* ------------------------------------------------------------------------- */
+
+/* The two steps of a layer that take a chunk of new tokens (a prompt or a part
+ * of one, drafted tokens, single ones, of one or many sequences) past a paged
+ * cache, for callers that run their own layers and for the cache forms that the
+ * layers here do not take ([SRV-52] "Current behavior": per-head QK norm and RoPE
+ * before the cache; the chunk's attention has no counterpart on the pages). A
+ * chunk's rows are projected (a8w8_linear: [Hq + 2 Hkv] heads of D), appended,
+ * and attend. */
+
+/* Row t of qkv ([T, ld] BF16, row stride ld elements, a multiple of 8 and at
+ * least (Hq + 2 Hkv) D) holds Hq query, Hkv key and Hkv value heads of the token
+ * at positions[t]. Query and key heads are normed where their weight ([D] BF16;
+ * nullable, each by itself: no norm) is given,
+ *   xn = bf16_rne( x / sqrt(mean(x^2) + eps) * w ),
+ * and rotated (rotate-half, table of a8w8_rope_table with max_pos rows),
+ *   y = bf16_rne( rotation of xn ),
+ * each rounding that of the exact value, as the layers have it. The queries go
+ * to q_rot ([T, Hq, D]; nullable: they are left out), keys and values to
+ * slot_mapping[t] of the cache (paged_kv_write's). positions[t] < 0 is a padded
+ * row: zeros in q_rot, nothing in the cache; so is positions[t] >= max_pos, which
+ * flags A8W8_DEVERR_POS. slot_mapping[t] < 0 leaves the cache alone; a slot >=
+ * num_blocks * page_size does, too, and flags A8W8_DEVERR_SLOT. The slots >= 0 of
+ * one call are distinct (of two tokens with one slot, either may be held, or a
+ * mixture). qkv and q_rot do not overlap. D is 64 or 128; T is at most 2^24,
+ * num_blocks * page_size below 2^31. */
+a8w8_status paged_kv_append(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                            const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                            const int32_t* positions, const float* rope, int max_pos,
+                            const int32_t* slot_mapping, a8w8_bf16* q_rot, a8w8_bf16* k_cache, a8w8_bf16* v_cache,
+                            int num_blocks, int page_size, void* stream);
+
+/* paged_kv_append into the INT8 cache (rows as paged_kv_write_i8 quantises them). */
+a8w8_status paged_kv_append_i8(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                               const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                               const int32_t* positions, const float* rope, int max_pos,
+                               const int32_t* slot_mapping, a8w8_bf16* q_rot, int8_t* k_codes,
+                               int8_t* v_codes, float* k_scale, float* v_scale,
+                               int num_blocks, int page_size, void* stream);
+
+/* paged_kv_append into the 4-bit cache (rows as paged_kv_write_i4 quantises them). */
+a8w8_status paged_kv_append_i4(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                               const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                               const int32_t* positions, const float* rope, int max_pos,
+                               const int32_t* slot_mapping, a8w8_bf16* q_rot, uint8_t* k_codes,
+                               uint8_t* v_codes, a8w8_bf16* k_meta, a8w8_bf16* v_meta,
+                               int num_blocks, int page_size, void* stream);
+
+/* Attention of a chunk over the paged BF16 cache. Request b's rows of q ([T, Hq,
+ * D]) are q_starts[b] to q_starts[b + 1] - 1 (q_starts [B + 1]); they are the
+ * last n_b tokens of its context: row i of them stands at position ctx_lens[b] -
+ * n_b + i and sees the tokens t up to and with its own (the cache holds them all):
+ *   out = sum_t softmax_t(softmax_scale * <q, K_t>) V_t,
+ * K_t and V_t at slot block_table[b][t / page] * page + t % page. A row before
+ * position 0 (n_b > ctx_lens[b]) sees nothing and gives zeros. Requests may have
+ * any number of rows, none among them; rows of q before q_starts[0] or from
+ * q_starts[B] on belong to no request, and their rows of out stay as they are.
+ * Products are exact, sums float32; the weights are rounded to BF16 (2^-8) before
+ * the product with V, out to BF16 once. A value that is infinite or NaN reaches
+ * the rows that see its token, no others; a NaN score makes its row NaN.
+ * ws: a8w8_chunk_attention_workspace_bytes of the same T, B, Hq, Hkv, D and
+ * max_blocks * page_size; its contents need no initialisation, and calls that
+ * share it must not overlap on the GPU. On the device: a context outside [0,
+ * max_blocks * page_size] counts as 0 and flags A8W8_DEVERR_CTX; q_starts that
+ * fall or leave [0, T] are clamped and flag A8W8_DEVERR_ROW (rows named by two
+ * requests get either's result); a block id outside [0, num_blocks) counts as
+ * rows of zeros and flags A8W8_DEVERR_BLOCK. D is 64 or 128, Hq / Hkv a whole
+ * number up to 8, max_blocks * page_size at most 2^24, T at most 2^24, B and Hq
+ * at most 65535, num_blocks * page_size below 2^31. */
+a8w8_status paged_chunk_attention_bf16(const a8w8_bf16* q, const a8w8_bf16* k_cache,
+                                       const a8w8_bf16* v_cache, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The same over the INT8 cache: K_t and V_t are codes times row scales. Arguments,
+ * workspace and errors as above. The products' operands are FP16: q and K of a
+ * run of 128 tokens count to 2^-28 of their largest |value| (a query head's, a
+ * run's), V to 2^-28 of the largest so far in its head, INT8 values and the
+ * weights besides to 2^-10 and 2^-11 of themselves. */
+a8w8_status paged_chunk_attention_i8kv(const a8w8_bf16* q, const int8_t* k_codes,
+                                       const int8_t* v_codes, const float* k_scale,
+                                       const float* v_scale, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The same over the 4-bit cache: code * s + m, rounded to FP16 once (2^-11). */
+a8w8_status paged_chunk_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
+                                       const uint8_t* v_codes, const a8w8_bf16* k_meta,
+                                       const a8w8_bf16* v_meta, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
+
+size_t a8w8_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_ctx);
+
+/* ------------------------------------------------------------------------- */
 /* Pages of a cache                                                          */
 /* ------------------------------------------------------------------------- */
 

@@ -108,6 +108,19 @@ _SIGNATURES = {
     "paged_decode_attention_i4kv": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
                                          _f, _p, _p, _sz, _p]),
     "a8w8_attention_i4_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "paged_kv_append": (_i, [_p, _i, _i, _i, _i, _i, _p, _p, _f, _p, _p, _i, _p, _p, _p, _p, _i, _i,
+                             _p]),
+    "paged_kv_append_i8": (_i, [_p, _i, _i, _i, _i, _i, _p, _p, _f, _p, _p, _i, _p, _p, _p, _p, _p, _p,
+                                _i, _i, _p]),
+    "paged_kv_append_i4": (_i, [_p, _i, _i, _i, _i, _i, _p, _p, _f, _p, _p, _i, _p, _p, _p, _p, _p, _p,
+                                _i, _i, _p]),
+    "paged_chunk_attention_bf16": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                        _p, _p, _sz, _p]),
+    "paged_chunk_attention_i8kv": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                                        _i, _f, _p, _p, _sz, _p]),
+    "paged_chunk_attention_i4kv": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                                        _i, _f, _p, _p, _sz, _p]),
+    "a8w8_chunk_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "a8w8_pages_workspace_bytes": (_sz, [_i, _i, _i]),
     "paged_copy_pages": (_i, [_p, _p, _i, _i, _p, _p, _i, _p]),
     "paged_fork": (_i, [_p, _p, _i, _i, _i, _p, _p, _p, _i, _i, _p, _p, _i, _p, _sz, _p]),
@@ -684,6 +697,147 @@ def paged_decode_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table
         None if ws is None else _typed(ws, torch.uint8, what, dev), 0 if ws is None else ws.numel(),
         _raw_stream(stream, dev)))
     return o
+
+
+def chunk_attention_workspace_bytes(T, B, Hq, Hkv, D, max_ctx) -> int:
+    return lib().a8w8_chunk_attention_workspace_bytes(T, B, Hq, Hkv, D, max_ctx)
+
+
+def _cache_rows(data, dtype, Hkv, D, page_size, what, dev):
+    """Pointers and page count of K and V rows [slots, Hkv, D] in whole pages."""
+    n = data[0].numel()
+    if Hkv <= 0 or D <= 0 or page_size <= 0 or n % (Hkv * D * page_size) or data[1].numel() != n:
+        raise A8W8Error(ERR_INVALID_ARG, f"{what}: caches [slots, {Hkv}, {D}] of whole pages of "
+                        f"{page_size} tokens expected")
+    return [_typed(t, dtype, what, dev) for t in data], n // (Hkv * D * page_size)
+
+
+def _chunk_attention(what, entry, q, ptrs, num_blocks, Hkv, dev, block_table, ctx_lens, q_starts,
+                     page_size, softmax_scale, ws, out, stream):
+    torch = _torch()
+    i32 = torch.int32
+    T, Hq, D = q.shape
+    B, max_blocks = block_table.shape
+    scale = (1.0 / D ** 0.5) if softmax_scale is None else softmax_scale
+    L = lib()
+    if ws is None:
+        need = L.a8w8_chunk_attention_workspace_bytes(T, B, Hq, Hkv, D, max_blocks * page_size)
+        ws = _empty(max(need, 16), torch.uint8, q.device, stream)
+    qp = _typed(q, torch.bfloat16, what, dev)
+    o = _host().rows(T, Hq, D, stream) if out is None else out
+    _check(getattr(L, entry)(
+        qp, *ptrs, _typed(block_table, i32, what, dev), _typed(ctx_lens, i32, what, dev, B),
+        _typed(q_starts, i32, what, dev, B + 1), T, B, Hq, Hkv, D, page_size, max_blocks, num_blocks,
+        scale, o.data_ptr() if out is None else _typed(o, torch.bfloat16, what, dev, T * Hq * D),
+        _typed(ws, torch.uint8, what, dev), ws.numel(), _raw_stream(stream, dev)))
+    return o
+
+
+def _kv_append(what, qkv, positions, slot_mapping, rope, ptrs, num_blocks, page_size, Hkv, D, q_norm_w,
+               k_norm_w, eps, q_out, stream, dev):
+    torch = _torch()
+    bf, i32 = torch.bfloat16, torch.int32
+    if qkv.dim() != 2 or qkv.dtype is not bf or qkv.get_device() != dev or qkv.stride(1) != 1:
+        raise A8W8Error(ERR_INVALID_ARG, f"{what}: qkv is a [T, (Hq + 2 Hkv) D] {bf} tensor on the "
+                        "current CUDA device, contiguous along its rows")
+    T, cols = qkv.shape
+    heads = cols // D
+    Hq = heads - 2 * Hkv
+    if cols % D or Hq < 0:
+        raise A8W8Error(ERR_INVALID_ARG, f"{what}: rows of {cols} elements are not Hq + 2 x {Hkv} "
+                        f"heads of {D}")
+    ld = qkv.stride(0) if T > 1 else cols
+    if rope.dim() != 2 or rope.shape[1] != 2 * D:
+        raise A8W8Error(ERR_INVALID_ARG, f"{what}: the rope table is [max_pos, {2 * D}]")
+    if q_out is None:
+        q_out = _host().rows(T, Hq, D, stream)
+        qp = q_out.data_ptr()
+    else:
+        qp = _typed(q_out, bf, what, dev, T * Hq * D)
+    norms = [None if w is None else _typed(w, bf, what, dev, D) for w in (q_norm_w, k_norm_w)]
+    _check(getattr(lib(), what)(
+        qkv.data_ptr(), T, Hq, Hkv, D, ld, *norms, eps, _typed(positions, i32, what, dev, T),
+        _typed(rope, torch.float32, what, dev), rope.shape[0], _typed(slot_mapping, i32, what, dev, T),
+        qp if T * Hq else None, *ptrs, num_blocks, page_size, _raw_stream(stream, dev)))
+    return q_out
+
+
+def paged_kv_append(qkv, positions, slot_mapping, rope, k_cache, v_cache, page_size, q_norm_w=None,
+                    k_norm_w=None, eps=1e-6, q_out=None, stream=None):
+    """A chunk's fused QKV rows [T, (Hq + 2 Hkv) D] bf16 (rows may be strided) past the per-head norm
+    (where a weight is given) and the rotation at positions [T] int32: queries to the returned
+    q_rot [T, Hq, D], keys and values to slot_mapping [T] int32 of the BF16 cache. `rope` is
+    a8w8_rope_table's."""
+    what, dev = "paged_kv_append", _device()
+    Hkv, D = k_cache.shape[-2:]
+    ptrs, num_blocks = _cache_rows((k_cache, v_cache), _torch().bfloat16, Hkv, D, page_size, what, dev)
+    return _kv_append(what, qkv, positions, slot_mapping, rope, ptrs, num_blocks, page_size, Hkv, D,
+                      q_norm_w, k_norm_w, eps, q_out, stream, dev)
+
+
+def paged_kv_append_i8(qkv, positions, slot_mapping, rope, k_codes, v_codes, k_scale, v_scale, page_size,
+                       q_norm_w=None, k_norm_w=None, eps=1e-6, q_out=None, stream=None):
+    """paged_kv_append into the INT8 cache."""
+    what, dev = "paged_kv_append_i8", _device()
+    Hkv, D = k_codes.shape[-2:]
+    ptrs, num_blocks = _cache_i8(k_codes, v_codes, k_scale, v_scale, Hkv, D, page_size, what, dev)
+    return _kv_append(what, qkv, positions, slot_mapping, rope, ptrs, num_blocks, page_size, Hkv, D,
+                      q_norm_w, k_norm_w, eps, q_out, stream, dev)
+
+
+def paged_kv_append_i4(qkv, positions, slot_mapping, rope, k_codes, v_codes, k_meta, v_meta, page_size,
+                       q_norm_w=None, k_norm_w=None, eps=1e-6, q_out=None, stream=None):
+    """paged_kv_append into the 4-bit cache."""
+    what, dev = "paged_kv_append_i4", _device()
+    Hkv, D = k_codes.shape[-2], 2 * k_codes.shape[-1]
+    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, D, page_size, what, dev)
+    return _kv_append(what, qkv, positions, slot_mapping, rope, ptrs, num_blocks, page_size, Hkv, D,
+                      q_norm_w, k_norm_w, eps, q_out, stream, dev)
+
+
+def paged_chunk_attention_bf16(q, k_cache, v_cache, block_table, ctx_lens, q_starts, page_size,
+                               softmax_scale=None, ws=None, out=None, stream=None):
+    """Attention of a chunk over the paged BF16 cache: request b's rows q_starts[b] to
+    q_starts[b + 1] - 1 of q [T, Hq, D] are the last tokens of its context, each seeing the tokens
+    up to its own. Rows of no request are left as they are."""
+    what, dev = "paged_chunk_attention_bf16", _device()
+    Hkv = k_cache.shape[-2]
+    ptrs, num_blocks = _cache_rows((k_cache, v_cache), _torch().bfloat16, Hkv, q.shape[-1],
+                                   page_size, what, dev)
+    return _chunk_attention(what, what, q, ptrs, num_blocks, Hkv, dev, block_table, ctx_lens,
+                            q_starts, page_size, softmax_scale, ws, out, stream)
+
+
+def _cache_i8(k_codes, v_codes, k_scale, v_scale, Hkv, D, page_size, what, dev):
+    """Pointers and page count of an INT8 cache: codes [slots, Hkv, D] int8 and row scales
+    [slots, Hkv] float32, in whole pages."""
+    torch = _torch()
+    ptrs, num_blocks = _cache_rows((k_codes, v_codes), torch.int8, Hkv, D, page_size, what, dev)
+    n = num_blocks * page_size * Hkv
+    return ptrs + [_typed(t, torch.float32, what, dev, n) for t in (k_scale, v_scale)], num_blocks
+
+
+def paged_chunk_attention_i8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, ctx_lens, q_starts,
+                               page_size, softmax_scale=None, ws=None, out=None, stream=None):
+    """paged_chunk_attention_bf16 over the INT8 cache (codes times row scales)."""
+    what, dev = "paged_chunk_attention_i8kv", _device()
+    Hkv = k_codes.shape[-2]
+    ptrs, num_blocks = _cache_i8(k_codes, v_codes, k_scale, v_scale, Hkv, q.shape[-1], page_size, what,
+                                 dev)
+    return _chunk_attention(what, what, q, ptrs, num_blocks, Hkv, dev, block_table, ctx_lens,
+                            q_starts, page_size, softmax_scale, ws, out, stream)
+
+
+def paged_chunk_attention_i4kv(q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens, q_starts,
+                               page_size, softmax_scale=None, ws=None, out=None, stream=None):
+    """paged_chunk_attention_bf16 over the 4-bit cache (codes [slots, Hkv, D / 2] uint8 and (s, m)
+    pairs [slots, Hkv, 2] bf16)."""
+    what, dev = "paged_chunk_attention_i4kv", _device()
+    Hkv = k_codes.shape[-2]
+    ptrs, num_blocks = _cache_i4(k_codes, v_codes, k_meta, v_meta, Hkv, q.shape[-1], page_size, what,
+                                 dev)
+    return _chunk_attention(what, what, q, ptrs, num_blocks, Hkv, dev, block_table, ctx_lens,
+                            q_starts, page_size, softmax_scale, ws, out, stream)
 
 
 class PagePool:

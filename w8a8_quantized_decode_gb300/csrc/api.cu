@@ -247,6 +247,113 @@ a8w8_status check_rows_i4(int T, int Hkv, int D, const char* what) {
     return A8W8_OK;
 }
 
+// A chunk's QKV rows into any cache form.
+a8w8_status kv_append(int kv, const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                      const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                      const int32_t* positions, const float* rope, int max_pos,
+                      const int32_t* slot_mapping, a8w8_bf16* q_rot, void* k, void* v, void* k_scale,
+                      void* v_scale, int num_blocks, int page_size, void* stream, const char* what) {
+    if (T < 0 || Hq < 0 || Hkv <= 0 || num_blocks <= 0 || page_size <= 0 || max_pos < 1)
+        return fail(A8W8_ERR_INVALID_ARG, "%s: bad size", what);
+    if ((q_norm_w || k_norm_w) && !(eps >= 0.0f))
+        return fail(A8W8_ERR_INVALID_ARG, "%s: eps must be >= 0", what);
+    if (D != 64 && D != 128)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %d not supported", what, D);
+    if (T > (1 << 24) || Hq > 65535 || Hkv > 65535 || (long long)num_blocks * page_size > INT32_MAX)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
+                    "%s: more than 2^24 rows, 65535 heads or 2^31 - 1 slots", what);
+    if (ld % 8 || ld < ((long long)Hq + 2 * Hkv) * D)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
+                    "%s: rows are a multiple of 8 elements apart, (Hq + 2 Hkv) D at least", what);
+    if (T == 0) return A8W8_OK;
+    a8w8_status s = check_ptrs({qkv, positions, rope, slot_mapping, k, v}, what);
+    if (s != A8W8_OK) return s;
+    if (kv != kKvBf16 && (s = check_ptrs({k_scale, v_scale}, what)) != A8W8_OK) return s;
+    if ((q_norm_w && !aligned16(q_norm_w)) || (k_norm_w && !aligned16(k_norm_w)) ||
+        (q_rot && !aligned16(q_rot)))
+        return fail(A8W8_ERR_INVALID_ARG, "%s: pointer not 16-byte aligned", what);
+    AppendParams p = {};
+    p.qkv = reinterpret_cast<const bf16*>(qkv);
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.ld = ld;
+    p.q_norm_w = reinterpret_cast<const bf16*>(q_norm_w);
+    p.k_norm_w = reinterpret_cast<const bf16*>(k_norm_w);
+    p.eps = eps;
+    p.positions = positions;
+    p.rope = rope;
+    p.max_pos = max_pos;
+    p.slot_mapping = slot_mapping;
+    p.q_out = reinterpret_cast<bf16*>(q_rot);
+    p.kv = kv;
+    p.k = k;
+    p.v = v;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_slots = (long)num_blocks * page_size;
+    p.err = device_error_word();
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_kv_append(p, L);
+    return e == cudaSuccess ? A8W8_OK : cuda_fail(e, what);
+}
+
+// The chunk attention over any cache form (the BF16 one has no scales).
+a8w8_status chunk_attention(int kv, const a8w8_bf16* q, const void* k, const void* v,
+                            const void* k_scale, const void* v_scale, const int32_t* block_table,
+                            const int32_t* ctx_lens, const int32_t* q_starts, int T, int B, int Hq,
+                            int Hkv, int D, int page_size, int max_blocks, int num_blocks,
+                            float softmax_scale, a8w8_bf16* out, void* ws, size_t ws_bytes,
+                            void* stream, const char* what) {
+    if (T < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || page_size <= 0 || max_blocks <= 0 || num_blocks <= 0)
+        return fail(A8W8_ERR_INVALID_ARG, "%s: bad size", what);
+    if (T == 0 || B == 0) return A8W8_OK;
+    if (D != 64 && D != 128)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: head_dim %d not supported", what, D);
+    if (Hq % Hkv || Hq / Hkv > 8)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: Hq/Hkv must be an integer <= 8", what);
+    if ((long long)max_blocks * page_size > (1 << 24))
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE, "%s: context longer than 2^24 tokens", what);
+    if (T > (1 << 24) || B > 65535 || Hq > 65535 || (long long)num_blocks * page_size > INT32_MAX)
+        return fail(A8W8_ERR_UNSUPPORTED_SHAPE,
+                    "%s: more than 2^24 rows, 65535 requests or heads, or 2^31 - 1 slots", what);
+    a8w8_status s = check_ptrs({q, k, v, block_table, ctx_lens, q_starts, out}, what);
+    if (s != A8W8_OK) return s;
+    if (kv != kKvBf16 && (s = check_ptrs({k_scale, v_scale}, what)) != A8W8_OK) return s;
+    const size_t need = attn_chunk_workspace_bytes(T, B, Hq, Hkv, D, max_blocks * page_size);
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(A8W8_ERR_WORKSPACE, "%s: workspace needs %zu bytes", what, need);
+    ChunkParams p = {};
+    p.q = reinterpret_cast<const bf16*>(q);
+    p.q_stride = Hq * D;
+    p.k = k;
+    p.v = v;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.ctx_lens = ctx_lens;
+    p.q_starts = q_starts;
+    p.T = T;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.page = page_size;
+    p.max_blocks = max_blocks;
+    p.num_blocks = num_blocks;
+    p.kv = kv;
+    p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+    p.out = reinterpret_cast<bf16*>(out);
+    p.ws = ws;
+    p.err = device_error_word();
+    const Launch L = make_launch(stream, true);
+    if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_attention_chunk(p, L);
+    return e == cudaSuccess ? A8W8_OK : cuda_fail(e, what);
+}
+
 // Page operations: the sizes shared by all of them.
 constexpr int kMaxPages = (1 << 21) - 1;   // ranks of 1024 rows' needs add up in 32 bits
 
@@ -1066,6 +1173,79 @@ a8w8_status paged_decode_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_cod
     if (L.num_sms <= 0) return fail(A8W8_ERR_CUDA, "no CUDA device");
     cudaError_t e = launch_attention_i4(a, L);
     return e == cudaSuccess ? A8W8_OK : cuda_fail(e, "paged_decode_attention_i4kv");
+}
+
+a8w8_status paged_kv_append(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                            const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                            const int32_t* positions, const float* rope, int max_pos,
+                            const int32_t* slot_mapping, a8w8_bf16* q_rot, a8w8_bf16* k_cache, a8w8_bf16* v_cache,
+                            int num_blocks, int page_size, void* stream) {
+    return kv_append(kKvBf16, qkv, T, Hq, Hkv, D, ld, q_norm_w, k_norm_w, eps, positions, rope, max_pos,
+                     slot_mapping, q_rot, k_cache, v_cache, nullptr, nullptr, num_blocks, page_size,
+                     stream, "paged_kv_append");
+}
+
+a8w8_status paged_kv_append_i8(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                               const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                               const int32_t* positions, const float* rope, int max_pos,
+                               const int32_t* slot_mapping, a8w8_bf16* q_rot, int8_t* k_codes,
+                               int8_t* v_codes, float* k_scale, float* v_scale,
+                               int num_blocks, int page_size, void* stream) {
+    return kv_append(kKvI8, qkv, T, Hq, Hkv, D, ld, q_norm_w, k_norm_w, eps, positions, rope, max_pos,
+                     slot_mapping, q_rot, k_codes, v_codes, k_scale, v_scale, num_blocks, page_size,
+                     stream, "paged_kv_append_i8");
+}
+
+a8w8_status paged_kv_append_i4(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int D, int ld,
+                               const a8w8_bf16* q_norm_w, const a8w8_bf16* k_norm_w, float eps,
+                               const int32_t* positions, const float* rope, int max_pos,
+                               const int32_t* slot_mapping, a8w8_bf16* q_rot, uint8_t* k_codes,
+                               uint8_t* v_codes, a8w8_bf16* k_meta, a8w8_bf16* v_meta,
+                               int num_blocks, int page_size, void* stream) {
+    return kv_append(kKvI4, qkv, T, Hq, Hkv, D, ld, q_norm_w, k_norm_w, eps, positions, rope, max_pos,
+                     slot_mapping, q_rot, k_codes, v_codes, k_meta, v_meta, num_blocks, page_size,
+                     stream, "paged_kv_append_i4");
+}
+
+size_t a8w8_chunk_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_ctx) {
+    if (T <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 8 || D <= 0 || max_ctx <= 0)
+        return 0;
+    return attn_chunk_workspace_bytes(T, B, Hq, Hkv, D, max_ctx);
+}
+
+a8w8_status paged_chunk_attention_bf16(const a8w8_bf16* q, const a8w8_bf16* k_cache,
+                                       const a8w8_bf16* v_cache, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+    return chunk_attention(kKvBf16, q, k_cache, v_cache, nullptr, nullptr, block_table, ctx_lens,
+                           q_starts, T, B, Hq, Hkv, D, page_size, max_blocks, num_blocks,
+                           softmax_scale, out, ws, ws_bytes, stream, "paged_chunk_attention_bf16");
+}
+
+a8w8_status paged_chunk_attention_i8kv(const a8w8_bf16* q, const int8_t* k_codes,
+                                       const int8_t* v_codes, const float* k_scale,
+                                       const float* v_scale, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+    return chunk_attention(kKvI8, q, k_codes, v_codes, k_scale, v_scale, block_table, ctx_lens,
+                           q_starts, T, B, Hq, Hkv, D, page_size, max_blocks, num_blocks,
+                           softmax_scale, out, ws, ws_bytes, stream, "paged_chunk_attention_i8kv");
+}
+
+a8w8_status paged_chunk_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
+                                       const uint8_t* v_codes, const a8w8_bf16* k_meta,
+                                       const a8w8_bf16* v_meta, const int32_t* block_table,
+                                       const int32_t* ctx_lens, const int32_t* q_starts, int T,
+                                       int B, int Hq, int Hkv, int D, int page_size,
+                                       int max_blocks, int num_blocks, float softmax_scale,
+                                       a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream) {
+    return chunk_attention(kKvI4, q, k_codes, v_codes, k_meta, v_meta, block_table, ctx_lens,
+                           q_starts, T, B, Hq, Hkv, D, page_size, max_blocks, num_blocks,
+                           softmax_scale, out, ws, ws_bytes, stream, "paged_chunk_attention_i4kv");
 }
 
 size_t a8w8_pages_workspace_bytes(int num_blocks, int B, int n) {

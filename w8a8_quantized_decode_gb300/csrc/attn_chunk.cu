@@ -1,0 +1,1508 @@
+// attn_chunk.cu -- attention of a chunk of new tokens over a paged KV cache.
+//
+// Request b's n new tokens are the last of its ctx cached ones; row i of them sees
+// keys t <= ctx - n + i. Per row and query head, over BF16, INT8 or 4-bit rows:
+//   s_t = scale q.k_t,  o = sum_t e^{s_t} v_t / sum_t e^{s_t}.
+//
+// What bounds it: the matrix units where a tile of rows is full (4 D operations a
+// row and key: a prompt), HBM where it is not (single tokens and drafts over long
+// contexts). One kernel covers both, since a batch mixes them:
+//   - A tile is 256 rows, the G query heads of one KV head times 256 / G tokens: a
+//     key read serves them all, and G = 1 to 8 fill the MMA's 128 lanes.
+//   - The tiles' blocks of 128 keys laid end to end are cut into equal parts, one
+//     a CTA (chunk_plan.cuh), wherever that falls. A tile in several parts leaves
+//     partials (O, maximum, sum, in float32), which a second kernel joins.
+//   - S = Q K^T and O = P V are tcgen05 products of 128 x 128 x 16 with the
+//     accumulators in tensor memory, P written back there over S as 16-bit. Two
+//     streams of 128 rows each take turns: one's softmax runs beside the other's
+//     products. A tile of 128 rows or fewer gives the streams every other block of
+//     keys instead, joined at its end.
+//   - Softmax: a thread a row, no shuffles. Exponentials are taken against the
+//     row's last reference first and its maximum beside them; only where that
+//     grew by more than 2^8 are O and the sum rescaled and they are taken again.
+//   - P is rounded to BF16 (a BF16 cache) or FP16: 2^-8 or 2^-11 of a weight, which
+//     the plain formula does as well. Sums, maxima and O are float32.
+//   - Sixteen warps: two warpgroups of softmax, one that fetches and lays out K and V
+//     (asynchronous copies of rows by the block table; a page may end anywhere), one
+//     thread that issues products, three warps for queries.
+// The order of the sums depends on the sizes and the grid alone: the same call gives
+// the same bits.
+//
+// Measured (GB300, a graph's launch, cold L2): a prompt of 16384 tokens, 40 heads on
+// 8, D 128: 2.0 ms, 1350 TFLOP/s of 1920 that a plain product reaches; 16 single
+// tokens with up to 4095 tokens before them: 39 us; 64 requests of 4 drafts over a 4-bit cache,
+// 230 us. A stream's chain S -> softmax -> P -> O of one block (about 3700 clocks of
+// two streams, 2048 of them products) bounds the long ones, starting up the short.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "chunk_plan.cuh"
+#include "kernels.cuh"
+#include "tc_common.cuh"
+
+namespace a8w8 {
+
+namespace {
+
+using namespace tc;
+using namespace chunk;
+
+constexpr unsigned kErrBlock = 0x2u, kErrCtx = 0x4u, kErrTimeout = 0x20u, kErrRow = 0x40u;
+
+constexpr int kStreamRows = 128;      // rows of a stream: the MMA's M, the tensor memory's lanes
+constexpr int kHalf = kKeys / 2;      // keys whose scores and weights go round at a time
+constexpr int kThreads = 512;         // warps 0-7 softmax, 8-11 keys and values, 12 MMA, 13-15 queries
+constexpr int kMaxParts = 152;
+constexpr int kMinUnits = 3;          // units of a part at least
+constexpr uint32_t kTmemCols = 512;   // S of stream s at 128 s, O of stream s at 256 + D s
+constexpr uint32_t kColO = 256;
+constexpr float kLazy = 8.0f;         // a row's reference may lag behind its maximum by 2^8
+
+template <int D>
+__host__ __device__ constexpr int tile_bytes() { return kKeys * D * 2; }
+template <int D, int KV>
+__host__ __device__ constexpr int num_stages() {
+    return (KV == kKvBf16 ? 5 : 3) * 128 / D;
+}
+// Tiles of codes on their way, INT8 and 4-bit caches: 48 KB of the shared memory.
+template <int D, int KV>
+__host__ __device__ constexpr int raw_tiles() {
+    return KV == kKvBf16 ? 0 : (KV == kKvI8 ? 3 : 6) * 128 / D;
+}
+
+struct Ctl {
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t q_full, q_free;
+    uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];   // of stream (and half block)
+    uint64_t o_free, merge, done;
+    long u0, u1;                   // this part's units
+    int b, h, i;                   // its first unit's request, KV head, tile
+    long first;                    // and that tile's first unit
+    int v_unit[2];                 // narrow tiles: a stream's O is in units of 2^this
+    int bad_tile;                  // the segment that bad[] is about, -1 for none
+    uint32_t tmem;
+    volatile int abort, never;     // never: always 0
+};
+
+constexpr int kFacRing = 8;
+
+template <int D, int KV>
+struct Lay {
+    static constexpr int kSt = num_stages<D, KV>();
+    static constexpr size_t q = 0;                                   // two tiles of 128 rows
+    static constexpr size_t kv = 2 * (size_t)tile_bytes<D>();
+    static constexpr size_t stat = kv + (size_t)kSt * tile_bytes<D>();   // (ref, sum) [2][128]
+    static constexpr size_t bad = stat + 2 * kStreamRows * 8;        // see BadValues
+    static constexpr size_t ctl = bad + D * 4;
+    static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see load_codes, load_q
+    static constexpr size_t raw = fac + (KV == kKvBf16 ? 0 : kFacRing * 8 + 2 * kTileRows * 4);
+    static constexpr size_t total = raw + (KV == kKvBf16 ? 0 : 48 * 1024);
+};
+
+// tc::mbar_wait with the limit (about two seconds) by the SM's clock: a third of
+// the code, which counts here, as the roles' loops have to share the
+// instruction cache.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
+        if (*abort || clock64() - t0 > 4000000000ll) return false;
+    } while (!mbar_try_wait(bar, parity));
+    return true;
+}
+
+// ex2 of the special function unit: 2^-22 relative, 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float a, float b) {   // a in the low half
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// Sixteen bytes to shared memory, zeros where `bytes` is 0.
+__device__ __forceinline__ void cp16z(uint32_t s, const void* g, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(bytes)
+                 : "memory");
+}
+// An arrival on the barrier once this thread's copies so far have landed (one of
+// the barrier's count). The copies write through the generic proxy: who waits
+// orders them before the tensor cores' reads by fence_async_shared().
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+template <int R>
+__device__ __forceinline__ void set_max_regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void set_max_regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+#define A8W8_R8(b) "=r"(r[b]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3]), "=r"(r[b + 4]), \
+                   "=r"(r[b + 5]), "=r"(r[b + 6]), "=r"(r[b + 7])
+// 64 consecutive columns of the warp's lanes, loaded and waited for in one statement.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+        "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+        "%62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : A8W8_R8(0), A8W8_R8(8), A8W8_R8(16), A8W8_R8(24), A8W8_R8(32), A8W8_R8(40), A8W8_R8(48),
+          A8W8_R8(56)
+        : "r"(taddr)
+        : "memory");
+}
+#undef A8W8_R8
+
+// Shared-memory descriptor of an operand whose rows are contiguous along M or
+// N (the values' rows: 64 dimensions of a token are 128 bytes), in the layout
+// of sw128_kmajor_desc: groups of 8 tokens 1024 bytes apart (stride offset),
+// the next 64 dimensions a whole sub-tile of 128 tokens further (leading
+// offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t next64) {
+    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)(next64 >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// idesc_f16_f32 with the operands' type (BF16: format 1) and, for B contiguous
+// along N, the transpose bit 16. Bit 13 negates A.
+constexpr uint32_t kNegateA = 1u << 13;
+__host__ __device__ constexpr uint32_t idesc_chunk(bool bf, int N, bool b_mn) {
+    return idesc_f16_f32(kStreamRows, N) | (bf ? (1u << 7) | (1u << 10) : 0u) |
+           (b_mn ? 1u << 16 : 0u);
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of 128 rows: sub-tiles of
+// 64 elements, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// A request as the tables give it: rows clamped to [0, T), no context where it
+// is out of range.
+__device__ __forceinline__ Req load_req(const ChunkParams& p, int b) {
+    Req r;
+    const int a = p.q_starts[b], e = p.q_starts[b + 1];
+    r.row0 = min(max(a, 0), p.T);
+    r.n = max(min(e, p.T) - r.row0, 0);
+    const int c = p.ctx_lens[b];
+    r.ctx = c < 0 || c > p.max_blocks * p.page ? 0 : c;
+    return r;
+}
+
+// A tile's blocks within the part.
+struct Seg {
+    int k;                // which segment of the part
+    int b, h, i;
+    int row0, ntok;       // the tile's first row of q and its tokens
+    int pos0;             // position of its first token
+    int kend;             // keys that its last token sees (0 or more)
+    int j0, j1;           // key blocks
+    bool head, tail;      // the tile begins, ends in this part
+    __device__ __forceinline__ int blocks() const { return j1 - j0; }
+};
+
+// Walks the part's tiles; every role of the CTA does, on its own.
+struct Walk {
+    const ChunkParams& p;
+    long u, u1, tile;      // next unit, end, first unit of the current tile
+    int b, h, i, tpt, nt, k;
+    Req r;
+    __device__ __forceinline__ Walk(const ChunkParams& p_, const Ctl& c)
+        : p(p_), u(c.u0), u1(c.u1), tile(c.first), b(c.b), h(c.h), i(c.i), k(0) {
+        tpt = tile_tokens(p.G);
+        if (u < u1) {
+            r = load_req(p, b);
+            nt = tiles_of(r, tpt);
+        }
+    }
+    __device__ __forceinline__ bool next(Seg& s) {
+        if (u >= u1) return false;
+        if (i == nt) {
+            i = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                do r = load_req(p, ++b);
+                while (r.n == 0);
+                nt = tiles_of(r, tpt);
+            }
+        }
+        const long keys = keys_of(r, tpt, i);
+        const int nb = blocks_of(keys);
+        s.k = k++;
+        s.b = b;
+        s.h = h;
+        s.i = i;
+        s.row0 = r.row0 + i * tpt;
+        s.ntok = tokens_in(r, tpt, i);
+        s.kend = keys > 0 ? (int)keys : 0;
+        s.pos0 = (int)(keys - s.ntok);
+        const long at = u - tile;                 // 0, or beyond the tile's own cost
+        s.head = at == 0;
+        s.j0 = s.head ? 0 : (int)at - kTileCost;
+        s.j1 = (int)min((long)nb, u1 - tile - kTileCost);
+        s.tail = s.j1 == nb;
+        u = tile + kTileCost + s.j1;
+        if (s.tail) {
+            tile = u;
+            ++i;
+        }
+        return true;
+    }
+};
+
+// What the second kernel needs of the tile that a part begins in.
+struct alignas(32) PlanEntry {
+    int inside;           // whether it begins inside one
+    int kf, kl;           // the parts that do in this tile; part kf - 1 holds the tile's begin
+    int row0, ntok;       // as Seg
+    int pos0, h, pad;
+};
+__host__ __device__ constexpr size_t plan_bytes() {
+    return (kMaxParts * sizeof(PlanEntry) + 255) / 256 * 256;
+}
+
+// Workspace: the plan, then per part two slots (0: the tile that it begins
+// inside, 1: the one whose begin it holds and whose end it does not): of `rows`
+// rows each (ref, sum), then o in groups of four columns, the rows of a group side by
+// side, as the threads that hold a row each write them.
+struct PartView {
+    float* base;
+    int D, rows;
+    __host__ __device__ static size_t floats(int D, int rows) { return (size_t)(rows + 3) / 4 * 4 * (D + 2); }
+    __device__ __forceinline__ int pad() const { return (rows + 3) / 4 * 4; }
+    __device__ __forceinline__ float* slot(int part, int which) const {
+        return base + (size_t)(part * 2 + which) * floats(D, rows);
+    }
+    __device__ __forceinline__ float2* stat(float* slot, int row) const {
+        return reinterpret_cast<float2*>(slot) + row;
+    }
+    __device__ __forceinline__ float4* o(float* slot, int row, int c) const {   // columns 4 c ..
+        return reinterpret_cast<float4*>(slot + 2 * pad()) + (size_t)c * pad() + row;
+    }
+};
+
+__device__ __forceinline__ void set_timeout(unsigned* err, volatile int* abort) {
+    *abort = 1;
+    set_error(err, kErrTimeout);
+}
+
+// ---------------------------------------------------------------------------
+// The part's units
+// ---------------------------------------------------------------------------
+
+// Exclusive sum of v over the CTA's threads; `s` is one long per warp.
+__device__ __forceinline__ long cta_exclusive(long v, long* s, long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s[warp] = x;
+    __syncthreads();
+    long before = 0;
+    total = 0;
+#pragma unroll 4
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s[w];
+        total += s[w];
+    }
+    return before + x - v;
+}
+
+// Finds this CTA's part: the requests' units added up, each thread a few; the
+// thread that holds the part's first unit (and the next part's) names the
+// request; half of the threads each then look for the tile, one tile a thread.
+// `scratch` is shared memory that nothing else uses yet.
+__device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* scratch) {
+    struct Hit {
+        long raw, tile;       // the unit, and the first one of its head, then of its tile
+        Req r;
+        int b, h, i;
+    };
+    long* sums = static_cast<long*>(scratch);
+    Hit* hits = reinterpret_cast<Hit*>(sums + kThreads / 32);
+    const int tpt = tile_tokens(p.G);
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    long mine = 0, last = 0;
+    Req r = {};
+    for (int b = b0; b < b1; ++b) {
+        r = load_req(p, b);
+        mine += last = head_units(r, tpt) * p.Hkv;
+        if (blockIdx.x == 0) {
+            const int c = p.ctx_lens[b], a = p.q_starts[b], e = p.q_starts[b + 1];
+            if (c < 0 || c > p.max_blocks * p.page) set_error(p.err, kErrCtx);
+            if (a < 0 || e < a || e > p.T) set_error(p.err, kErrRow);
+        }
+    }
+    long W;
+    const long before = cta_exclusive(mine, sums, W);
+    const Shares sh(W, gridDim.x, kMinUnits);
+    const int c = blockIdx.x;
+    if (c < sh.parts && mine > 0) {
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const long raw = sh.raw(c + k);
+            if (c + k == sh.parts || raw < before || raw - before >= mine) continue;
+            long at = before, n = last;
+            int b = b1 - 1;
+            if (per > 1) {
+                for (b = b0;; ++b) {
+                    r = load_req(p, b);
+                    n = head_units(r, tpt) * p.Hkv;
+                    if (raw - at < n) break;
+                    at += n;
+                }
+            }
+            const long head = head_units(r, tpt);
+            const int h = (int)div_long(raw - at, head);
+            hits[k].raw = raw;
+            hits[k].tile = at + h * head;
+            hits[k].r = r;
+            hits[k].b = b;
+            hits[k].h = h;
+        }
+    }
+    __syncthreads();
+    const int k = threadIdx.x / (kThreads / 2);
+    const bool searched = c + k < sh.parts;
+    int tile = -1;
+    if (searched) {
+        const Req& rk = hits[k].r;
+        const long at = hits[k].raw - hits[k].tile;
+        const int nt = tiles_of(rk, tpt);
+        for (int i = threadIdx.x % (kThreads / 2); i < nt; i += kThreads / 2) {
+            const long u = units_before(rk, tpt, i);
+            if (u <= at && at < u + tile_units(rk, tpt, i)) tile = i;
+        }
+    }
+    __syncthreads();
+    if (tile >= 0) {
+        Hit& x = hits[k];
+        x.i = tile;
+        x.tile += units_before(x.r, tpt, tile);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        PlanEntry e = {};
+        ctl.u0 = ctl.u1 = 0;
+        if (c < sh.parts) {
+            Hit x = hits[0];
+            const long end = x.tile + tile_units(x.r, tpt, x.i);
+            ctl.u0 = sh.snap(x.raw, x.tile, end);
+            ctl.u1 = W;
+            if (c + 1 < sh.parts) {
+                const Hit& y = hits[1];
+                ctl.u1 = sh.snap(y.raw, y.tile, y.tile + tile_units(y.r, tpt, y.i));
+            }
+            if (ctl.u0 > x.tile && ctl.u0 < end) {
+                const long keys = keys_of(x.r, tpt, x.i);
+                sh.inside(x.tile, end, c, e.kf, e.kl);
+                e.inside = 1;
+                e.row0 = x.r.row0 + x.i * tpt;
+                e.ntok = tokens_in(x.r, tpt, x.i);
+                e.pos0 = (int)(keys - e.ntok);
+                e.h = x.h;
+            } else if (ctl.u0 == end) {      // the next tile's begin
+                x.tile = end;
+                if (++x.i == tiles_of(x.r, tpt)) {
+                    x.i = 0;
+                    if (++x.h == p.Hkv) {
+                        x.h = 0;
+                        do ++x.b;
+                        while (x.b < p.B && load_req(p, x.b).n == 0);
+                    }
+                }
+            }
+            ctl.b = x.b;
+            ctl.h = x.h;
+            ctl.i = x.i;
+            ctl.first = x.tile;
+        }
+        reinterpret_cast<PlanEntry*>(p.ws)[c] = e;
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// Infinities and NaN among the values
+// ---------------------------------------------------------------------------
+
+// A product with V multiplies a weight of zero with the values of tokens that a
+// row does not see; that is nothing for finite values only. So the values of the
+// tokens that some rows of a tile see and others do not (those behind its first
+// token) are looked over as they are loaded: an infinity or NaN becomes zero and
+// is noted by its dimension as the first token that has a NaN, plus or minus
+// infinity there (ten bits each, counted from `base`); the rows that see it get
+// it back at the end. One segment at a time holds the notes.
+constexpr uint32_t kNoBad = 0x3FFFFFFFu;
+struct BadValues {
+    uint32_t* words;      // [D]
+    Ctl& ctl;
+    __device__ __forceinline__ static int base(const Seg& s) { return (s.pos0 + 1) & ~(kKeys - 1); }
+    // kind 0: NaN, 1: infinity, 2: minus infinity
+    __device__ __noinline__ void note(int seg, int token, int d, int kind) {
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            const int owner = atomicCAS(&ctl.bad_tile, -1, seg);
+            if (owner == -1 || owner == seg) break;
+            if (ctl.abort || globaltimer_ns() - t0 > 2000000000ull) return;   // a wait that gives up elsewhere
+        }
+        uint32_t old = words[d], was;
+        do {
+            was = old;
+            const uint32_t field = (was >> (10 * kind)) & 1023u;
+            if (field <= (uint32_t)token) return;
+            const uint32_t now = (was & ~(1023u << (10 * kind))) | ((uint32_t)token << (10 * kind));
+            old = atomicCAS(&words[d], was, now);
+        } while (old != was);
+    }
+    __device__ __forceinline__ bool any(int seg) const {
+        return *reinterpret_cast<volatile int*>(&ctl.bad_tile) == seg;
+    }
+    // Adds what the notes hold for a row that sees the tokens up to `last` (from base) to its
+    // dimensions [d0, d1): in `out`, or in `part` (groups of four, `step` floats apart).
+    template <int D>
+    __device__ __noinline__ void add(int last, int d0, int d1, bf16* out, float* part, int step) const {
+        for (int d = d0; d < d1; ++d) {
+            const uint32_t w = *reinterpret_cast<volatile uint32_t*>(&words[d]);
+            float x = 0.0f;
+            if ((int)(w & 1023u) <= last) x = __int_as_float(0x7FC00000);
+            if ((int)((w >> 10) & 1023u) <= last) x += INFINITY;
+            if ((int)((w >> 20) & 1023u) <= last) x -= INFINITY;
+            if (x == 0.0f) continue;
+            if (out) out[d] = f2bf(__bfloat162float(out[d]) + x);
+            else part[(size_t)(d >> 2) * step + (d & 3)] += x;
+        }
+    }
+    // By one warp, when all have read segment seg's notes.
+    __device__ __forceinline__ void clear(int seg, int D) {
+        if (!any(seg)) return;
+        for (int d = threadIdx.x & 31; d < D; d += 32) words[d] = kNoBad;
+        __threadfence_block();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) atomicExch(&ctl.bad_tile, -1);
+        __syncwarp();
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Keys and values: four warps, a warp the tokens 32 w .. 32 w + 31 of a block
+// ---------------------------------------------------------------------------
+
+// Where token t of request b lies, in two steps: its block id is read (no token
+// beyond kend, the tile's last key), and some work later made a slot, -1 for no
+// token and for a bad block id. Read and used at once, each costs its latency.
+struct Look {
+    int blk, off;         // blk -2: no token
+};
+__device__ __forceinline__ Look look_up(const ChunkParams& p, int b, int kend, int t) {
+    const unsigned k = (unsigned)t / (unsigned)p.page;
+    Look l = {-2, t - (int)k * p.page};
+    if (t < kend) l.blk = p.block_table[(size_t)b * p.max_blocks + k];
+    return l;
+}
+__device__ __forceinline__ int slot_of(const ChunkParams& p, const Look& l) {
+    if ((unsigned)l.blk < (unsigned)p.num_blocks) return l.blk * p.page + l.off;
+    if (l.blk != -2) set_error(p.err, kErrBlock);
+    return -1;
+}
+
+template <int D>
+__device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned char* kvp,
+                          BadValues bad) {
+    constexpr int kSt = num_stages<D, kKvBf16>();
+    constexpr int CPR = D / 8;            // 16-byte chunks of a row
+    constexpr int RPI = 32 / CPR;         // rows that one copy instruction covers
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+    const int c = lane % CPR, rl = lane / CPR;
+    unsigned cnt = 0;
+    Walk walk(p, ctl);
+    Seg s;
+    bool ok = true;
+    // a tile of values that is still to be looked over: its ring tile, segment, rows
+    // [lo, hi) and the first row's token from BadValues::base
+    struct { int st, seg, lo, hi, tok; } look = {-1, 0, 0, 0, 0};
+    auto look_over = [&]() {
+        unsigned char* tile = kvp + look.st * tile_bytes<D>();
+#pragma unroll 1
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const int row = 32 * w + i * RPI + rl;
+            if (row < look.lo || row >= look.hi) continue;
+            uint4& v = *reinterpret_cast<uint4*>(tile + tile_off(row, c));
+            const uint4 x = v;
+            auto odd = [](uint32_t u) { return (u & 0x7F80u) == 0x7F80u || (u & 0x7F800000u) == 0x7F800000u; };
+            if (!(odd(x.x) || odd(x.y) || odd(x.z) || odd(x.w))) continue;
+            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t h = (u[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                if ((h & 0x7F80u) != 0x7F80u) continue;
+                bad.note(look.seg, look.tok + row, 8 * c + e, h & 0x7Fu ? 0 : h & 0x8000u ? 2 : 1);
+                u[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+            }
+            v = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl.kv_full[look.st]);
+        look.st = -1;
+    };
+    while (ok && walk.next(s)) {
+        Look next = look_up(p, s.b, s.kend, s.j0 * kKeys + 32 * w + lane);
+        for (int j = s.j0; ok && j < s.j1; ++j) {
+            const int slot = slot_of(p, next);
+            if (j + 1 < s.j1) next = look_up(p, s.b, s.kend, (j + 1) * kKeys + 32 * w + lane);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                const int st = cnt % kSt;
+                if (cnt >= kSt && !mbar_try_wait(&ctl.kv_empty[st], (cnt / kSt - 1) & 1)) {
+                    if (look.st >= 0) {
+                        cp_async_wait_all();
+                        look_over();
+                    }
+                    if (!wait_bar(&ctl.kv_empty[st], (cnt / kSt - 1) & 1, &ctl.abort)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                const bf16* src = static_cast<const bf16*>(v ? p.v : p.k);
+                const uint32_t dst = kv + st * tile_bytes<D>();
+#pragma unroll
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int rr = i * RPI + rl, row = 32 * w + rr;
+                    const int sl = __shfl_sync(0xffffffffu, slot, rr);
+                    const bf16* g = src + ((size_t)max(sl, 0) * p.Hkv + s.h) * D + 8 * c;
+                    cp16z(dst + tile_off(row, c), g, sl >= 0 ? 16u : 0u);
+                }
+                cp_async_commit();
+                if (look.st >= 0) {              // behind this tile's copies, which go on
+                    cp_async_wait_group<1>();
+                    look_over();
+                }
+                const int lo = s.pos0 + 1 - j * kKeys, hi = s.kend - j * kKeys;
+                if (v == 1 && lo < kKeys && hi > max(lo, 0)) {
+                    look.st = st;
+                    look.seg = s.k;
+                    look.lo = lo;
+                    look.hi = hi;
+                    look.tok = j * kKeys - BadValues::base(s);
+                } else {
+                    cp_async_arrive(&ctl.kv_full[st]);
+                }
+                ++cnt;
+            }
+        }
+    }
+    if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
+    cp_async_wait_all();
+    if (look.st >= 0) look_over();
+}
+
+// INT8 and 4-bit rows become FP16 on the way into the ring: value 2^-E, E a
+// whole number per block for keys (the softmax takes the power of two back with
+// the scale) and for values one that only grows through a segment (O is in units
+// of it). A block's largest |value| comes to 16 at most, and of later blocks of
+// values to 2^15: FP16 holds a value to 2^-11 of itself, or 2^-28 of the largest
+// where that is more. 4-bit (s, m) pairs are BF16 and stay exact, an INT8 row's
+// scale is rounded to FP16 (2^-11), the value once more. (As BF16 rows, scores
+// would be off by 2^-8 of |q| |k|, several times what the weights' rounding
+// does.)
+//
+// The codes come by asynchronous copies into a ring of their own, each thread
+// the 16-byte pieces that it converts itself, so that it waits for nobody else.
+// Per block a lane also reads the pairs of a token in each quarter of the block,
+// its warp's own first (for the exponents; each warp all of them, again to wait
+// for no other).
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+// The power of two 2^e, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// e with |a| < 2^e, -100 at least; nothing (-1000) for zero, an infinity and NaN.
+__device__ __forceinline__ int exponent(float a) {
+    const int e = (__float_as_int(a) >> 23) & 255;
+    return e == 255 || a == 0.0f ? -1000 : max(e - 126, -100);
+}
+
+// The dimensions of value rows with an infinity or NaN, row r's in the mask of
+// `odd` (its slot's first code and pair in lane r), go to the notes; tok0 is row
+// 0's token from BadValues::base.
+template <int D, int KV>
+__device__ __noinline__ void note_rows(const void* codes, size_t row, uint32_t meta, unsigned odd, int tok0,
+                                       int seg, BadValues bad) {
+    const int lane = threadIdx.x & 31;
+    for (; odd; odd &= odd - 1) {
+        const int r = __ffs(odd) - 1;
+        const size_t at = __shfl_sync(0xffffffffu, row, r);
+        const uint32_t m = __shfl_sync(0xffffffffu, meta, r);
+        const float sc = KV == kKvI8 ? __uint_as_float(m) : __uint_as_float(m << 16);
+        const float mn = KV == kKvI8 ? 0.0f : __uint_as_float(m & 0xFFFF0000u);
+        for (int d = lane; d < D; d += 32) {
+            const size_t i = at * D + d;
+            const float code = KV == kKvI8 ? (float)static_cast<const int8_t*>(codes)[i]
+                                           : (float)(static_cast<const uint8_t*>(codes)[i / 2] >> (4 * (d & 1)) & 15);
+            const float val = __fmaf_rn(code, sc, mn);
+            bad.note(seg, tok0 + r, d, isnan(val) ? 0 : val < 0.0f ? 2 : 1);
+        }
+        __syncwarp();
+    }
+}
+
+template <int D, int KV>
+__device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, unsigned char* raw,
+                           float2* fac, BadValues bad) {
+    constexpr int kSt = num_stages<D, KV>(), kRaw = raw_tiles<D, KV>();
+    constexpr int RB = KV == kKvI8 ? D : D / 2;      // bytes of a row's codes
+    constexpr int LPR = RB / 16, RPI = 32 / LPR, NI = LPR;
+    constexpr int CPC = KV == kKvI8 ? 2 : 4;         // 16-byte chunks of FP16 per 16 bytes of codes
+    static_assert(kRaw * kKeys * RB == 48 * 1024, "the ring of codes");
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+    const int c = lane % LPR, rl = lane / LPR;
+    unsigned char* mine = raw + 16 * (threadIdx.x & 127);       // piece i of a tile at mine + 2048 i
+
+    // The part's blocks one after the other.
+    struct Blocks {
+        Walk walk;
+        Seg s;
+        int j;
+        bool live, first;
+        __device__ __forceinline__ Blocks(const ChunkParams& p, const Ctl& ctl) : walk(p, ctl) {
+            j = -1;
+            s.j1 = 0;
+            next();
+        }
+        __device__ __forceinline__ void next() {
+            first = false;
+            if (++j >= s.j1) {
+                live = walk.next(s);
+                j = s.j0;
+                first = true;
+            }
+        }
+    };
+    auto row_at = [&](int slot, int h) { return (size_t)max(slot, 0) * p.Hkv + h; };
+
+    // copies: tile by tile, keys then values; the block after is looked up ahead
+    Blocks in(p, ctl);
+    Look in_look = {-2, 0};
+    if (in.live) in_look = look_up(p, in.s.b, in.s.kend, in.j * kKeys + 32 * w + lane);
+    int in_slot = slot_of(p, in_look), in_h = in.s.h;
+    unsigned in_cnt = 0;
+    bool in_live = in.live;
+    if (in.live) in.next();
+    auto copy_tile = [&]() {
+        if (in_live) {
+            const unsigned char* codes = static_cast<const unsigned char*>(in_cnt & 1 ? p.v : p.k);
+            unsigned char* dst = mine + (in_cnt % kRaw) * (kKeys * RB);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int sl = __shfl_sync(0xffffffffu, in_slot, i * RPI + rl);
+                cp16z(smem_u32(dst + 2048 * i), codes + row_at(sl, in_h) * RB + 16 * c, sl >= 0 ? 16u : 0u);
+            }
+            if (in_cnt & 1) {
+                in_slot = slot_of(p, in_look);
+                in_live = in.live;
+                in_h = in.s.h;
+                if (in.live) in.next();
+            } else {
+                in_look.blk = -2;
+                if (in.live) in_look = look_up(p, in.s.b, in.s.kend, in.j * kKeys + 32 * w + lane);
+            }
+            ++in_cnt;
+        }
+        cp_async_commit();
+    };
+
+    auto find_slots = [&](const Blocks& x, Look (&look)[4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            look[q] = look_up(p, x.s.b, x.live ? x.s.kend : 0, x.j * kKeys + 32 * ((w + q) & 3) + lane);
+    };
+    // the slot of the own quarter's token
+    auto load_meta = [&](const Look (&look)[4], int h, uint32_t (&km)[4], uint32_t (&vm)[4]) {
+        int first = -1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int slot = slot_of(p, look[q]);
+            if (q == 0) first = slot;
+            km[q] = vm[q] = 0u;
+            if (slot >= 0) {
+                km[q] = __ldcg(static_cast<const uint32_t*>(p.k_scale) + row_at(slot, h));
+                vm[q] = __ldcg(static_cast<const uint32_t*>(p.v_scale) + row_at(slot, h));
+            }
+        }
+        return first;
+    };
+    // whether a row holds an infinity or NaN
+    auto odd_row = [](uint32_t m) {
+        if (KV == kKvI8) return (m & 0x7F800000u) == 0x7F800000u;
+        return (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u;
+    };
+    // e with |value| <= 2^e for the finite rows, from the exponents: 127 s, or |m| + 15 s at
+    // most twice the larger of |m| and 16 s; -100 at least, -1000 for rows of zeros alone
+    auto block_exponent = [&](const uint32_t (&m)[4]) {
+        unsigned top = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            unsigned u = m[q] & 0x7FFFFFFFu;
+            if (KV == kKvI4) {
+                const unsigned sc = (m[q] & 0x7FFFu) << 16;
+                u = max(m[q] & 0x7FFF0000u, sc ? sc + (4u << 23) : 0u);
+            }
+            top = max(top, odd_row(m[q]) ? 0u : u);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        return top == 0 ? -1000 : min(max((int)(top >> 23) - 126 + (KV == kKvI8 ? 7 : 1), -100), 131);
+    };
+    // Ring tile cnt from the thread's pieces of codes (pairs `meta` of the lanes' tokens) times `up`.
+    unsigned cnt = 0;
+    auto convert = [&](uint32_t meta, float up) {
+        const unsigned char* src = mine + (cnt % kRaw) * (kKeys * RB);
+        unsigned char* tile = kvp + (cnt % kSt) * tile_bytes<D>();
+        // (not unrolled further: the instruction cache is what these warps wait for most)
+#pragma unroll 2
+        for (int i = 0; i < NI; ++i) {
+            const int rr = i * RPI + rl, row = 32 * w + rr;
+            const uint32_t m = __shfl_sync(0xffffffffu, meta, rr);
+            const uint4 r = *reinterpret_cast<const uint4*>(src + 2048 * i);
+            const uint32_t word[4] = {r.x, r.y, r.z, r.w};
+            uint4 o[CPC];
+            uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+            if (KV == kKvI8) {
+                const __half2 sc = __float2half2_rn(__uint_as_float(m) * up);
+                const __half2 off = as_half2(0x64806480u);           // 1152
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t u = word[g] ^ 0x80808080u;        // 1024 + 128 + code
+                    ow[2 * g] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4140)), off), sc));
+                    ow[2 * g + 1] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4342)), off), sc));
+                }
+            } else {
+                const float sf = __uint_as_float(m << 16) * up, mf = __uint_as_float(m & 0xFFFF0000u) * up;
+                const __half2 sc = __floats2half2_rn(sf, sf * 0.0625f), mn = __float2half2_rn(mf);
+                const __half2 off = as_half2(0x64006400u);           // 1024
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // 1024 + low nibble, 1024 + 16 times the high one
+                        const uint32_t u = __byte_perm(word[g], 0x64646464u, 0x4040 + 0x0101 * e) & 0x64F0640Fu;
+                        ow[4 * g + e] = as_u32(__hfma2(__hsub2(as_half2(u), off), sc, mn));
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < CPC; ++e) {
+                // lanes of one store in different banks: the second half of a row's lanes in
+                // another order (the sub-tiles lie a multiple of all banks apart)
+                const bool turn = D == 128 && (KV == kKvI8 ? c >> 2 : c >> 1);
+                const int f = KV == kKvI8 ? e ^ 1 : e ^ 2;
+                *reinterpret_cast<uint4*>(tile + tile_off(row, CPC * c + (turn ? f : e))) = turn ? o[f] : o[e];
+            }
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl.kv_full[cnt % kSt]);
+        ++cnt;
+    };
+    auto room = [&]() {
+        return cnt < kSt || wait_bar(&ctl.kv_empty[cnt % kSt], (cnt / kSt - 1) & 1, &ctl.abort);
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < kRaw - 1; ++i) copy_tile();
+    // pairs: block x's in registers, those of the next on their way, the slots of the one after
+    Blocks x(p, ctl), ahead(p, ctl);
+    if (!x.live) {
+        cp_async_wait_all();
+        return;
+    }
+    unsigned blk = 0;
+    int ev = -1000;
+    Look look[4];
+    uint32_t km[4], vm[4];
+    find_slots(ahead, look);
+    int was = load_meta(look, ahead.s.h, km, vm), own = -1;   // the own quarter's slots of x, the next
+    ahead.next();
+    find_slots(ahead, look);
+    bool ok = true;
+    for (;;) {
+        // the exponents, before the keys are handed over: the softmax reads them behind those
+        int ek = block_exponent(km);
+        ek = ek == -1000 ? 0 : ek;
+        const int e = block_exponent(vm);
+        if (x.first) ev = e == -1000 ? -100 : e;
+        else if (e > ev + 11) ev = e;
+        if (threadIdx.x % 128 == 0)
+            fac[blk % kFacRing] = make_float2(pow2(min(ek - 4, 127)), __int_as_float(min(ev - 4, 127)));
+        uint32_t pair_of = km[0], vmine = vm[0];
+        float up = pow2(max(4 - ek, -126));
+        if (ahead.live) {
+            own = load_meta(look, ahead.s.h, km, vm);
+            ahead.next();
+            find_slots(ahead, look);
+        }
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+            copy_tile();
+            cp_async_wait_group<kRaw - 1>();
+            if (!(ok = room())) break;
+            convert(pair_of, up);
+            // the values: rows that are not finite, of tokens that some rows of the tile do not see
+            const int t = x.j * kKeys + 32 * w + lane;
+            const unsigned odd = __ballot_sync(0xffffffffu, t > x.s.pos0 && t < x.s.kend && odd_row(vmine));
+            if (v == 0 && odd) {
+                note_rows<D, KV>(p.v, row_at(was, x.s.h), vmine, odd,
+                                 x.j * kKeys + 32 * w - BadValues::base(x.s), x.s.k, bad);
+                if (odd >> lane & 1) vmine = 0u;       // zeros
+            }
+            pair_of = vmine;
+            up = pow2(max(4 - ev, -126));
+        }
+        if (!ok) break;
+        ++blk;
+        was = own;
+        x.next();
+        if (!x.live) break;
+    }
+    if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
+    cp_async_wait_all();
+}
+
+// ---------------------------------------------------------------------------
+// Queries: three warps
+// ---------------------------------------------------------------------------
+
+template <int D>
+__device__ void load_q_bf16(const ChunkParams& p, Ctl& ctl, uint32_t q) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
+    const int c = lane % CPR, rl = lane / CPR;
+    const int inv = (65536 + p.G - 1) / p.G;      // r / G = r inv >> 16 for r < 256
+    Walk walk(p, ctl);
+    Seg s;
+    for (int k = 0; walk.next(s); ++k) {
+        if (k > 0 && !wait_bar(&ctl.q_free, (k - 1) & 1, &ctl.abort)) {
+            if (!ctl.abort) set_timeout(p.err, &ctl.abort);
+            break;
+        }
+        const int rows = s.ntok * p.G;
+        const int all = rows <= kStreamRows ? kStreamRows : kTileRows;
+        for (int r0 = RPI * w; r0 < all; r0 += 3 * RPI) {
+            const int r = r0 + rl;
+            const int t = (r * inv) >> 16;
+            const bool live = r < rows;
+            const bf16* g = p.q + (size_t)(s.row0 + (live ? t : 0)) * p.q_stride +
+                            (s.h * p.G + (live ? r - t * p.G : 0)) * D + 8 * c;
+            cp16z(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
+        }
+        cp_async_arrive(&ctl.q_full);
+    }
+    cp_async_wait_all();
+}
+
+// The same as FP16 times a power of two per row that brings its largest |q| to
+// 16 at most; unit [2][256] holds what a row is in units of, by the segment's
+// parity (the softmax has read a segment's before the next but one is written).
+template <int D>
+__device__ void load_q_f16(const ChunkParams& p, Ctl& ctl, unsigned char* q, float* unit) {
+    constexpr int CPR = D / 8, RPI = 32 / CPR, U = 4;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
+    const int c = lane % CPR, rl = lane / CPR;
+    const int inv = (65536 + p.G - 1) / p.G;
+    Walk walk(p, ctl);
+    Seg s;
+    for (int k = 0; walk.next(s); ++k) {
+        if (k > 0 && !wait_bar(&ctl.q_free, (k - 1) & 1, &ctl.abort)) {
+            if (!ctl.abort) set_timeout(p.err, &ctl.abort);
+            break;
+        }
+        const int rows = s.ntok * p.G;
+        const int all = rows <= kStreamRows ? kStreamRows : kTileRows;
+        for (int r0 = RPI * U * w; r0 < all; r0 += 3 * RPI * U) {
+            int4 raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + RPI * u + rl, t = (r * inv) >> 16;
+                raw[u] = make_int4(0, 0, 0, 0);
+                if (r < rows)
+                    raw[u] = ld_cg_v4(p.q + (size_t)(s.row0 + t) * p.q_stride + (s.h * p.G + r - t * p.G) * D + 8 * c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + RPI * u + rl;
+                float x[8];
+                unpack8(raw[u], x);
+                int e = -1000;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e = max(e, exponent(x[i]));
+#pragma unroll
+                for (int o = CPR / 2; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+                e = e == -1000 ? 0 : e;
+                const float up = pow2(min(4 - e, 127));
+                uint4 v;
+                v.x = f16x2_of(x[0] * up, x[1] * up);
+                v.y = f16x2_of(x[2] * up, x[3] * up);
+                v.z = f16x2_of(x[4] * up, x[5] * up);
+                v.w = f16x2_of(x[6] * up, x[7] * up);
+                if (r >= all) continue;
+                *reinterpret_cast<uint4*>(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c)) = v;
+                if (c == 0) unit[(k & 1) * kTileRows + r] = pow2(e - 4);
+            }
+        }
+        fence_async_shared();
+        mbar_arrive(&ctl.q_full);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Matrix products: one warp, of which one thread issues them
+//
+// Scores of a block overwrite the weights of the stream's block before, which
+// the product issued just before reads: products of one thread go through the
+// SM's tensor pipe in the order of their issue. A commit covers all products
+// before it, so that of a block's scores tells the softmax that the product with
+// V before them is done, too.
+// True in one thread of the (converged) warp. Under this predicate the compiler
+// knows that a single thread is active, and hands the products' descriptors to
+// the uniform registers that the instruction takes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
+template <int D, int KV>
+__device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t kv, BadValues bad) {
+    constexpr int kSt = num_stages<D, KV>();
+    constexpr bool kBf = KV == kKvBf16;
+    constexpr uint32_t kIdS = idesc_chunk(kBf, kKeys, false), kIdO = idesc_chunk(kBf, D, true);
+    const uint32_t tmem = ctl.tmem, id_s = kIdS | (p.negate ? kNegateA : 0u);   // a negative scale
+    unsigned cnt = 0;                       // tiles of the ring before this segment
+    unsigned np[2] = {0, 0};                // blocks of weights waited for, per stream
+    bool ok = true;
+
+    auto wait_full = [&](unsigned t) {
+        if (!wait_bar(&ctl.kv_full[t % kSt], (t / kSt) & 1, &ctl.abort)) return false;
+        fence_async_shared();
+        return true;
+    };
+    // S of stream st from query tile buf and ring tile t
+    auto qk = [&](int st, int buf, unsigned t, bool free, bool q_last) {
+        const uint64_t a = sw128_kmajor_desc(q + buf * tile_bytes<D>());
+        const uint64_t b = sw128_kmajor_desc(kv + (t % kSt) * tile_bytes<D>());
+        if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t o = (uint64_t)((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                mma_f16(tmem + 128 * st, a + o, b + o, id_s, k > 0);
+            }
+            mma_commit(&ctl.s_full[st]);
+            if (free) mma_commit(&ctl.kv_empty[t % kSt]);
+            if (q_last) mma_commit(&ctl.q_free);
+        }
+        __syncwarp();
+    };
+    // O of stream st from its weights and ring tile t
+    auto pv = [&](int st, unsigned t, bool add, bool free, bool done) {
+        const uint64_t b = sw128_mnmajor_desc(kv + (t % kSt) * tile_bytes<D>(), kKeys * 128);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            if (!wait_bar(&ctl.p_full[st][part], np[st] & 1, &ctl.abort)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 4 * part; k < 4 * part + 4; ++k)
+                    mma_f16_ta(tmem + kColO + D * st, tmem + 128 * st + kHalf * (k >> 2) + 8 * (k & 3),
+                               b + (uint64_t)(k * 2048 >> 4), kIdO, add || k > 0);
+                if (part == 0) mma_commit(&ctl.pv_half[st]);
+                if (part == 1) {
+                    if (free) mma_commit(&ctl.kv_empty[t % kSt]);
+                    if (done) mma_commit(&ctl.pv_done[st]);
+                }
+            }
+            __syncwarp();
+        }
+        ++np[st];
+        return true;
+    };
+
+    Walk walk(p, ctl);
+    Seg s;
+    for (int k = 0; ok && walk.next(s); ++k) {
+        const int nb = s.blocks();
+        const bool narrow = s.ntok * p.G <= kStreamRows;
+        ok = wait_bar(&ctl.q_full, k & 1, &ctl.abort) && wait_full(cnt);
+        if (!ok) break;
+        // the segment before has left the tensor memory (and the notes on its values)
+        auto free_o = [&]() {
+            if (k == 0) return true;
+            if (!wait_bar(&ctl.o_free, (k - 1) & 1, &ctl.abort)) return false;
+            bad.clear(k - 1, D);
+            return true;
+        };
+        if (!narrow) {
+            qk(0, 0, cnt, false, false);
+            qk(1, 1, cnt, true, nb == 1);
+            ok = free_o();
+            for (int j = 0; ok && j < nb; ++j) {
+                const unsigned tv = cnt + 2 * j + 1, tk = tv + 1;
+                const bool more = j + 1 < nb;
+                ok = wait_full(tv) && (!more || wait_full(tk)) && pv(0, tv, j > 0, false, !more);
+                if (ok && more) qk(0, 0, tk, false, false);
+                ok = ok && pv(1, tv, j > 0, true, !more);
+                if (ok && more) qk(1, 1, tk, true, j + 2 == nb);
+            }
+        } else {
+            // block j goes to stream j % 2
+            for (int j = 0; ok && j < min(2, nb); ++j) {
+                ok = wait_full(cnt + 2 * j);
+                if (ok) qk(j, 0, cnt + 2 * j, true, j + 1 == nb);
+            }
+            ok = ok && free_o();
+            for (int j = 0; ok && j < nb; ++j) {
+                const unsigned tv = cnt + 2 * j + 1, tk = tv + 3;
+                const bool more = j + 2 < nb;
+                ok = wait_full(tv) && pv(j & 1, tv, j >= 2, true, !more) && (!more || wait_full(tk));
+                if (ok && more) qk(j & 1, 0, tk, true, j + 3 == nb);
+            }
+        }
+        cnt += 2 * nb;
+    }
+    if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
+    // no product may still run when the tensor memory is given back
+    if (elect_one()) mma_commit(&ctl.done);
+    __syncwarp();
+    wait_bar(&ctl.done, 0, &ctl.never);
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and results: a row per thread, four warps per stream
+// ---------------------------------------------------------------------------
+
+// 32 columns of the warp's 32 rows, a row per lane, times the rows' inv, as BF16
+// to the rows' addresses (null: none). Four lanes exchange their rows' four
+// 16-byte pieces first, so that a store covers 64 bytes of eight rows; of the
+// lanes' own rows it wrote half sectors.
+__device__ __forceinline__ void store32(bf16* out, const float (&o)[32], float inv) {
+    const int lane = threadIdx.x & 31;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i].x = bf16x2_of(o[8 * i] * inv, o[8 * i + 1] * inv);
+        v[i].y = bf16x2_of(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+        v[i].z = bf16x2_of(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+        v[i].w = bf16x2_of(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+    }
+    auto swap = [&](uint4& a, uint4& b, int bit) {
+        // lanes with the bit give a and keep b, the others give b and keep a
+        const bool up = lane & bit;
+        uint4 give = up ? a : b;
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+        if (up) a = give;
+        else b = give;
+    };
+    swap(v[0], v[1], 1);
+    swap(v[2], v[3], 1);
+    swap(v[0], v[2], 2);
+    swap(v[1], v[3], 2);
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // v[i]: piece lane % 4 of row 4 (lane / 4) + i
+        const unsigned long long to = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
+        if (to) reinterpret_cast<uint4*>(to)[lane & 3] = v[i];
+    }
+}
+
+template <int D, int KV>
+__device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const float2* fac, BadValues bad) {
+    constexpr bool kBf = KV == kKvBf16;
+    constexpr float kUp = kBf ? 0.0f : 7.0f;   // weights are 2^(x - ref + kUp)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int st = warp >> 2;                   // stream
+    const int lr = 32 * (warp & 3) + lane;      // lane of the tensor memory
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = ctl.tmem + lanes + 128 * st, to = ctl.tmem + lanes + kColO;
+    const int inv_g = (65536 + p.G - 1) / p.G;
+    const PartView parts = {p.part, D, p.part_rows};
+    unsigned ns = 0, nm = 0, nv[2] = {0, 0};    // blocks of scores, merges, tiles of either stream
+    unsigned blk = 0;                           // blocks before this segment
+    bool ok = true;
+    Walk walk(p, ctl);
+    Seg s;
+    for (int k = 0; ok && walk.next(s); ++k) {
+        const int nb = s.blocks();
+        const int rows = s.ntok * p.G;
+        const bool narrow = rows <= kStreamRows;
+        const int row = narrow ? lr : kStreamRows * st + lr;
+        const int tok = (row * inv_g) >> 16;
+        const bool live = row < rows;
+        const int limit = live ? s.pos0 + tok : -1;        // last key that the row sees
+        float ref = -INFINITY, sum = 0.0f;
+        float f = p.scale_log2, row_scale = f;     // a block's scores to units of log2
+        int unit = 0;                              // O is in units of 2^unit
+        const int step = narrow ? 2 : 1;
+        const int mine = narrow ? (nb + 1 - st) / 2 : nb;  // blocks of this stream
+        for (int j = 0; j < mine; ++j) {
+            const int key0 = (s.j0 + (narrow ? st : 0) + j * step) * kKeys;
+            ok = wait_bar(&ctl.s_full[st], ns & 1, &ctl.abort);
+            if (!ok) break;
+            ++ns;
+            tc_fence_after();
+            int v_unit = 0;
+            if (!kBf) {
+                const float2 e = fac[(blk + (narrow ? st : 0) + j * step) % kFacRing];
+                if (j == 0) row_scale *= reinterpret_cast<const float*>(fac + kFacRing)[(k & 1) * kTileRows + row];
+                f = fmaxf(row_scale * e.x, 1e-37f);      // (as the launcher's, see there)
+                v_unit = __float_as_int(e.y);
+                if (j == 0) unit = v_unit;
+            }
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t v[kHalf], w[kHalf / 2];
+                tmem_ld64(ts + kHalf * hf, v);
+                if (key0 + kHalf * hf + kHalf - 1 > s.pos0) {
+                    const int lim = limit - key0 - kHalf * hf;
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) v[c] = c > lim ? 0xFF800000u : v[c];
+                }
+                float top, part;
+                for (;;) {
+                    const float base = kUp - (ref == -INFINITY ? 0.0f : ref);
+                    const f32x2 f2v = pair(f, f), b2v = pair(base, base);
+                    f32x2 acc[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+                    float mx[2] = {__uint_as_float(v[0]), __uint_as_float(v[1])};
+#pragma unroll
+                    for (int c = 0; c < kHalf / 2; ++c) {
+                        const float x0 = __uint_as_float(v[2 * c]), x1 = __uint_as_float(v[2 * c + 1]);
+                        if (c) mx[c & 1] = fmaxf(mx[c & 1], fmaxf(x0, x1));
+                        else mx[0] = fmaxf(x0, x1);
+                        float a, b;
+                        split(fma2(pair(x0, x1), f2v, b2v), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        acc[c & 1] = add2(acc[c & 1], pair(a, b));
+                        w[c] = kBf ? bf16x2_of(a, b) : f16x2_of(a, b);
+                    }
+                    float s0, s1;
+                    split(add2(acc[0], acc[1]), s0, s1);
+                    part = s0 + s1;
+                    top = fmaxf(mx[0], mx[1]) * f;
+                    const bool regrown = !kBf && hf == 0 && unit != v_unit;   // the same in all threads
+                    if (!__any_sync(0xffffffffu, top > ref + kLazy) && !regrown) break;
+                    const float up = fmaxf(ref, top);
+                    const float a = ref == -INFINITY ? 0.0f : ex2(ref - up);
+                    const float ao = kBf ? a : a * pow2(max(unit - v_unit, -126));   // v_unit only grows
+                    unit = v_unit;
+                    if (hf == 1 && !wait_bar(&ctl.pv_half[st], (ns - 1) & 1, &ctl.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (j > 0 || hf == 1) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + D * st + c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ao);
+                            tmem_st32(to + D * st + c, o);
+                        }
+                    }
+                    sum *= a;
+                    ref = up;
+                }
+                sum += part;
+                tmem_st32(ts + kHalf * hf, w);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full[st][hf]);
+            }
+            if (!ok) break;
+        }
+        if (!ok) break;
+
+        // ---- results ----
+        // A wide tile's stream holds its rows' O. Of a narrow tile both streams hold the same
+        // rows, and each warp joins half of the columns: o u0 of one and o u1 of the other.
+        const bool two = narrow && nb > 1;
+        const bool none = limit < 0;
+        float up = ref, all = sum, u0 = 1.0f, u1 = 0.0f;
+        if (narrow) {
+            // (read until o_free: a stream with blocks comes here again only after that)
+            if (st == 0 || two) {
+                stat[kStreamRows * st + lr] = make_float2(ref, sum);
+                ctl.v_unit[st] = unit;             // (the same in all threads)
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.merge);
+            ok = wait_bar(&ctl.merge, nm & 1, &ctl.abort);
+            ++nm;
+        }
+        ok = ok && (narrow && st == 1 || wait_bar(&ctl.pv_done[st], nv[st] & 1, &ctl.abort));
+        if (narrow) ok = ok && (st == 0 || wait_bar(&ctl.pv_done[0], nv[0] & 1, &ctl.abort)) &&
+                         (!two || wait_bar(&ctl.pv_done[1], nv[1] & 1, &ctl.abort));
+        ++nv[0];
+        if (!narrow || two) ++nv[1];
+        if (!ok) break;
+        tc_fence_after();
+        int first_col = 0, last_col = D;
+        uint32_t o_col = to + D * st;
+        if (narrow) {
+            const float2 e0 = stat[lr], e1 = two ? stat[kStreamRows + lr] : make_float2(-INFINITY, 0.0f);
+            up = fmaxf(e0.x, e1.x);
+            u0 = e0.x == -INFINITY ? 0.0f : ex2(e0.x - up);
+            u1 = e1.x == -INFINITY ? 0.0f : ex2(e1.x - up);
+            all = e0.y * u0 + e1.y * u1;
+            first_col = st * (D / 2);
+            last_col = first_col + D / 2;
+            o_col = to;
+        }
+        if (!kBf) {
+            u0 *= pow2(narrow ? ctl.v_unit[0] : unit);
+            if (two) u1 *= pow2(ctl.v_unit[1]);
+        }
+        const bool whole = s.head && s.tail;
+        const float inv = none ? 0.0f : __fdividef(1.0f, all);
+        bf16* const out = p.out + ((size_t)(s.row0 + (live ? tok : 0)) * p.Hq + s.h * p.G + (live ? row - tok * p.G : 0)) * D;
+        float* const part = parts.slot(blockIdx.x, s.head);
+#pragma unroll 1
+        for (int c = first_col; c < last_col; c += 32) {
+            uint32_t o[32];
+            float x[32];
+            tmem_ld32(o_col + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * u0;
+            if (two) {
+                tmem_ld32(o_col + D + c, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __fmaf_rn(__uint_as_float(o[i]), u1, x[i]);
+            }
+            if (whole) {
+                store32(live ? out + c : nullptr, x, inv);
+            } else if (live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *parts.o(part, row, c / 4 + i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+        }
+        if (!whole && live && (!narrow || st == 0)) *parts.stat(part, row) = make_float2(up, all);
+        if (bad.any(s.k)) {                        // (noted before the products with V)
+            __syncwarp();                          // the row's columns are written, by four lanes
+            if (live) bad.add<D>(limit - BadValues::base(s), first_col, last_col, whole ? out : nullptr,
+                                 reinterpret_cast<float*>(parts.o(part, row, 0)), 4 * parts.pad());
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.o_free);
+        blk += nb;
+    }
+    if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
+}
+
+// ---------------------------------------------------------------------------
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkParams p) {
+    using Y = Lay<D, KV>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Ctl& ctl = *reinterpret_cast<Ctl*>(smem + Y::ctl);
+    const int warp = threadIdx.x >> 5;
+    const uint32_t q = smem_u32(smem + Y::q), kv = smem_u32(smem + Y::kv);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Y::kSt; ++i) {
+            mbar_init(&ctl.kv_full[i], 128);
+            mbar_init(&ctl.kv_empty[i], 1);
+        }
+        mbar_init(&ctl.q_full, 96);
+        mbar_init(&ctl.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.p_full[i][0], 4);
+            mbar_init(&ctl.p_full[i][1], 4);
+            mbar_init(&ctl.pv_half[i], 1);
+            mbar_init(&ctl.pv_done[i], 1);
+        }
+        mbar_init(&ctl.o_free, 8);
+        mbar_init(&ctl.merge, 8);
+        mbar_init(&ctl.done, 1);
+        ctl.abort = ctl.never = 0;
+        ctl.bad_tile = -1;
+        mbar_init_fence();
+    }
+    if (warp == 12) tmem_alloc(&ctl.tmem, kTmemCols);
+    if (threadIdx.x < D) reinterpret_cast<uint32_t*>(smem + Y::bad)[threadIdx.x] = kNoBad;
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    find_part(p, ctl, smem + Y::stat);   // synchronises the CTA
+    tc_fence_after();
+
+    // Registers: a launch gives every thread 128; their sum over the four groups of
+    // four warps stays 512.
+    constexpr bool kBf = KV == kKvBf16;
+    const BadValues bad = {reinterpret_cast<uint32_t*>(smem + Y::bad), ctl};
+    float2* fac = reinterpret_cast<float2*>(smem + Y::fac);
+    if (warp < 8) {
+        set_max_regs_inc<152>();
+        softmax<D, KV>(p, ctl, reinterpret_cast<float2*>(smem + Y::stat), fac, bad);
+    } else if (warp < 12) {
+        set_max_regs_dec<kBf ? 104 : 120>();
+        if constexpr (kBf) load_bf16<D>(p, ctl, kv, smem + Y::kv, bad);
+        else load_codes<D, KV>(p, ctl, smem + Y::kv, smem + Y::raw, fac, bad);
+    } else {
+        set_max_regs_dec<kBf ? 104 : 88>();
+        if (warp == 12) issue_mma<D, KV>(p, ctl, q, kv, bad);
+        else if constexpr (kBf) load_q_bf16<D>(p, ctl, q);
+        else load_q_f16<D>(p, ctl, smem + Y::q, reinterpret_cast<float*>(fac + kFacRing));
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(ctl.tmem, kTmemCols);
+}
+
+// Second kernel: tiles that several parts hold. CTA c - 1 looks at part c's
+// begin; of the k parts that begin inside one tile each joins a k-th of its
+// rows. The rows' weights of all parts come first, into shared memory; then a
+// thread adds up four columns of a row, eight threads side by side along it.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;                               // rows of a CTA, about
+constexpr int kJoinWeights = 2 * (kTileRows + kMaxParts);   // (256 / k + 1) rows of k + 1 parts
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_chunk_join_kernel(const ChunkParams p) {
+    __shared__ float s_w[kJoinWeights];
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x + 1;
+    const int4* entry = reinterpret_cast<const int4*>(reinterpret_cast<const PlanEntry*>(p.ws) + c);
+    const int4 e0 = __ldcg(entry), e1 = __ldcg(entry + 1);
+    if (!e0.x) return;
+    const int kf = e0.y, kl = e0.z, row0 = e0.w, rows = e1.x * p.G, pos0 = e1.y, h = e1.z;
+    // of the tile's `share` parts this one takes a share of its rows, and of those
+    // the CTAs along y shares again
+    const int share = kl - kf + 1, n = share + 1;
+    const int a0 = rows * (c - kf) / share, a1 = rows * (c - kf + 1) / share;
+    const int r0 = a0 + (a1 - a0) * (int)blockIdx.y / (int)gridDim.y;
+    const int r1 = a0 + (a1 - a0) * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    const PartView parts = {p.part, D, p.part_rows};
+    auto slot_of_part = [&](int k) { return parts.slot(kf - 1 + k, k == 0); };
+    for (int row = r0 + (int)threadIdx.x; row < r1; row += kJoinThreads) {
+        float up = -INFINITY, sum = 0.0f;
+        for (int k = 0; k < n; ++k) up = fmaxf(up, __ldcg(parts.stat(slot_of_part(k), row)).x);
+        float* w = s_w + (row - r0) * n;
+        for (int k = 0; k < n; ++k) {
+            const float2 e = __ldcg(parts.stat(slot_of_part(k), row));
+            // a part that saw nothing (or whose scores are all minus infinity) counts with its sum
+            const float a = e.x == up ? 1.0f : ex2(e.x - up);
+            sum = __fmaf_rn(e.y, a, sum);
+            w[k] = a;
+        }
+        const float inv = pos0 + row / p.G < 0 ? 0.0f : __fdividef(1.0f, sum);
+        for (int k = 0; k < n; ++k) w[k] *= inv;
+    }
+    __syncthreads();
+    constexpr int C = D / 4;
+    for (int at = threadIdx.x; at < (r1 - r0 + 3) / 4 * 4 * C; at += kJoinThreads) {
+        // eight column groups of four rows per warp
+        const int unit = at >> 5, l = at & 31;
+        const int row = r0 + unit / (C / 8) * 4 + (l >> 3), cg = unit % (C / 8) * 8 + (l & 7);
+        if (row >= r1) continue;
+        const float* w = s_w + (row - r0) * n;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float4 v = __ldcg(parts.o(slot_of_part(k), row, cg));
+            o.x = __fmaf_rn(v.x, w[k], o.x);
+            o.y = __fmaf_rn(v.y, w[k], o.y);
+            o.z = __fmaf_rn(v.z, w[k], o.z);
+            o.w = __fmaf_rn(v.w, w[k], o.w);
+        }
+        const int t = row / p.G;
+        bf16* out = p.out + ((size_t)(row0 + t) * p.Hq + h * p.G + row - t * p.G) * D;
+        reinterpret_cast<uint2*>(out)[cg] = make_uint2(bf16x2_of(o.x, o.y), bf16x2_of(o.z, o.w));
+    }
+}
+
+template <int D, int KV>
+cudaError_t launch(const ChunkParams& p, int grid, const Launch& L) {
+    auto kern = attn_chunk_kernel<D, KV>;
+    constexpr size_t bytes = Lay<D, KV>::total;
+    static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+    cudaError_t e = once_per_context(reinterpret_cast<const void*>(kern), [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.pdl ? 1 : 0;
+    if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+    if (cfg.gridDim.x == 1) return cudaSuccess;
+    cfg.gridDim = dim3(grid - 1, (p.part_rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_chunk_join_kernel<D>, p);
+}
+
+int part_rows(int T, int G) { return std::min(T, tile_tokens(G)) * G; }
+
+// Parts that a call of these sizes can have at most.
+int max_parts(int T, int B, int G, int Hkv, int max_ctx) {
+    const long units = (long)Hkv * (T / tile_tokens(G) + B) * blocks_of(max_ctx);
+    return (int)std::min<long>(kMaxParts, (units + kMinUnits - 1) / kMinUnits);
+}
+
+}  // namespace
+
+size_t attn_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_ctx) {
+    const int G = Hq / Hkv, parts = max_parts(T, B, G, Hkv, max_ctx);
+    return plan_bytes() + (parts > 1 ? (size_t)parts * 2 * PartView::floats(D, part_rows(T, G)) * 4 : 0);
+}
+
+cudaError_t launch_attention_chunk(ChunkParams p, const Launch& L) {
+    if (p.T <= 0 || p.B <= 0) return cudaSuccess;
+    p.G = p.Hq / p.Hkv;
+    p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(p.ws) + plan_bytes());
+    p.part_rows = part_rows(p.T, p.G);
+    const int grid = std::min(L.num_sms, max_parts(p.T, p.B, p.G, p.Hkv, p.max_blocks * p.page));
+    // scores in units of log2; a scale of 0 stands as the smallest that leaves
+    // masked scores at minus infinity
+    p.negate = p.scale_log2 < 0.0f;
+    if (p.negate) p.scale_log2 = -p.scale_log2;
+    if (p.scale_log2 < 1e-37f) p.scale_log2 = 1e-37f;
+    if (p.D == 128)
+        return p.kv == kKvBf16 ? launch<128, kKvBf16>(p, grid, L)
+               : p.kv == kKvI8 ? launch<128, kKvI8>(p, grid, L) : launch<128, kKvI4>(p, grid, L);
+    if (p.D == 64)
+        return p.kv == kKvBf16 ? launch<64, kKvBf16>(p, grid, L)
+               : p.kv == kKvI8 ? launch<64, kKvI8>(p, grid, L) : launch<64, kKvI4>(p, grid, L);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace a8w8

@@ -203,6 +203,59 @@ long attn_i4_run_tokens(int B, int Hkv, int max_ctx);
 size_t attn_i4_part_bytes(int B, int Hq, int Hkv, int D, int max_ctx);
 cudaError_t launch_attention_i4(const AttnI4Params& p, const Launch& L);
 
+// The forms of a cache: BF16 rows, INT8 codes and a float per row, 4-bit codes
+// and a pair (s, m) of BF16 per row.
+enum { kKvBf16 = 0, kKvI8 = 1, kKvI4 = 2 };
+
+// A chunk's fused QKV rows into a cache (kv_append.cu).
+struct AppendParams {
+    const bf16* qkv;            // [T, ld]: Hq query, Hkv key, Hkv value heads of D
+    int T, Hq, Hkv, D, ld;
+    const bf16* q_norm_w;       // [D] or null: no norm
+    const bf16* k_norm_w;
+    float eps;
+    const int32_t* positions;   // [T], negative: a padded row
+    const float* rope;          // [max_pos, 2 D]
+    int max_pos;
+    const int32_t* slot_mapping;// [T], negative: no cache row
+    bf16* q_out;                // [T, Hq, D] or null: queries are left out
+    int kv;                     // kKv*
+    void* k;                    // rows or codes
+    void* v;
+    void* k_scale;
+    void* v_scale;
+    long num_slots;
+    unsigned* err;
+};
+cudaError_t launch_kv_append(const AppendParams& p, const Launch& L);
+
+// Attention of a chunk of new tokens over the paged cache (attn_chunk.cu):
+// request b's rows q_starts[b] .. q_starts[b + 1] - 1 of q are the last tokens
+// of its context.
+struct ChunkParams {
+    const bf16* q;              // [T, q_stride]
+    int q_stride;
+    const void* k;              // rows or codes
+    const void* v;
+    const void* k_scale;        // float per row (INT8), (s, m) per row (4-bit)
+    const void* v_scale;
+    const int32_t* block_table; // [B, max_blocks]
+    const int32_t* ctx_lens;    // [B]
+    const int32_t* q_starts;    // [B + 1]
+    int T, B, Hq, Hkv, D, page, max_blocks, num_blocks;
+    int kv;                     // kKv*
+    float scale_log2;           // softmax scale times log2(e)
+    bf16* out;                  // [T, Hq, D]
+    void* ws;
+    unsigned* err;
+    // set by the launcher
+    int G, part_rows;
+    bool negate;
+    float* part;
+};
+size_t attn_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_ctx);
+cudaError_t launch_attention_chunk(ChunkParams p, const Launch& L);
+
 // Pages of a cache (pages.cu). A pool is num_caches device arrays of
 // num_blocks pages each (page_bytes[c] bytes, a multiple of 4).
 constexpr int kMaxCaches = 256;

@@ -23,6 +23,7 @@
 // of 8 heads of 128, write and read in turn, calls queued: 170 MB in 28.2 us
 // (6.0 TB/s, 0.90 of the copy rate); as a replayed graph 30.8.
 #include "kernels.cuh"
+#include "quant_i4.cuh"
 
 namespace a8w8 {
 
@@ -32,89 +33,10 @@ namespace {
 // 64; of 2048 tokens 9.0, 10.3, 8.5.
 constexpr int kI4Threads = 128;
 
-__device__ __forceinline__ __nv_bfloat162 as_bf162(unsigned u) {
-    return *reinterpret_cast<__nv_bfloat162*>(&u);
-}
-__device__ __forceinline__ unsigned as_u32(__nv_bfloat162 h) {
-    return *reinterpret_cast<unsigned*>(&h);
-}
-
 // Sixteen bytes of a row that is read once. Not by the read-only path: the
 // kernel that writes the rows may still run when this grid starts.
 __device__ __forceinline__ int4 ld_row_v4(const bf16* p) {
     return __ldcs(reinterpret_cast<const int4*>(p));
-}
-
-// The row's (s, m) word and the lane's sixteen codes. LPR lanes hold the row,
-// sixteen values each; every lane of the warp calls this.
-template <int LPR>
-__device__ __forceinline__ unsigned quant_row_i4(const int4 (&raw)[2], unsigned (&codes)[2]) {
-    // maximum and negated minimum side by side, NaN taken over
-    __nv_bfloat162 mx = as_bf162(raw[0].x), mn = mx;
-    const int w[7] = {raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-#pragma unroll
-    for (int i = 0; i < 7; ++i) {
-        mx = __hmax2_nan(mx, as_bf162(w[i]));
-        mn = __hmin2_nan(mn, as_bf162(w[i]));
-    }
-    __nv_bfloat162 r = __halves2bfloat162(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx)),
-                                          __hneg(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn))));
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1)
-        r = __hmax2_nan(r, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(r), o)));
-    const float top = __bfloat162float(__low2bfloat16(r));
-    const __nv_bfloat16 mb = __hneg(__high2bfloat16(r));
-    const float m = __bfloat162float(mb);
-    const float range = __fsub_rn(top, m);
-    codes[0] = codes[1] = 0u;
-    if (!isfinite(range)) return 0x7FC07FC0u;   // NaN, NaN
-    // Quotients without a division: the float product with R = RN(1 / y) and
-    // one correction by the exact remainder (as quant_code in common.cuh),
-    // where neither R nor the remainder leaves the normal range.
-    constexpr float kR15 = 1.0f / 15.0f;
-    const bool plain = !(range >= 1.6e-29f && range <= 1.2e30f);   // about 2^-96, 2^100
-    float sf;
-    if (plain) {
-        sf = __fdiv_rn(range, 15.0f);
-    } else {
-        sf = __fmul_rn(range, kR15);
-        sf = __fmaf_rn(__fmaf_rn(-sf, 15.0f, range), kR15, sf);
-    }
-    const __nv_bfloat16 sb = __float2bfloat16_rn(sf);
-    const float s = __bfloat162float(sb);
-    const unsigned meta = as_u32(__halves2bfloat162(sb, mb));
-    if (s == 0.0f) return meta;
-    float x[2][8];
-    unpack8(raw[0], x[0]);
-    unpack8(raw[1], x[1]);
-    if (plain) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float q = fminf(__fdiv_rn(__fsub_rn(x[e / 8][e % 8], m), s), 15.0f);
-            codes[e / 8] |= (unsigned)__float2int_rn(q) << (4 * (e % 8));
-        }
-        return meta;
-    }
-    // The quotient is at most 15 (1 + 2^-8) here, so its rounding needs no
-    // clamp: adding 2^23 leaves rne(q) in the low bits, and eight of them join
-    // by multiply-adds, the exponents' bits adding up to a constant.
-    const float R = __frcp_rn(s);
-    const f32x2 ms = pair(-m, -m), ns = pair(-s, -s), Rs = pair(R, R),
-                big = pair(8388608.0f, 8388608.0f);
-    unsigned acc[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 6; e >= 0; e -= 2)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x2 d = add2(pair(x[h][e], x[h][e + 1]), ms);
-            const f32x2 q0 = mul2(d, Rs);
-            float lo, hi;
-            split(add2(fma2(fma2(q0, ns, d), Rs, q0), big), lo, hi);
-            acc[h] = (acc[h] * 16u + __float_as_uint(hi)) * 16u + __float_as_uint(lo);
-        }
-    codes[0] = acc[0] - 0xFB000000u;
-    codes[1] = acc[1] - 0xFB000000u;
-    return meta;
 }
 
 template <int D>
@@ -144,8 +66,8 @@ __global__ void __launch_bounds__(kI4Threads)
         slot = -1;
     }
     unsigned kc[2], vc[2];
-    const unsigned km = quant_row_i4<LPR>(kr, kc);
-    const unsigned vm = quant_row_i4<LPR>(vr, vc);
+    const unsigned km = quant_row_i4<LPR, 2>(kr, kc);
+    const unsigned vm = quant_row_i4<LPR, 2>(vr, vc);
     if (slot < 0) return;
     const size_t dst = (size_t)slot * Hkv + hh;
 #pragma unroll
