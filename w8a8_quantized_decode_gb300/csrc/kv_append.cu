@@ -13,15 +13,15 @@
 // What bounds it: HBM, 2 (Hq + 2 Hkv) D bytes of a token in, 2 Hq D and the
 // cache's row out. What stands against it is arithmetic: in pairs of floats
 // (common.cuh) the norm and rotation take about 60 instructions an element. So
-// they run in float32 first, with a bound on how far the result is from the
-// exact one: where no boundary between two BF16 values lies that near, its
-// rounding is the exact value's. Otherwise (some 6 % of a warp's turns) the
-// warp's heads are done again in pairs.
+// they run in float32 with a bound on how far the result is from the exact one:
+// both ends of that interval are rounded, and where they agree this is the exact
+// value's rounding (rotated values from 2^-100; below, the last bit may differ).
+// Otherwise the one value is done again in pairs.
 //   norm: every x^2 is exact, and so is x w; of the root's argument the 7 roundings
-//     of the sum and the one of eps count half, then come the root's own and the
-//     product's: 6 x 2^-24 of the value, 6 units in the last place at most;
-//   rotation: two products, the table's two lo parts and the sum, together 3 x
-//     2^-24 (|xn c| + |xn' s|), and one more for the ends of the interval.
+//     of the sum and the one of eps count half, then come the root's own, the
+//     product's and the interval's: 7 x 2^-24 of the value, 8 taken;
+//   rotation: two products, the table's two lo parts, the sum and the interval's
+//     ends: 4 x 2^-24 (|xn c| + |xn' s|) and what is beyond first order, 4.2 taken.
 //
 // A head belongs to D / 8 lanes of 8 values; a rotation's partner value is in the
 // lane half a head away. A warp takes the heads of one token in turns, its sines
@@ -38,22 +38,10 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kFill = 32;              // warps a multiprocessor, at least, before a warp takes a second turn
+// Largest relative distance of the normed value's interval ends from the float32 one,
+// and of a rotated value's from |xn c| + |xn' s|: the counts of the comment above.
+constexpr float kNormErr = 8.0f / (1 << 24), kRotErr = 4.2f / (1 << 24);
 constexpr unsigned kErrSlot = 0x1u, kErrPos = 0x10u;
-
-// Whether the normed v of x, at most 6 units in its last place from the exact
-// value, is too near a midpoint between BF16 values (low half 0x8000) to be
-// rounded, not finite, or so small (2^-67) that a product on its way may have
-// been below the normal numbers.
-__device__ __forceinline__ bool near_midpoint(float v, float x) {
-    const unsigned u = __float_as_uint(v), ex = (u >> 23) & 255u;
-    return (u & 0xFFFFu) - 0x7FF9u <= 14u || (ex - 60u >= 195u && x != 0.0f);
-}
-// r of the exact value within e: its BF16 bits, and whether e leaves them open.
-__device__ __forceinline__ unsigned round_within(float r, float e, bool& open) {
-    const unsigned both = as_u32(__floats2bfloat162_rn(r - e, r + e));
-    open |= (both >> 16) != (both & 0xFFFFu);
-    return both & 0xFFFFu;
-}
 
 template <int LPR>
 __device__ __forceinline__ f2 row_sum_f2(f2 v) {
@@ -67,86 +55,137 @@ __device__ __forceinline__ f2 row_sum_f2(f2 v) {
     return v;
 }
 
-// The lane's 8 values of a head, normed and rotated in pairs of floats. `rope` is
-// the position's row of the table, i0 the lane's first angle, upper whether it
-// holds the head's upper half. Every lane of the warp calls this.
-template <int D>
-__device__ __noinline__ int4 rotate_exact(int4 raw, const bf16* w, float eps, const float* rope, int i0,
-                                          bool upper) {
-    constexpr int LPR = D / 8;
-    float x[8];
-    unpack8(raw, x);
-    if (__any_sync(0xffffffffu, w != nullptr)) {
-        f2 ss = {0.0f, 0.0f};
+// Value e of 8, and its place taken by the BF16 bits r.
+__device__ __forceinline__ float value(const int4& v, int e) {
+    const int i = e >> 1, w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return __uint_as_float((unsigned)w >> (16 * (e & 1)) << 16);
+}
+__device__ __forceinline__ void put(int4& v, int e, bf16 r) {
+    const int i = e >> 1, sh = 16 * (e & 1), keep = ~(0xFFFF << sh), to = __bfloat16_as_ushort(r) << sh;
+    if (i == 0) v.x = (v.x & keep) | to;
+    if (i == 1) v.y = (v.y & keep) | to;
+    if (i == 2) v.z = (v.z & keep) | to;
+    if (i == 3) v.w = (v.w & keep) | to;
+}
+// The values of mask `differ` (16 bits each, those that are not zero) as a mask of 8 bits.
+__device__ __forceinline__ unsigned open_of(const unsigned (&differ)[4]) {
+    unsigned open = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f2_acc(ss, __fmul_rn(x[e], x[e]));
-        const f2 inv = rms_inv(row_sum_f2<LPR>(ss), D, eps);
-        if (w) {
-            float wf[8];
-            unpack8(ld_nc_v4(w), wf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = bf2f(norm_bf16(x[e], wf[e], inv));
-        }
-    }
-    unsigned o[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float partner = __shfl_xor_sync(0xffffffffu, x[e], LPR / 2);
-        const float* t = rope + i0 + e;
-        const f2 a = f2_mulf(f2{__ldg(t), __ldg(t + D)}, x[e]);
-        const f2 b = f2_mulf(f2{__ldg(t + D / 2), __ldg(t + 3 * D / 2)}, partner);
-        const bf16 y = f2_to_bf16(upper ? f2_add(a, b) : f2_sub(a, b));
-        o[e >> 1] |= (unsigned)__bfloat16_as_ushort(y) << (16 * (e & 1));
-    }
-    return make_int4(o[0], o[1], o[2], o[3]);
+    for (int e = 0; e < 8; ++e) open |= (differ[e >> 1] >> (16 * (e & 1)) & 0xFFFFu ? 1u : 0u) << e;
+    return open;
 }
 
-// The same in float32 where its bounds decide every rounding, otherwise by the above.
+// Of the lane's 8 values x of a head those in `open` normed in pairs of floats, in
+// place of those in y. Every lane of the warp calls this.
 template <int D>
-__device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const float (&wf)[8], float eps,
-                                       const float* rope, const float (&c)[8], const float (&s)[8], int i0,
-                                       bool upper) {
-    constexpr int LPR = D / 8;
+__device__ __noinline__ int4 norm_exact(int4 raw, int4 y, unsigned open, const bf16* w, float eps) {
     float x[8];
     unpack8(raw, x);
-    bool open = false;
+    f2 ss = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f2_acc(ss, __fmul_rn(x[e], x[e]));
+    const f2 inv = rms_inv(row_sum_f2<D / 8>(ss), D, eps);
+#pragma unroll 1
+    for (; open; open &= open - 1) {
+        const int e = __ffs(open) - 1;
+        put(y, e, norm_bf16(value(raw, e), bf2f(w[e]), inv));
+    }
+    return y;
+}
+
+// Of the lane's 8 values x and their partners z those in `open` rotated in pairs of
+// floats, in place of those in y. `rope` is the position's row of the table, i0 the
+// lane's first angle, upper whether it holds the head's upper half.
+template <int D>
+__device__ __noinline__ int4 rotate_exact(int4 x, int4 z, int4 y, unsigned open, const float* rope, int i0,
+                                          bool upper) {
+#pragma unroll 1
+    for (; open; open &= open - 1) {
+        const int e = __ffs(open) - 1;
+        const float* t = rope + i0 + e;
+        const f2 a = f2_mulf(f2{__ldg(t), __ldg(t + D)}, value(x, e));
+        const f2 b = f2_mulf(f2{__ldg(t + D / 2), __ldg(t + 3 * D / 2)}, value(z, e));
+        put(y, e, f2_to_bf16(upper ? f2_add(a, b) : f2_sub(a, b)));
+    }
+    return y;
+}
+
+__device__ __forceinline__ void unpack_pairs(const int4& v, f32x2 (&f)[4]) {
+    float x[8];
+    unpack8(v, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ unsigned bf16x2(f32x2 v) {
+    float a, b;
+    split(v, a, b);
+    return as_u32(__floats2bfloat162_rn(a, b));
+}
+
+// The lane's 8 values of a head, normed (with w) and rotated: in float32, both ends
+// of the interval that holds the exact value rounded to BF16, and where those
+// differ by the above.
+template <int D>
+__device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf)[4], float eps,
+                                       const float* rope, const f32x2 (&c)[4], const f32x2 (&s)[4], int i0,
+                                       bool upper) {
+    constexpr int LPR = D / 8;
+    f32x2 x[4];
+    unpack_pairs(raw, x);
     int4 xn = raw;
     if (__any_sync(0xffffffffu, w != nullptr)) {       // (the lanes of two heads may differ)
-        float ss = ((x[0] * x[0] + x[1] * x[1]) + (x[2] * x[2] + x[3] * x[3])) +
-                   ((x[4] * x[4] + x[5] * x[5]) + (x[6] * x[6] + x[7] * x[7]));
+        float ss, s1;
+        split(add2(fma2(x[0], x[0], mul2(x[1], x[1])), fma2(x[2], x[2], mul2(x[3], x[3]))), ss, s1);
+        ss += s1;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float square = __fmaf_rn(ss, 1.0f / D, eps), inv = __frsqrt_rn(square);
+        unsigned open = 0u;
         if (w) {
-            open = square < 1e-30f;
-            unsigned o[4];
+            const float lo = inv * (1.0f - kNormErr), hi = inv * (1.0f + kNormErr);
+            const f32x2 lo2 = pair(lo, lo), hi2 = pair(hi, hi);
+            unsigned o[4], differ[4];
+            float small = INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float a = x[e] * wf[e] * inv, b = x[e + 1] * wf[e + 1] * inv;
-                open |= near_midpoint(a, x[e]) | near_midpoint(b, x[e + 1]);
-                o[e >> 1] = as_u32(__floats2bfloat162_rn(a, b));
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 t = mul2(x[e], wf[e]);
+                float a, b;
+                split(t, a, b);
+                small = fminf(fminf(small, fabsf(a)), fabsf(b));
+                o[e] = bf16x2(mul2(t, lo2));
+                differ[e] = o[e] ^ bf16x2(mul2(t, hi2));
             }
             xn = make_int4(o[0], o[1], o[2], o[3]);
-            unpack8(xn, x);
+            // (products out of the normal numbers' range have other errors)
+            if ((small < 1e-17f && ss != 0.0f) || !(square > 1e-30f && square < 3e38f)) open = 0xFFu;
+            else if ((differ[0] | differ[1]) | (differ[2] | differ[3])) open = open_of(differ);
         }
+        if (__any_sync(0xffffffffu, open != 0u)) xn = norm_exact<D>(raw, xn, open, w, eps);
+        unpack_pairs(xn, x);
     }
     int4 other;
     other.x = __shfl_xor_sync(0xffffffffu, xn.x, LPR / 2);
     other.y = __shfl_xor_sync(0xffffffffu, xn.y, LPR / 2);
     other.z = __shfl_xor_sync(0xffffffffu, xn.z, LPR / 2);
     other.w = __shfl_xor_sync(0xffffffffu, xn.w, LPR / 2);
-    float z[8];
-    unpack8(other, z);
-    unsigned o[4] = {0u, 0u, 0u, 0u};
+    f32x2 z[4];
+    unpack_pairs(other, z);
+    const f32x2 up = pair(kRotErr, kRotErr), down = pair(-kRotErr, -kRotErr);
+    unsigned o[4], differ[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // s carries the sign of the lane's half
-        const float a = x[e] * c[e], b = z[e] * s[e], size = fabsf(a) + fabsf(b);
-        open |= size < 1e-30f && size != 0.0f;
-        o[e >> 1] |= round_within(a + b, size * 3e-7f, open) << (16 * (e & 1));
+    for (int e = 0; e < 4; ++e) {
+        const f32x2 a = mul2(x[e], c[e]), b = mul2(z[e], s[e]), r = add2(a, b);
+        float a0, a1, b0, b1;
+        split(a, a0, a1);
+        split(b, b0, b1);
+        const f32x2 size = pair(fabsf(a0) + fabsf(b0), fabsf(a1) + fabsf(b1));
+        o[e] = bf16x2(fma2(size, up, r));
+        differ[e] = o[e] ^ bf16x2(fma2(size, down, r));
     }
-    if (__any_sync(0xffffffffu, open)) return rotate_exact<D>(raw, w, eps, rope, i0, upper);
-    return make_int4(o[0], o[1], o[2], o[3]);
+    int4 y = make_int4(o[0], o[1], o[2], o[3]);
+    if ((differ[0] | differ[1]) | (differ[2] | differ[3]))
+        y = rotate_exact<D>(xn, other, y, open_of(differ), rope, i0, upper);
+    return y;
 }
 
 // The lane's 8 values of a row into the cache, rows of LPR lanes; nothing is written without `live`.
@@ -187,7 +226,7 @@ __device__ __forceinline__ void store_row(int4 v, void* rows, void* scales, size
 
 // Warp w takes `turns` turns of 32 / (D / 8) heads of token w / per.
 template <int D, int KV>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p, int turns, int per) {
+__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendParams p, int turns, int per) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     pdl_wait();
     pdl_trigger();
@@ -210,23 +249,22 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     const float* rope = p.rope + (size_t)pos * 2 * D;
     const int first = p.q_out ? 0 : p.Hq, all = p.Hq + 2 * p.Hkv;
     const int h0 = first + part * turns * RPW, h1 = min(all, h0 + turns * RPW);
-    float c[8], s[8];
+    f32x2 c[4], s[4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(rope + i0 + e));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(rope + D / 2 + i0 + e));
-        c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
-        s[e] = b.x, s[e + 1] = b.y, s[e + 2] = b.z, s[e + 3] = b.w;
+    for (int e = 0; e < 4; e += 2) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(rope + i0 + 2 * e));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(rope + D / 2 + i0 + 2 * e));
+        c[e] = pair(a.x, a.y), c[e + 1] = pair(a.z, a.w);
+        s[e] = upper ? pair(b.x, b.y) : pair(-b.x, -b.y);
+        s[e + 1] = upper ? pair(b.z, b.w) : pair(-b.z, -b.w);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = upper ? s[e] : -s[e];
     const bf16* row = p.qkv + (size_t)t * p.ld + 8 * j;
     auto load = [&](int h) {
         const int at = min(h + lane / LPR, all - 1);
         return __ldcs(reinterpret_cast<const int4*>(row + (size_t)at * D));
     };
     const bf16 *wq = p.q_norm_w ? p.q_norm_w + 8 * j : nullptr, *wk = p.k_norm_w ? p.k_norm_w + 8 * j : nullptr;
-    float wf[8];
+    f32x2 wf[4];
     const bf16* w = nullptr;
     int kind = -1;                       // of the heads that w belongs to: queries, keys
     int4 next = load(h0);
@@ -238,12 +276,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         const bool in = at < h1;
         // A turn's heads may be of two kinds: rows are rotated where any is a query or key,
         // and each takes its own weights.
-        if (h < p.Hq + p.Hkv) {
+        if (h < p.Hq + p.Hkv && token) {
             const int mine = at < p.Hq ? 0 : 1;
             if (mine != kind) {
                 kind = mine;
                 w = mine ? wk : wq;
-                if (w) unpack8(ld_nc_v4(w), wf);
+                if (w) unpack_pairs(ld_nc_v4(w), wf);
             }
             const int4 y = rotate<D>(v, w, wf, p.eps, rope, c, s, i0, upper);
             if (at < p.Hq + p.Hkv) v = y;
