@@ -31,7 +31,7 @@
 // Measured (GB300, a graph's launch, cold L2): a prompt of 16384 tokens, 40 heads on
 // 8, D 128: 2.0 ms, 1350 TFLOP/s of 1920 that a plain product reaches; 16 single
 // tokens with up to 4095 tokens before them: 39 us; 64 requests of 4 drafts over a 4-bit cache,
-// 230 us. A stream's chain S -> softmax -> P -> O of one block (about 3700 clocks of
+// 187 us. A stream's chain S -> softmax -> P -> O of one block (about 3700 clocks of
 // two streams, 2048 of them products) bounds the long ones, starting up the short.
 #include <algorithm>
 
@@ -75,17 +75,18 @@ struct Ctl {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full, q_free;
     uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];   // of stream (and half block)
-    uint64_t o_free, merge, done;
+    uint64_t o_free, merge, done, tops;
     long u0, u1;                   // this part's units
     int b, h, i;                   // its first unit's request, KV head, tile
     long first;                    // and that tile's first unit
+    uint2 top[2][4];               // load_codes: a block's largest pairs by the warps
     int v_unit[2];                 // narrow tiles: a stream's O is in units of 2^this
     int bad_tile;                  // the segment that bad[] is about, -1 for none
     uint32_t tmem;
     volatile int abort, never;     // never: always 0
 };
 
-constexpr int kFacRing = 8;
+constexpr int kFacRing = 8, kPairRing = 8;     // blocks
 
 template <int D, int KV>
 struct Lay {
@@ -97,7 +98,8 @@ struct Lay {
     static constexpr size_t ctl = bad + D * 4;
     static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see load_codes, load_q
     static constexpr size_t raw = fac + (KV == kKvBf16 ? 0 : kFacRing * 8 + 2 * kTileRows * 4);
-    static constexpr size_t total = raw + (KV == kKvBf16 ? 0 : 48 * 1024);
+    static constexpr size_t pairs = raw + (KV == kKvBf16 ? 0 : 48 * 1024);
+    static constexpr size_t total = pairs + (KV == kKvBf16 ? 0 : kPairRing * kKeys * 8);
 };
 
 // tc::mbar_wait with the limit (about two seconds) by the SM's clock: a third of
@@ -132,6 +134,9 @@ __device__ __forceinline__ uint32_t f16x2_of(float a, float b) {
 __device__ __forceinline__ void cp16z(uint32_t s, const void* g, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void cp4z(uint32_t s, const void* g, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(g), "r"(bytes) : "memory");
 }
 // An arrival on the barrier once this thread's copies so far have landed (one of
 // the barrier's count). The copies write through the generic proxy: who waits
@@ -624,10 +629,10 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
 // does.)
 //
 // The codes come by asynchronous copies into a ring of their own, each thread
-// the 16-byte pieces that it converts itself, so that it waits for nobody else.
-// Per block a lane also reads the pairs of a token in each quarter of the block,
-// its warp's own first (for the exponents; each warp all of them, again to wait
-// for no other).
+// the 16-byte pieces that it converts itself, and each lane the two pairs of a
+// token of its warp's quarter of the block. The four warps wait for one another
+// once a block, for the largest pair (each reading all pairs instead took 3000
+// clocks of a block's 7900).
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 // The power of two 2^e, e in [-126, 127].
@@ -664,15 +669,17 @@ __device__ __noinline__ void note_rows(const void* codes, size_t row, uint32_t m
 
 template <int D, int KV>
 __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, unsigned char* raw,
-                           float2* fac, BadValues bad) {
+                           uint2* pairs, float2* fac, BadValues bad) {
     constexpr int kSt = num_stages<D, KV>(), kRaw = raw_tiles<D, KV>();
     constexpr int RB = KV == kKvI8 ? D : D / 2;      // bytes of a row's codes
     constexpr int LPR = RB / 16, RPI = 32 / LPR, NI = LPR;
     constexpr int CPC = KV == kKvI8 ? 2 : 4;         // 16-byte chunks of FP16 per 16 bytes of codes
     static_assert(kRaw * kKeys * RB == 48 * 1024, "the ring of codes");
+    static_assert(kRaw / 2 + 1 < kPairRing, "copies are ahead by kRaw - 1 tiles, two a block");
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
     const int c = lane % LPR, rl = lane / LPR;
     unsigned char* mine = raw + 16 * (threadIdx.x & 127);       // piece i of a tile at mine + 2048 i
+    uint2* my_pairs = pairs + (threadIdx.x & 127);
 
     // The part's blocks one after the other.
     struct Blocks {
@@ -708,6 +715,12 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         if (in_live) {
             const unsigned char* codes = static_cast<const unsigned char*>(in_cnt & 1 ? p.v : p.k);
             unsigned char* dst = mine + (in_cnt % kRaw) * (kKeys * RB);
+            if (!(in_cnt & 1)) {
+                const uint32_t to = smem_u32(my_pairs + (in_cnt / 2 % kPairRing) * kKeys);
+                const size_t at = row_at(in_slot, in_h);
+                cp4z(to, static_cast<const uint32_t*>(p.k_scale) + at, in_slot >= 0 ? 4u : 0u);
+                cp4z(to + 4, static_cast<const uint32_t*>(p.v_scale) + at, in_slot >= 0 ? 4u : 0u);
+            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int sl = __shfl_sync(0xffffffffu, in_slot, i * RPI + rl);
@@ -727,45 +740,21 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         cp_async_commit();
     };
 
-    auto find_slots = [&](const Blocks& x, Look (&look)[4]) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            look[q] = look_up(p, x.s.b, x.live ? x.s.kend : 0, x.j * kKeys + 32 * ((w + q) & 3) + lane);
-    };
-    // the slot of the own quarter's token
-    auto load_meta = [&](const Look (&look)[4], int h, uint32_t (&km)[4], uint32_t (&vm)[4]) {
-        int first = -1;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int slot = slot_of(p, look[q]);
-            if (q == 0) first = slot;
-            km[q] = vm[q] = 0u;
-            if (slot >= 0) {
-                km[q] = __ldcg(static_cast<const uint32_t*>(p.k_scale) + row_at(slot, h));
-                vm[q] = __ldcg(static_cast<const uint32_t*>(p.v_scale) + row_at(slot, h));
-            }
-        }
-        return first;
-    };
     // whether a row holds an infinity or NaN
     auto odd_row = [](uint32_t m) {
         if (KV == kKvI8) return (m & 0x7F800000u) == 0x7F800000u;
         return (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u;
     };
-    // e with |value| <= 2^e for the finite rows, from the exponents: 127 s, or |m| + 15 s at
-    // most twice the larger of |m| and 16 s; -100 at least, -1000 for rows of zeros alone
-    auto block_exponent = [&](const uint32_t (&m)[4]) {
-        unsigned top = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            unsigned u = m[q] & 0x7FFFFFFFu;
-            if (KV == kKvI4) {
-                const unsigned sc = (m[q] & 0x7FFFu) << 16;
-                u = max(m[q] & 0x7FFF0000u, sc ? sc + (4u << 23) : 0u);
-            }
-            top = max(top, odd_row(m[q]) ? 0u : u);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
+    // a bound on the |values| of a finite row by its pair, as a float's bits but for a power of
+    // two: s, or twice the larger of |m| and 16 s
+    auto size_of = [&](uint32_t m) {
+        if (odd_row(m)) return 0u;
+        if (KV == kKvI8) return m & 0x7FFFFFFFu;
+        const unsigned sc = (m & 0x7FFFu) << 16;
+        return max(m & 0x7FFF0000u, sc ? sc + (4u << 23) : 0u);
+    };
+    // e with |value| <= 2^e: -100 at least, -1000 for rows of zeros alone
+    auto exponent_of = [](unsigned top) {
         return top == 0 ? -1000 : min(max((int)(top >> 23) - 126 + (KV == kKvI8 ? 7 : 1), -100), 131);
     };
     // Ring tile cnt from the thread's pieces of codes (pairs `meta` of the lanes' tokens) times `up`.
@@ -823,48 +812,52 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
 
 #pragma unroll 1
     for (int i = 0; i < kRaw - 1; ++i) copy_tile();
-    // pairs: block x's in registers, those of the next on their way, the slots of the one after
-    Blocks x(p, ctl), ahead(p, ctl);
-    if (!x.live) {
-        cp_async_wait_all();
-        return;
-    }
+    Blocks x(p, ctl);
     unsigned blk = 0;
     int ev = -1000;
-    Look look[4];
-    uint32_t km[4], vm[4];
-    find_slots(ahead, look);
-    int was = load_meta(look, ahead.s.h, km, vm), own = -1;   // the own quarter's slots of x, the next
-    ahead.next();
-    find_slots(ahead, look);
     bool ok = true;
-    for (;;) {
+    while (x.live) {
+        copy_tile();
+        cp_async_wait_group<kRaw - 1>();
+        const uint2 m = my_pairs[(blk % kPairRing) * kKeys];
+        const unsigned tk = __reduce_max_sync(0xffffffffu, size_of(m.x));
+        const unsigned tv = __reduce_max_sync(0xffffffffu, size_of(m.y));
+        if (lane == 0) {
+            ctl.top[blk & 1][w] = make_uint2(tk, tv);
+            mbar_arrive(&ctl.tops);
+        }
+        __syncwarp();
+        if (!(ok = wait_bar(&ctl.tops, blk & 1, &ctl.abort))) break;
+        uint2 top = ctl.top[blk & 1][0];
+#pragma unroll
+        for (int q = 1; q < 4; ++q) {
+            const uint2 t = ctl.top[blk & 1][q];
+            top = make_uint2(max(top.x, t.x), max(top.y, t.y));
+        }
         // the exponents, before the keys are handed over: the softmax reads them behind those
-        int ek = block_exponent(km);
+        int ek = exponent_of(top.x);
         ek = ek == -1000 ? 0 : ek;
-        const int e = block_exponent(vm);
+        const int e = exponent_of(top.y);
         if (x.first) ev = e == -1000 ? -100 : e;
         else if (e > ev + 11) ev = e;
         if (threadIdx.x % 128 == 0)
             fac[blk % kFacRing] = make_float2(pow2(min(ek - 4, 127)), __int_as_float(min(ev - 4, 127)));
-        uint32_t pair_of = km[0], vmine = vm[0];
+        uint32_t pair_of = m.x, vmine = m.y;
         float up = pow2(max(4 - ek, -126));
-        if (ahead.live) {
-            own = load_meta(look, ahead.s.h, km, vm);
-            ahead.next();
-            find_slots(ahead, look);
-        }
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-            copy_tile();
-            cp_async_wait_group<kRaw - 1>();
+            if (v == 1) {
+                copy_tile();
+                cp_async_wait_group<kRaw - 1>();
+            }
             if (!(ok = room())) break;
             convert(pair_of, up);
             // the values: rows that are not finite, of tokens that some rows of the tile do not see
             const int t = x.j * kKeys + 32 * w + lane;
             const unsigned odd = __ballot_sync(0xffffffffu, t > x.s.pos0 && t < x.s.kend && odd_row(vmine));
             if (v == 0 && odd) {
-                note_rows<D, KV>(p.v, row_at(was, x.s.h), vmine, odd,
+                const int slot = slot_of(p, look_up(p, x.s.b, x.s.kend, t));
+                note_rows<D, KV>(p.v, row_at(slot, x.s.h), vmine, odd,
                                  x.j * kKeys + 32 * w - BadValues::base(x.s), x.s.k, bad);
                 if (odd >> lane & 1) vmine = 0u;       // zeros
             }
@@ -873,9 +866,7 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         }
         if (!ok) break;
         ++blk;
-        was = own;
         x.next();
-        if (!x.live) break;
     }
     if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
     cp_async_wait_all();
@@ -1344,6 +1335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         mbar_init(&ctl.o_free, 8);
         mbar_init(&ctl.merge, 8);
         mbar_init(&ctl.done, 1);
+        mbar_init(&ctl.tops, 4);
         ctl.abort = ctl.never = 0;
         ctl.bad_tile = -1;
         mbar_init_fence();
@@ -1367,7 +1359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     } else if (warp < 12) {
         set_max_regs_dec<kBf ? 104 : 120>();
         if constexpr (kBf) load_bf16<D>(p, ctl, kv, smem + Y::kv, bad);
-        else load_codes<D, KV>(p, ctl, smem + Y::kv, smem + Y::raw, fac, bad);
+        else load_codes<D, KV>(p, ctl, smem + Y::kv, smem + Y::raw, reinterpret_cast<uint2*>(smem + Y::pairs), fac, bad);
     } else {
         set_max_regs_dec<kBf ? 104 : 88>();
         if (warp == 12) issue_mma<D, KV>(p, ctl, q, kv, bad);
