@@ -701,6 +701,7 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
             }
         }
     };
+    const unsigned slot_bytes = (unsigned)p.Hkv * RB;
     auto row_at = [&](int slot, int h) { return (size_t)max(slot, 0) * p.Hkv + h; };
 
     // copies: tile by tile, keys then values; the block after is looked up ahead
@@ -713,7 +714,7 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
     if (in.live) in.next();
     auto copy_tile = [&]() {
         if (in_live) {
-            const unsigned char* codes = static_cast<const unsigned char*>(in_cnt & 1 ? p.v : p.k);
+            const unsigned char* codes = static_cast<const unsigned char*>(in_cnt & 1 ? p.v : p.k) + in_h * RB + 16 * c;
             unsigned char* dst = mine + (in_cnt % kRaw) * (kKeys * RB);
             if (!(in_cnt & 1)) {
                 const uint32_t to = smem_u32(my_pairs + (in_cnt / 2 % kPairRing) * kKeys);
@@ -724,7 +725,7 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int sl = __shfl_sync(0xffffffffu, in_slot, i * RPI + rl);
-                cp16z(smem_u32(dst + 2048 * i), codes + row_at(sl, in_h) * RB + 16 * c, sl >= 0 ? 16u : 0u);
+                cp16z(smem_u32(dst + 2048 * i), codes + (size_t)max(sl, 0) * slot_bytes, sl >= 0 ? 16u : 0u);
             }
             if (in_cnt & 1) {
                 in_slot = slot_of(p, in_look);
@@ -758,6 +759,14 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         return top == 0 ? -1000 : min(max((int)(top >> 23) - 126 + (KV == kKvI8 ? 7 : 1), -100), 131);
     };
     // Ring tile cnt from the thread's pieces of codes (pairs `meta` of the lanes' tokens) times `up`.
+    // Where piece 0's chunks go. Lanes of one store in different banks: the second half of a
+    // row's lanes takes its words' halves in the other order (the sub-tiles lie a multiple of
+    // all banks apart).
+    const bool turn = D == 128 && (KV == kKvI8 ? c >> 2 : c >> 1);
+    uint32_t to[CPC];
+#pragma unroll
+    for (int e = 0; e < CPC; ++e)
+        to[e] = tile_off(32 * w + rl, CPC * c + (turn ? e ^ (CPC / 2) : e));
     unsigned cnt = 0;
     auto convert = [&](uint32_t meta, float up) {
         const unsigned char* src = mine + (cnt % kRaw) * (kKeys * RB);
@@ -765,41 +774,40 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         // (not unrolled further: the instruction cache is what these warps wait for most)
 #pragma unroll 2
         for (int i = 0; i < NI; ++i) {
-            const int rr = i * RPI + rl, row = 32 * w + rr;
-            const uint32_t m = __shfl_sync(0xffffffffu, meta, rr);
+            const uint32_t m = __shfl_sync(0xffffffffu, meta, i * RPI + rl);
             const uint4 r = *reinterpret_cast<const uint4*>(src + 2048 * i);
-            const uint32_t word[4] = {r.x, r.y, r.z, r.w};
-            uint4 o[CPC];
-            uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+            const uint32_t word[4] = {turn ? r.z : r.x, turn ? r.w : r.y, turn ? r.x : r.z, turn ? r.y : r.w};
+            unsigned char* const row = tile + i * RPI * 128;
+            const uint32_t flip = RPI == 4 && (i & 1) ? 64u : 0u;      // bit 2 of the row
             if (KV == kKvI8) {
                 const __half2 sc = __float2half2_rn(__uint_as_float(m) * up);
                 const __half2 off = as_half2(0x64806480u);           // 1152
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t u = word[g] ^ 0x80808080u;        // 1024 + 128 + code
-                    ow[2 * g] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4140)), off), sc));
-                    ow[2 * g + 1] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4342)), off), sc));
+                for (int e = 0; e < CPC; ++e) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint32_t u = word[2 * e + g] ^ 0x80808080u;        // 1024 + 128 + code
+                        o[2 * g] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4140)), off), sc));
+                        o[2 * g + 1] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4342)), off), sc));
+                    }
+                    *reinterpret_cast<uint4*>(row + (to[e] ^ flip)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             } else {
                 const float sf = __uint_as_float(m << 16) * up, mf = __uint_as_float(m & 0xFFFF0000u) * up;
                 const __half2 sc = __floats2half2_rn(sf, sf * 0.0625f), mn = __float2half2_rn(mf);
                 const __half2 off = as_half2(0x64006400u);           // 1024
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int e = 0; e < CPC; ++e) {
+                    uint32_t o[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int g = 0; g < 4; ++g) {
                         // 1024 + low nibble, 1024 + 16 times the high one
-                        const uint32_t u = __byte_perm(word[g], 0x64646464u, 0x4040 + 0x0101 * e) & 0x64F0640Fu;
-                        ow[4 * g + e] = as_u32(__hfma2(__hsub2(as_half2(u), off), sc, mn));
+                        const uint32_t u = __byte_perm(word[e], 0x64646464u, 0x4040 + 0x0101 * g) & 0x64F0640Fu;
+                        o[g] = as_u32(__hfma2(__hsub2(as_half2(u), off), sc, mn));
                     }
-            }
-#pragma unroll
-            for (int e = 0; e < CPC; ++e) {
-                // lanes of one store in different banks: the second half of a row's lanes in
-                // another order (the sub-tiles lie a multiple of all banks apart)
-                const bool turn = D == 128 && (KV == kKvI8 ? c >> 2 : c >> 1);
-                const int f = KV == kKvI8 ? e ^ 1 : e ^ 2;
-                *reinterpret_cast<uint4*>(tile + tile_off(row, CPC * c + (turn ? f : e))) = turn ? o[f] : o[e];
+                    *reinterpret_cast<uint4*>(row + (to[e] ^ flip)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
         }
         fence_async_shared();
@@ -1151,11 +1159,23 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
         int unit = 0;                              // O is in units of 2^unit
         const int step = narrow ? 2 : 1;
         const int mine = narrow ? (nb + 1 - st) / 2 : nb;  // blocks of this stream
+        // A warp without a row of the tile has nothing to weigh: what its lanes of P hold
+        // reaches no other row. It leaves its issue slots to the others (64 requests of 4
+        // drafts, 20 rows a tile: X -> Y us).
+        const bool idle = row - lane >= rows;
         for (int j = 0; j < mine; ++j) {
             const int key0 = (s.j0 + (narrow ? st : 0) + j * step) * kKeys;
             ok = wait_bar(&ctl.s_full[st], ns & 1, &ctl.abort);
             if (!ok) break;
             ++ns;
+            if (idle) {
+                if (lane == 0) {
+                    mbar_arrive(&ctl.p_full[st][0]);
+                    mbar_arrive(&ctl.p_full[st][1]);
+                }
+                __syncwarp();
+                continue;
+            }
             tc_fence_after();
             int v_unit = 0;
             if (!kBf) {
@@ -1241,7 +1261,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
             // (read until o_free: a stream with blocks comes here again only after that)
             if (st == 0 || two) {
                 stat[kStreamRows * st + lr] = make_float2(ref, sum);
-                ctl.v_unit[st] = unit;             // (the same in all threads)
+                if (!idle) ctl.v_unit[st] = unit;  // (the same in all of these)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.merge);
