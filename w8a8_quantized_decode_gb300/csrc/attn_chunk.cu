@@ -54,7 +54,6 @@ constexpr int kStreamRows = 128;      // rows of a stream: the MMA's M, the tens
 constexpr int kHalf = kKeys / 2;      // keys whose scores and weights go round at a time
 constexpr int kThreads = 512;         // warps 0-7 softmax, 8-11 keys and values, 12 MMA, 13-15 queries
 constexpr int kMaxParts = 152;
-constexpr int kMinUnits = 3;          // units of a part at least
 constexpr uint32_t kTmemCols = 512;   // S of stream s at 128 s, O of stream s at 256 + D s
 constexpr uint32_t kColO = 256;
 constexpr float kLazy = 8.0f;         // a row's reference may lag behind its maximum by 2^8
@@ -73,19 +72,24 @@ __host__ __device__ constexpr int raw_tiles() {
 
 struct Ctl {
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_full, q_free;
+    uint64_t q_full[2], q_free[2];                              // by the segment's parity
     uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];   // of stream (and half block)
-    uint64_t o_free, merge, done, tops;
+    uint64_t o_free, merge, done;
     long u0, u1;                   // this part's units
     int b, h, i;                   // its first unit's request, KV head, tile
     long first;                    // and that tile's first unit
-    uint2 top[2][4];               // load_codes: a block's largest pairs by the warps
     int v_unit[2];                 // narrow tiles: a stream's O is in units of 2^this
     int bad_tile;                  // the segment that bad[] is about, -1 for none
     uint32_t tmem;
     volatile int abort, never;     // never: always 0
 };
 
+constexpr int kFeeders = 3;            // warps 13-15
+// INT8 and 4-bit caches: the ring of codes, a block's largest pairs by the warps that convert.
+struct CodesCtl {
+    uint64_t full[12], empty[12], tops;
+    uint2 top[2][4];
+};
 constexpr int kFacRing = 8, kPairRing = 8;     // blocks
 
 template <int D, int KV>
@@ -96,10 +100,11 @@ struct Lay {
     static constexpr size_t stat = kv + (size_t)kSt * tile_bytes<D>();   // (ref, sum) [2][128]
     static constexpr size_t bad = stat + 2 * kStreamRows * 8;        // see BadValues
     static constexpr size_t ctl = bad + D * 4;
-    static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see load_codes, load_q
-    static constexpr size_t raw = fac + (KV == kKvBf16 ? 0 : kFacRing * 8 + 2 * kTileRows * 4);
+    static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see convert_codes, load_q_f16
+    static constexpr size_t raw = fac + (KV == kKvBf16 ? 0 : kFacRing * 8 + 4 * kTileRows * 4);
     static constexpr size_t pairs = raw + (KV == kKvBf16 ? 0 : 48 * 1024);
-    static constexpr size_t total = pairs + (KV == kKvBf16 ? 0 : kPairRing * kKeys * 8);
+    static constexpr size_t codes = pairs + (KV == kKvBf16 ? 0 : kPairRing * kKeys * 8);
+    static constexpr size_t total = codes + (KV == kKvBf16 ? 0 : sizeof(CodesCtl));
 };
 
 // tc::mbar_wait with the limit (about two seconds) by the SM's clock: a third of
@@ -112,6 +117,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
         if (*abort || clock64() - t0 > 4000000000ll) return false;
     } while (!mbar_try_wait(bar, parity));
     return true;
+}
+
+// Whether that phase is over, without a wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // ex2 of the special function unit: 2^-22 relative, 0 below 2^-126.
@@ -254,12 +272,12 @@ struct Walk {
         s.ntok = tokens_in(r, tpt, i);
         s.kend = keys > 0 ? (int)keys : 0;
         s.pos0 = (int)(keys - s.ntok);
-        const long at = u - tile;                 // 0, or beyond the tile's own cost
-        s.head = at == 0;
-        s.j0 = s.head ? 0 : (int)at - kTileCost;
-        s.j1 = (int)min((long)nb, u1 - tile - kTileCost);
+        const int cost = cost_of(is_narrow(s.ntok, tpt));
+        s.head = u == tile;
+        s.j0 = s.head ? 0 : (int)(u - tile) - cost;
+        s.j1 = (int)min((long)nb, u1 - tile - cost);
         s.tail = s.j1 == nb;
-        u = tile + kTileCost + s.j1;
+        u = tile + cost + s.j1;
         if (s.tail) {
             tile = u;
             ++i;
@@ -357,7 +375,7 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
     }
     long W;
     const long before = cta_exclusive(mine, sums, W);
-    const Shares sh(W, gridDim.x, kMinUnits);
+    const Shares sh(W, gridDim.x);
     const int c = blockIdx.x;
     if (c < sh.parts && mine > 0) {
 #pragma unroll 1
@@ -409,15 +427,17 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
         if (c < sh.parts) {
             Hit x = hits[0];
             const long end = x.tile + tile_units(x.r, tpt, x.i);
-            ctl.u0 = sh.snap(x.raw, x.tile, end);
+            const bool narrow = is_narrow(tokens_in(x.r, tpt, x.i), tpt);
+            ctl.u0 = sh.snap(x.raw, x.tile, end, narrow);
             ctl.u1 = W;
             if (c + 1 < sh.parts) {
                 const Hit& y = hits[1];
-                ctl.u1 = sh.snap(y.raw, y.tile, y.tile + tile_units(y.r, tpt, y.i));
+                ctl.u1 = sh.snap(y.raw, y.tile, y.tile + tile_units(y.r, tpt, y.i),
+                                 is_narrow(tokens_in(y.r, tpt, y.i), tpt));
             }
             if (ctl.u0 > x.tile && ctl.u0 < end) {
                 const long keys = keys_of(x.r, tpt, x.i);
-                sh.inside(x.tile, end, c, e.kf, e.kl);
+                sh.inside(x.tile, end, narrow, c, e.kf, e.kl);
                 e.inside = 1;
                 e.row0 = x.r.row0 + x.i * tpt;
                 e.ntok = tokens_in(x.r, tpt, x.i);
@@ -628,10 +648,9 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
 // would be off by 2^-8 of |q| |k|, several times what the weights' rounding
 // does.)
 //
-// The codes come by asynchronous copies into a ring of their own, each thread
-// the 16-byte pieces that it converts itself, and each lane the two pairs of a
-// token of its warp's quarter of the block. The four warps wait for one another
-// once a block, for the largest pair (each reading all pairs instead took 3000
+// The codes and the pairs come by asynchronous copies into rings of their own
+// (feed_codes). The four converting warps wait for one another once a block, for
+// the largest pair of their quarters (each reading all pairs instead took 3000
 // clocks of a block's 7900).
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -667,79 +686,49 @@ __device__ __noinline__ void note_rows(const void* codes, size_t row, uint32_t m
     }
 }
 
+// The part's blocks one after the other.
+struct Blocks {
+    Walk walk;
+    Seg s;
+    int j;
+    bool live, first;
+    __device__ __forceinline__ Blocks(const ChunkParams& p, const Ctl& ctl) : walk(p, ctl) {
+        j = -1;
+        s.j1 = 0;
+        next();
+    }
+    __device__ __forceinline__ void next() {
+        first = false;
+        if (++j >= s.j1) {
+            live = walk.next(s);
+            j = s.j0;
+            first = true;
+        }
+    }
+};
+
+// A ring tile's codes: thread t of the four converting warps finds its 16-byte
+// pieces, rows 32 (t / 32) + i RPI + (t % 32) / LPR, at 16 t + 2048 i.
 template <int D, int KV>
-__device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, unsigned char* raw,
-                           uint2* pairs, float2* fac, BadValues bad) {
-    constexpr int kSt = num_stages<D, KV>(), kRaw = raw_tiles<D, KV>();
-    constexpr int RB = KV == kKvI8 ? D : D / 2;      // bytes of a row's codes
-    constexpr int LPR = RB / 16, RPI = 32 / LPR, NI = LPR;
+struct Raw {
+    static constexpr int kTiles = raw_tiles<D, KV>();
+    static constexpr int RB = KV == kKvI8 ? D : D / 2;      // bytes of a row's codes
+    static constexpr int LPR = RB / 16, RPI = 32 / LPR, NI = LPR;
+    static_assert(kTiles * kKeys * RB == 48 * 1024 && kTiles <= 12, "the ring of codes");
+    static_assert(kTiles / 2 + 1 < kPairRing, "copies are ahead by kTiles tiles, two a block");
+};
+
+template <int D, int KV>
+__device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsigned char* kvp, const unsigned char* raw,
+                              const uint2* pairs, float2* fac, BadValues bad) {
+    using R = Raw<D, KV>;
+    constexpr int kSt = num_stages<D, KV>(), kRaw = R::kTiles;
+    constexpr int RB = R::RB, LPR = R::LPR, RPI = R::RPI, NI = R::NI;
     constexpr int CPC = KV == kKvI8 ? 2 : 4;         // 16-byte chunks of FP16 per 16 bytes of codes
-    static_assert(kRaw * kKeys * RB == 48 * 1024, "the ring of codes");
-    static_assert(kRaw / 2 + 1 < kPairRing, "copies are ahead by kRaw - 1 tiles, two a block");
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
     const int c = lane % LPR, rl = lane / LPR;
-    unsigned char* mine = raw + 16 * (threadIdx.x & 127);       // piece i of a tile at mine + 2048 i
-    uint2* my_pairs = pairs + (threadIdx.x & 127);
-
-    // The part's blocks one after the other.
-    struct Blocks {
-        Walk walk;
-        Seg s;
-        int j;
-        bool live, first;
-        __device__ __forceinline__ Blocks(const ChunkParams& p, const Ctl& ctl) : walk(p, ctl) {
-            j = -1;
-            s.j1 = 0;
-            next();
-        }
-        __device__ __forceinline__ void next() {
-            first = false;
-            if (++j >= s.j1) {
-                live = walk.next(s);
-                j = s.j0;
-                first = true;
-            }
-        }
-    };
-    const unsigned slot_bytes = (unsigned)p.Hkv * RB;
-    auto row_at = [&](int slot, int h) { return (size_t)max(slot, 0) * p.Hkv + h; };
-
-    // copies: tile by tile, keys then values; the block after is looked up ahead
-    Blocks in(p, ctl);
-    Look in_look = {-2, 0};
-    if (in.live) in_look = look_up(p, in.s.b, in.s.kend, in.j * kKeys + 32 * w + lane);
-    int in_slot = slot_of(p, in_look), in_h = in.s.h;
-    unsigned in_cnt = 0;
-    bool in_live = in.live;
-    if (in.live) in.next();
-    auto copy_tile = [&]() {
-        if (in_live) {
-            const unsigned char* codes = static_cast<const unsigned char*>(in_cnt & 1 ? p.v : p.k) + in_h * RB + 16 * c;
-            unsigned char* dst = mine + (in_cnt % kRaw) * (kKeys * RB);
-            if (!(in_cnt & 1)) {
-                const uint32_t to = smem_u32(my_pairs + (in_cnt / 2 % kPairRing) * kKeys);
-                const size_t at = row_at(in_slot, in_h);
-                cp4z(to, static_cast<const uint32_t*>(p.k_scale) + at, in_slot >= 0 ? 4u : 0u);
-                cp4z(to + 4, static_cast<const uint32_t*>(p.v_scale) + at, in_slot >= 0 ? 4u : 0u);
-            }
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int sl = __shfl_sync(0xffffffffu, in_slot, i * RPI + rl);
-                cp16z(smem_u32(dst + 2048 * i), codes + (size_t)max(sl, 0) * slot_bytes, sl >= 0 ? 16u : 0u);
-            }
-            if (in_cnt & 1) {
-                in_slot = slot_of(p, in_look);
-                in_live = in.live;
-                in_h = in.s.h;
-                if (in.live) in.next();
-            } else {
-                in_look.blk = -2;
-                if (in.live) in_look = look_up(p, in.s.b, in.s.kend, in.j * kKeys + 32 * w + lane);
-            }
-            ++in_cnt;
-        }
-        cp_async_commit();
-    };
+    const unsigned char* mine = raw + 16 * (threadIdx.x & 127);
+    const uint2* my_pairs = pairs + (threadIdx.x & 127);
 
     // whether a row holds an infinity or NaN
     auto odd_row = [](uint32_t m) {
@@ -812,34 +801,34 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         }
         fence_async_shared();
         mbar_arrive(&ctl.kv_full[cnt % kSt]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cc.empty[cnt % kRaw]);
         ++cnt;
     };
+    auto landed = [&]() { return wait_bar(&cc.full[cnt % kRaw], (cnt / kRaw) & 1, &ctl.abort); };
     auto room = [&]() {
         return cnt < kSt || wait_bar(&ctl.kv_empty[cnt % kSt], (cnt / kSt - 1) & 1, &ctl.abort);
     };
 
-#pragma unroll 1
-    for (int i = 0; i < kRaw - 1; ++i) copy_tile();
     Blocks x(p, ctl);
     unsigned blk = 0;
     int ev = -1000;
     bool ok = true;
     while (x.live) {
-        copy_tile();
-        cp_async_wait_group<kRaw - 1>();
+        if (!(ok = landed())) break;
         const uint2 m = my_pairs[(blk % kPairRing) * kKeys];
         const unsigned tk = __reduce_max_sync(0xffffffffu, size_of(m.x));
         const unsigned tv = __reduce_max_sync(0xffffffffu, size_of(m.y));
         if (lane == 0) {
-            ctl.top[blk & 1][w] = make_uint2(tk, tv);
-            mbar_arrive(&ctl.tops);
+            cc.top[blk & 1][w] = make_uint2(tk, tv);
+            mbar_arrive(&cc.tops);
         }
         __syncwarp();
-        if (!(ok = wait_bar(&ctl.tops, blk & 1, &ctl.abort))) break;
-        uint2 top = ctl.top[blk & 1][0];
+        if (!(ok = wait_bar(&cc.tops, blk & 1, &ctl.abort))) break;
+        uint2 top = cc.top[blk & 1][0];
 #pragma unroll
         for (int q = 1; q < 4; ++q) {
-            const uint2 t = ctl.top[blk & 1][q];
+            const uint2 t = cc.top[blk & 1][q];
             top = make_uint2(max(top.x, t.x), max(top.y, t.y));
         }
         // the exponents, before the keys are handed over: the softmax reads them behind those
@@ -854,18 +843,14 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         float up = pow2(max(4 - ek, -126));
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-            if (v == 1) {
-                copy_tile();
-                cp_async_wait_group<kRaw - 1>();
-            }
-            if (!(ok = room())) break;
+            if (!(ok = (v == 0 || landed()) && room())) break;
             convert(pair_of, up);
             // the values: rows that are not finite, of tokens that some rows of the tile do not see
             const int t = x.j * kKeys + 32 * w + lane;
             const unsigned odd = __ballot_sync(0xffffffffu, t > x.s.pos0 && t < x.s.kend && odd_row(vmine));
             if (v == 0 && odd) {
                 const int slot = slot_of(p, look_up(p, x.s.b, x.s.kend, t));
-                note_rows<D, KV>(p.v, row_at(slot, x.s.h), vmine, odd,
+                note_rows<D, KV>(p.v, (size_t)max(slot, 0) * p.Hkv + x.s.h, vmine, odd,
                                  x.j * kKeys + 32 * w - BadValues::base(x.s), x.s.k, bad);
                 if (odd >> lane & 1) vmine = 0u;       // zeros
             }
@@ -877,12 +862,29 @@ __device__ void load_codes(const ChunkParams& p, Ctl& ctl, unsigned char* kvp, u
         x.next();
     }
     if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
-    cp_async_wait_all();
 }
 
 // ---------------------------------------------------------------------------
 // Queries: three warps
+//
+// A wide tile's rows take both of the query tiles, the rows of narrow ones in turn
+// the first and the second, so that the next is loaded beside a narrow segment.
+// Only warps' rows (32) that hold some are filled.
 // ---------------------------------------------------------------------------
+
+// Segment k's half of the queries, and whether it may be loaded: the last segment but
+// one, where both are narrow, or the last one has no products to come. Both barriers
+// are one phase ahead of what is asked for at most: the next segment of their parity
+// is loaded only after this one.
+__device__ __forceinline__ int q_half(int k, bool narrow) { return narrow ? k & 1 : 0; }
+struct QueryTurn {
+    int k;
+    bool narrow, was;        // segment k, segment k - 1
+    __device__ __forceinline__ bool free_at_start() const { return k < (narrow && was ? 2 : 1); }
+    __device__ __forceinline__ uint64_t* bar(Ctl& ctl) const { return &ctl.q_free[narrow && was ? k & 1 : (k - 1) & 1]; }
+    __device__ __forceinline__ unsigned parity() const { return (narrow && was ? (k >> 1) - 1 : (k - 1) >> 1) & 1; }
+};
+__device__ __forceinline__ int rows_filled(int rows) { return (rows + 31) & ~31; }
 
 template <int D>
 __device__ void load_q_bf16(const ChunkParams& p, Ctl& ctl, uint32_t q) {
@@ -892,78 +894,180 @@ __device__ void load_q_bf16(const ChunkParams& p, Ctl& ctl, uint32_t q) {
     const int inv = (65536 + p.G - 1) / p.G;      // r / G = r inv >> 16 for r < 256
     Walk walk(p, ctl);
     Seg s;
-    for (int k = 0; walk.next(s); ++k) {
-        if (k > 0 && !wait_bar(&ctl.q_free, (k - 1) & 1, &ctl.abort)) {
+    QueryTurn turn = {0, false, false};
+    for (; walk.next(s); ++turn.k) {
+        const int rows = s.ntok * p.G;
+        turn.was = turn.narrow;
+        turn.narrow = rows <= kStreamRows;
+        if (!turn.free_at_start() && !wait_bar(turn.bar(ctl), turn.parity(), &ctl.abort)) {
             if (!ctl.abort) set_timeout(p.err, &ctl.abort);
             break;
         }
-        const int rows = s.ntok * p.G;
-        const int all = rows <= kStreamRows ? kStreamRows : kTileRows;
-        for (int r0 = RPI * w; r0 < all; r0 += 3 * RPI) {
+        const uint32_t to = q + q_half(turn.k, turn.narrow) * tile_bytes<D>();
+        for (int r0 = RPI * w; r0 < rows_filled(rows); r0 += kFeeders * RPI) {
             const int r = r0 + rl;
             const int t = (r * inv) >> 16;
             const bool live = r < rows;
             const bf16* g = p.q + (size_t)(s.row0 + (live ? t : 0)) * p.q_stride +
                             (s.h * p.G + (live ? r - t * p.G : 0)) * D + 8 * c;
-            cp16z(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
+            cp16z(to + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
         }
-        cp_async_arrive(&ctl.q_full);
+        cp_async_arrive(&ctl.q_full[turn.k & 1]);
     }
     cp_async_wait_all();
 }
 
 // The same as FP16 times a power of two per row that brings its largest |q| to
-// 16 at most; unit [2][256] holds what a row is in units of, by the segment's
-// parity (the softmax has read a segment's before the next but one is written).
+// 16 at most; unit [4][256] holds what a row is in units of, by the segment's number
+// (a segment is loaded when the products of the last but one have been issued, so that
+// the softmax has begun with that one or the one before).
 template <int D>
-__device__ void load_q_f16(const ChunkParams& p, Ctl& ctl, unsigned char* q, float* unit) {
+__device__ __forceinline__ void load_q_f16(const ChunkParams& p, const Seg& s, int k, unsigned char* q,
+                                           float* unit) {
     constexpr int CPR = D / 8, RPI = 32 / CPR, U = 4;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
     const int c = lane % CPR, rl = lane / CPR;
     const int inv = (65536 + p.G - 1) / p.G;
+    const int rows = s.ntok * p.G;
+    const int all = rows_filled(rows);
+    q += q_half(k, rows <= kStreamRows) * tile_bytes<D>();
+#pragma unroll 1
+    for (int r0 = RPI * U * w; r0 < all; r0 += kFeeders * RPI * U) {
+        int4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + RPI * u + rl, t = (r * inv) >> 16;
+            raw[u] = make_int4(0, 0, 0, 0);
+            if (r < rows)
+                raw[u] = ld_cg_v4(p.q + (size_t)(s.row0 + t) * p.q_stride + (s.h * p.G + r - t * p.G) * D + 8 * c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + RPI * u + rl;
+            float x[8];
+            unpack8(raw[u], x);
+            int e = -1000;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e = max(e, exponent(x[i]));
+#pragma unroll
+            for (int o = CPR / 2; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+            e = e == -1000 ? 0 : e;
+            const float up = pow2(min(4 - e, 127));
+            uint4 v;
+            v.x = f16x2_of(x[0] * up, x[1] * up);
+            v.y = f16x2_of(x[2] * up, x[3] * up);
+            v.z = f16x2_of(x[4] * up, x[5] * up);
+            v.w = f16x2_of(x[6] * up, x[7] * up);
+            if (r >= all) continue;
+            *reinterpret_cast<uint4*>(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c)) = v;
+            if (c == 0) unit[(k & 3) * kTileRows + r] = pow2(e - 4);
+        }
+    }
+}
+
+// What comes from outside, INT8 and 4-bit caches: codes and pairs by asynchronous
+// copies into their rings, keys then values of block after block, and a tile's
+// queries as soon as the last tile's are used, whichever can go on (a wait for one
+// of them alone could wait for itself). Each of the three warps takes a third of a
+// block's rows. By the warps that convert, the copies took 1400 clocks of a block's
+// 5000 there.
+template <int D, int KV>
+__device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsigned char* q, float* unit, unsigned char* raw,
+                           uint2* pairs) {
+    using R = Raw<D, KV>;
+    constexpr int RPI = R::RPI, NG = kKeys / RPI;         // groups of rows of one copy instruction
+    constexpr int N = (NG + kFeeders - 1) / kFeeders;
+    static_assert(N * RPI <= 64, "a lane holds two slots");
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
+    const int rl = lane / R::LPR, g0 = NG * w / kFeeders, n = NG * (w + 1) / kFeeders - g0;
+    const int row0 = g0 * RPI, rows = n * RPI;
+    const unsigned slot_bytes = (unsigned)p.Hkv * R::RB;
+
     Walk walk(p, ctl);
     Seg s;
-    for (int k = 0; walk.next(s); ++k) {
-        if (k > 0 && !wait_bar(&ctl.q_free, (k - 1) & 1, &ctl.abort)) {
+    QueryTurn turn = {-1, false, false};
+    bool queries = false;
+    auto next_queries = [&]() {
+        queries = walk.next(s);
+        ++turn.k;
+        turn.was = turn.narrow;
+        turn.narrow = s.ntok * p.G <= kStreamRows;
+    };
+    next_queries();
+    Blocks in(p, ctl);
+    Look look[2];
+    auto look_ahead = [&]() {            // the next block's tokens
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            look[i] = look_up(p, in.s.b, in.live && lane + 32 * i < rows ? in.s.kend : 0,
+                              in.j * kKeys + row0 + 32 * i + lane);
+    };
+    int slot[2] = {-1, -1}, h = 0;
+    bool live = in.live;
+    auto step = [&]() {                  // its slots
+        live = in.live;
+        if (!live) return;
+        slot[0] = slot_of(p, look[0]);
+        slot[1] = slot_of(p, look[1]);
+        h = in.s.h;
+        in.next();
+    };
+    if (live) {
+        look_ahead();
+        step();
+    }
+    unsigned cnt = 0;
+    long long t0 = clock64();
+    while (live || queries) {
+        bool moved = false;
+        if (live && (cnt < R::kTiles ||
+                     __all_sync(0xffffffffu, mbar_test(&cc.empty[cnt % R::kTiles], (cnt / R::kTiles - 1) & 1)))) {
+            const bool values = cnt & 1;
+            const unsigned char* codes = static_cast<const unsigned char*>(values ? p.v : p.k) + h * R::RB +
+                                         16 * (lane % R::LPR);
+            const uint32_t dst = smem_u32(raw) + (cnt % R::kTiles) * (kKeys * R::RB) + 16 * lane;
+            if (!values) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (lane + 32 * i >= rows) continue;
+                    const uint32_t to = smem_u32(pairs + (cnt / 2 % kPairRing) * kKeys + row0 + 32 * i + lane);
+                    const size_t at = (size_t)max(slot[i], 0) * p.Hkv + h;
+                    cp4z(to, static_cast<const uint32_t*>(p.k_scale) + at, slot[i] >= 0 ? 4u : 0u);
+                    cp4z(to + 4, static_cast<const uint32_t*>(p.v_scale) + at, slot[i] >= 0 ? 4u : 0u);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int sl = __shfl_sync(0xffffffffu, slot[i * RPI / 32], (i * RPI + rl) & 31);
+                const int g = g0 + i;
+                if (i < n)
+                    cp16z(dst + 2048 * (g % R::NI) + 512 * (g / R::NI), codes + (size_t)max(sl, 0) * slot_bytes,
+                          sl >= 0 ? 16u : 0u);
+            }
+            cp_async_arrive(&cc.full[cnt % R::kTiles]);
+            if (values) step();
+            else look_ahead();
+            ++cnt;
+            moved = true;
+        }
+        if (queries && (turn.free_at_start() || __all_sync(0xffffffffu, mbar_test(turn.bar(ctl), turn.parity())))) {
+            load_q_f16<D>(p, s, turn.k, q, unit);
+            fence_async_shared();
+            mbar_arrive(&ctl.q_full[turn.k & 1]);
+            next_queries();
+            moved = true;
+        }
+        if (moved) {
+            t0 = clock64();
+            continue;
+        }
+        __nanosleep(40);
+        if (__any_sync(0xffffffffu, ctl.abort || clock64() - t0 > 4000000000ll)) {
             if (!ctl.abort) set_timeout(p.err, &ctl.abort);
             break;
         }
-        const int rows = s.ntok * p.G;
-        const int all = rows <= kStreamRows ? kStreamRows : kTileRows;
-        for (int r0 = RPI * U * w; r0 < all; r0 += 3 * RPI * U) {
-            int4 raw[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + RPI * u + rl, t = (r * inv) >> 16;
-                raw[u] = make_int4(0, 0, 0, 0);
-                if (r < rows)
-                    raw[u] = ld_cg_v4(p.q + (size_t)(s.row0 + t) * p.q_stride + (s.h * p.G + r - t * p.G) * D + 8 * c);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + RPI * u + rl;
-                float x[8];
-                unpack8(raw[u], x);
-                int e = -1000;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e = max(e, exponent(x[i]));
-#pragma unroll
-                for (int o = CPR / 2; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-                e = e == -1000 ? 0 : e;
-                const float up = pow2(min(4 - e, 127));
-                uint4 v;
-                v.x = f16x2_of(x[0] * up, x[1] * up);
-                v.y = f16x2_of(x[2] * up, x[3] * up);
-                v.z = f16x2_of(x[4] * up, x[5] * up);
-                v.w = f16x2_of(x[6] * up, x[7] * up);
-                if (r >= all) continue;
-                *reinterpret_cast<uint4*>(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c)) = v;
-                if (c == 0) unit[(k & 1) * kTileRows + r] = pow2(e - 4);
-            }
-        }
-        fence_async_shared();
-        mbar_arrive(&ctl.q_full);
     }
+    cp_async_wait_all();
 }
 
 // ---------------------------------------------------------------------------
@@ -1000,7 +1104,7 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
         return true;
     };
     // S of stream st from query tile buf and ring tile t
-    auto qk = [&](int st, int buf, unsigned t, bool free, bool q_last) {
+    auto qk = [&](int st, int buf, unsigned t, bool free, uint64_t* q_last) {
         const uint64_t a = sw128_kmajor_desc(q + buf * tile_bytes<D>());
         const uint64_t b = sw128_kmajor_desc(kv + (t % kSt) * tile_bytes<D>());
         if (elect_one()) {
@@ -1011,7 +1115,7 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
             }
             mma_commit(&ctl.s_full[st]);
             if (free) mma_commit(&ctl.kv_empty[t % kSt]);
-            if (q_last) mma_commit(&ctl.q_free);
+            if (q_last) mma_commit(q_last);
         }
         __syncwarp();
     };
@@ -1044,7 +1148,8 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
     for (int k = 0; ok && walk.next(s); ++k) {
         const int nb = s.blocks();
         const bool narrow = s.ntok * p.G <= kStreamRows;
-        ok = wait_bar(&ctl.q_full, k & 1, &ctl.abort) && wait_full(cnt);
+        uint64_t* const q_free = &ctl.q_free[k & 1];
+        ok = wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort) && wait_full(cnt);
         if (!ok) break;
         // the segment before has left the tensor memory (and the notes on its values)
         auto free_o = [&]() {
@@ -1054,29 +1159,29 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
             return true;
         };
         if (!narrow) {
-            qk(0, 0, cnt, false, false);
-            qk(1, 1, cnt, true, nb == 1);
+            qk(0, 0, cnt, false, nullptr);
+            qk(1, 1, cnt, true, nb == 1 ? q_free : nullptr);
             ok = free_o();
             for (int j = 0; ok && j < nb; ++j) {
                 const unsigned tv = cnt + 2 * j + 1, tk = tv + 1;
                 const bool more = j + 1 < nb;
                 ok = wait_full(tv) && (!more || wait_full(tk)) && pv(0, tv, j > 0, false, !more);
-                if (ok && more) qk(0, 0, tk, false, false);
+                if (ok && more) qk(0, 0, tk, false, nullptr);
                 ok = ok && pv(1, tv, j > 0, true, !more);
-                if (ok && more) qk(1, 1, tk, true, j + 2 == nb);
+                if (ok && more) qk(1, 1, tk, true, j + 2 == nb ? q_free : nullptr);
             }
         } else {
             // block j goes to stream j % 2
             for (int j = 0; ok && j < min(2, nb); ++j) {
                 ok = wait_full(cnt + 2 * j);
-                if (ok) qk(j, 0, cnt + 2 * j, true, j + 1 == nb);
+                if (ok) qk(j, q_half(k, true), cnt + 2 * j, true, j + 1 == nb ? q_free : nullptr);
             }
             ok = ok && free_o();
             for (int j = 0; ok && j < nb; ++j) {
                 const unsigned tv = cnt + 2 * j + 1, tk = tv + 3;
                 const bool more = j + 2 < nb;
                 ok = wait_full(tv) && pv(j & 1, tv, j >= 2, true, !more) && (!more || wait_full(tk));
-                if (ok && more) qk(j & 1, 0, tk, true, j + 3 == nb);
+                if (ok && more) qk(j & 1, q_half(k, true), tk, true, j + 3 == nb ? q_free : nullptr);
             }
         }
         cnt += 2 * nb;
@@ -1180,7 +1285,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
             int v_unit = 0;
             if (!kBf) {
                 const float2 e = fac[(blk + (narrow ? st : 0) + j * step) % kFacRing];
-                if (j == 0) row_scale *= reinterpret_cast<const float*>(fac + kFacRing)[(k & 1) * kTileRows + row];
+                if (j == 0) row_scale *= reinterpret_cast<const float*>(fac + kFacRing)[(k & 3) * kTileRows + row];
                 f = fmaxf(row_scale * e.x, 1e-37f);      // (as the launcher's, see there)
                 v_unit = __float_as_int(e.y);
                 if (j == 0) unit = v_unit;
@@ -1336,6 +1441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     using Y = Lay<D, KV>;
     extern __shared__ __align__(1024) unsigned char smem[];
     Ctl& ctl = *reinterpret_cast<Ctl*>(smem + Y::ctl);
+    CodesCtl& cc = *reinterpret_cast<CodesCtl*>(smem + Y::codes);
     const int warp = threadIdx.x >> 5;
     const uint32_t q = smem_u32(smem + Y::q), kv = smem_u32(smem + Y::kv);
     if (threadIdx.x == 0) {
@@ -1343,9 +1449,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
             mbar_init(&ctl.kv_full[i], 128);
             mbar_init(&ctl.kv_empty[i], 1);
         }
-        mbar_init(&ctl.q_full, 96);
-        mbar_init(&ctl.q_free, 1);
+        for (int i = 0; i < raw_tiles<D, KV>(); ++i) {
+            mbar_init(&cc.full[i], kFeeders * 32);
+            mbar_init(&cc.empty[i], 4);
+        }
+        if (KV != kKvBf16) mbar_init(&cc.tops, 4);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.q_full[i], kFeeders * 32);
+            mbar_init(&ctl.q_free[i], 1);
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.p_full[i][0], 4);
             mbar_init(&ctl.p_full[i][1], 4);
@@ -1355,7 +1466,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         mbar_init(&ctl.o_free, 8);
         mbar_init(&ctl.merge, 8);
         mbar_init(&ctl.done, 1);
-        mbar_init(&ctl.tops, 4);
         ctl.abort = ctl.never = 0;
         ctl.bad_tile = -1;
         mbar_init_fence();
@@ -1377,14 +1487,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         set_max_regs_inc<152>();
         softmax<D, KV>(p, ctl, reinterpret_cast<float2*>(smem + Y::stat), fac, bad);
     } else if (warp < 12) {
-        set_max_regs_dec<kBf ? 104 : 120>();
+        set_max_regs_dec<104>();
         if constexpr (kBf) load_bf16<D>(p, ctl, kv, smem + Y::kv, bad);
-        else load_codes<D, KV>(p, ctl, smem + Y::kv, smem + Y::raw, reinterpret_cast<uint2*>(smem + Y::pairs), fac, bad);
+        else convert_codes<D, KV>(p, ctl, cc, smem + Y::kv, smem + Y::raw, reinterpret_cast<uint2*>(smem + Y::pairs), fac, bad);
     } else {
-        set_max_regs_dec<kBf ? 104 : 88>();
+        set_max_regs_dec<104>();
         if (warp == 12) issue_mma<D, KV>(p, ctl, q, kv, bad);
         else if constexpr (kBf) load_q_bf16<D>(p, ctl, q);
-        else load_q_f16<D>(p, ctl, smem + Y::q, reinterpret_cast<float*>(fac + kFacRing));
+        else feed_codes<D, KV>(p, ctl, cc, smem + Y::q, reinterpret_cast<float*>(fac + kFacRing), smem + Y::raw,
+                               reinterpret_cast<uint2*>(smem + Y::pairs));
     }
     tc_fence_before();
     __syncthreads();
@@ -1486,7 +1597,7 @@ int part_rows(int T, int G) { return std::min(T, tile_tokens(G)) * G; }
 
 // Parts that a call of these sizes can have at most.
 int max_parts(int T, int B, int G, int Hkv, int max_ctx) {
-    const long units = (long)Hkv * (T / tile_tokens(G) + B) * blocks_of(max_ctx);
+    const long units = (long)Hkv * (T / tile_tokens(G) + B) * (kWideCost + (long)blocks_of(max_ctx));
     return (int)std::min<long>(kMaxParts, (units + kMinUnits - 1) / kMinUnits);
 }
 
