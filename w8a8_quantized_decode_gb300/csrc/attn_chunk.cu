@@ -73,6 +73,7 @@ __host__ __device__ constexpr int raw_tiles() {
 struct Ctl {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[2], q_free[2];                              // by the segment's parity
+    uint64_t q_ready[2];                                        // INT8, 4-bit: made FP16
     uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];   // of stream (and half block)
     uint64_t o_free, merge, done;
     long u0, u1;                   // this part's units
@@ -100,7 +101,7 @@ struct Lay {
     static constexpr size_t stat = kv + (size_t)kSt * tile_bytes<D>();   // (ref, sum) [2][128]
     static constexpr size_t bad = stat + 2 * kStreamRows * 8;        // see BadValues
     static constexpr size_t ctl = bad + D * 4;
-    static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see convert_codes, load_q_f16
+    static constexpr size_t fac = ctl + (sizeof(Ctl) + 15) / 16 * 16;    // see convert_codes, q_to_f16
     static constexpr size_t raw = fac + (KV == kKvBf16 ? 0 : kFacRing * 8 + 4 * kTileRows * 4);
     static constexpr size_t pairs = raw + (KV == kKvBf16 ? 0 : 48 * 1024);
     static constexpr size_t codes = pairs + (KV == kKvBf16 ? 0 : kPairRing * kKeys * 8);
@@ -656,12 +657,6 @@ __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 // The power of two 2^e, e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// e with |a| < 2^e, -100 at least; nothing (-1000) for zero, an infinity and NaN.
-__device__ __forceinline__ int exponent(float a) {
-    const int e = (__float_as_int(a) >> 23) & 255;
-    return e == 255 || a == 0.0f ? -1000 : max(e - 126, -100);
-}
-
 // The dimensions of value rows with an infinity or NaN, row r's in the mask of
 // `odd` (its slot's first code and pair in lane r), go to the notes; tok0 is row
 // 0's token from BadValues::base.
@@ -886,83 +881,78 @@ struct QueryTurn {
 };
 __device__ __forceinline__ int rows_filled(int rows) { return (rows + 31) & ~31; }
 
+// Segment k's queries by asynchronous copies, a third by each of the three warps.
 template <int D>
-__device__ void load_q_bf16(const ChunkParams& p, Ctl& ctl, uint32_t q) {
+__device__ __forceinline__ void copy_q(const ChunkParams& p, Ctl& ctl, const Seg& s, int k, uint32_t q) {
     constexpr int CPR = D / 8, RPI = 32 / CPR;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
     const int c = lane % CPR, rl = lane / CPR;
     const int inv = (65536 + p.G - 1) / p.G;      // r / G = r inv >> 16 for r < 256
+    const int rows = s.ntok * p.G;
+    const uint32_t to = q + q_half(k, rows <= kStreamRows) * tile_bytes<D>();
+    for (int r0 = RPI * w; r0 < rows_filled(rows); r0 += kFeeders * RPI) {
+        const int r = r0 + rl;
+        const int t = (r * inv) >> 16;
+        const bool live = r < rows;
+        const bf16* g = p.q + (size_t)(s.row0 + (live ? t : 0)) * p.q_stride +
+                        (s.h * p.G + (live ? r - t * p.G : 0)) * D + 8 * c;
+        cp16z(to + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
+    }
+    cp_async_arrive(&ctl.q_full[k & 1]);
+}
+
+template <int D>
+__device__ void load_q(const ChunkParams& p, Ctl& ctl, uint32_t q) {
     Walk walk(p, ctl);
     Seg s;
     QueryTurn turn = {0, false, false};
     for (; walk.next(s); ++turn.k) {
-        const int rows = s.ntok * p.G;
         turn.was = turn.narrow;
-        turn.narrow = rows <= kStreamRows;
+        turn.narrow = s.ntok * p.G <= kStreamRows;
         if (!turn.free_at_start() && !wait_bar(turn.bar(ctl), turn.parity(), &ctl.abort)) {
             if (!ctl.abort) set_timeout(p.err, &ctl.abort);
             break;
         }
-        const uint32_t to = q + q_half(turn.k, turn.narrow) * tile_bytes<D>();
-        for (int r0 = RPI * w; r0 < rows_filled(rows); r0 += kFeeders * RPI) {
-            const int r = r0 + rl;
-            const int t = (r * inv) >> 16;
-            const bool live = r < rows;
-            const bf16* g = p.q + (size_t)(s.row0 + (live ? t : 0)) * p.q_stride +
-                            (s.h * p.G + (live ? r - t * p.G : 0)) * D + 8 * c;
-            cp16z(to + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
-        }
-        cp_async_arrive(&ctl.q_full[turn.k & 1]);
+        copy_q<D>(p, ctl, s, turn.k, q);
     }
     cp_async_wait_all();
 }
 
-// The same as FP16 times a power of two per row that brings its largest |q| to
-// 16 at most; unit [4][256] holds what a row is in units of, by the segment's number
-// (a segment is loaded when the products of the last but one have been issued, so that
-// the softmax has begun with that one or the one before).
+// INT8 and 4-bit caches: the thread's row r of a query tile in place as FP16 times a
+// power of two that brings its largest |q| to 16 at most; returns what the row is in
+// units of. The softmax does this, a row per thread, before it writes the last
+// segment's results: the warps that load queries took 16000 clocks for a wide tile's.
 template <int D>
-__device__ __forceinline__ void load_q_f16(const ChunkParams& p, const Seg& s, int k, unsigned char* q,
-                                           float* unit) {
-    constexpr int CPR = D / 8, RPI = 32 / CPR, U = 4;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
-    const int c = lane % CPR, rl = lane / CPR;
-    const int inv = (65536 + p.G - 1) / p.G;
-    const int rows = s.ntok * p.G;
-    const int all = rows_filled(rows);
-    q += q_half(k, rows <= kStreamRows) * tile_bytes<D>();
+__device__ __noinline__ float q_to_f16(unsigned char* tile, int r) {
+    uint4 v[D / 8];
+    unsigned top = 0;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        v[c] = *reinterpret_cast<const uint4*>(tile + tile_off(r, c));
+        const unsigned m = __vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu),
+                                    __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu));
+        top = __vmaxu2(top, m);
+    }
+    top = max(top >> 16, top & 0xFFFFu);
+    if (top >= 0x7F80u) {                // infinities and NaN do not count
+        top = 0;
 #pragma unroll 1
-    for (int r0 = RPI * U * w; r0 < all; r0 += kFeeders * RPI * U) {
-        int4 raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + RPI * u + rl, t = (r * inv) >> 16;
-            raw[u] = make_int4(0, 0, 0, 0);
-            if (r < rows)
-                raw[u] = ld_cg_v4(p.q + (size_t)(s.row0 + t) * p.q_stride + (s.h * p.G + r - t * p.G) * D + 8 * c);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + RPI * u + rl;
-            float x[8];
-            unpack8(raw[u], x);
-            int e = -1000;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e = max(e, exponent(x[i]));
-#pragma unroll
-            for (int o = CPR / 2; o > 0; o >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-            e = e == -1000 ? 0 : e;
-            const float up = pow2(min(4 - e, 127));
-            uint4 v;
-            v.x = f16x2_of(x[0] * up, x[1] * up);
-            v.y = f16x2_of(x[2] * up, x[3] * up);
-            v.z = f16x2_of(x[4] * up, x[5] * up);
-            v.w = f16x2_of(x[6] * up, x[7] * up);
-            if (r >= all) continue;
-            *reinterpret_cast<uint4*>(q + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c)) = v;
-            if (c == 0) unit[(k & 3) * kTileRows + r] = pow2(e - 4);
+        for (int i = 0; i < D; ++i) {
+            const unsigned h = *reinterpret_cast<const uint16_t*>(tile + tile_off(r, i >> 3) + 2 * (i & 7)) & 0x7FFFu;
+            if (h < 0x7F80u) top = max(top, h);
         }
     }
+    const int e = top ? max((int)(top >> 7) - 126, -100) : 0;
+    const float up = pow2(min(4 - e, 127));
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        float x[8];
+        unpack8(make_int4(v[c].x, v[c].y, v[c].z, v[c].w), x);
+        *reinterpret_cast<uint4*>(tile + tile_off(r, c)) =
+            make_uint4(f16x2_of(x[0] * up, x[1] * up), f16x2_of(x[2] * up, x[3] * up),
+                       f16x2_of(x[4] * up, x[5] * up), f16x2_of(x[6] * up, x[7] * up));
+    }
+    return pow2(e - 4);
 }
 
 // What comes from outside, INT8 and 4-bit caches: codes and pairs by asynchronous
@@ -972,7 +962,7 @@ __device__ __forceinline__ void load_q_f16(const ChunkParams& p, const Seg& s, i
 // block's rows. By the warps that convert, the copies took 1400 clocks of a block's
 // 5000 there.
 template <int D, int KV>
-__device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsigned char* q, float* unit, unsigned char* raw,
+__device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_t q, unsigned char* raw,
                            uint2* pairs) {
     using R = Raw<D, KV>;
     constexpr int RPI = R::RPI, NG = kKeys / RPI;         // groups of rows of one copy instruction
@@ -1051,9 +1041,7 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsigne
             moved = true;
         }
         if (queries && (turn.free_at_start() || __all_sync(0xffffffffu, mbar_test(turn.bar(ctl), turn.parity())))) {
-            load_q_f16<D>(p, s, turn.k, q, unit);
-            fence_async_shared();
-            mbar_arrive(&ctl.q_full[turn.k & 1]);
+            copy_q<D>(p, ctl, s, turn.k, q);
             next_queries();
             moved = true;
         }
@@ -1149,7 +1137,8 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
         const int nb = s.blocks();
         const bool narrow = s.ntok * p.G <= kStreamRows;
         uint64_t* const q_free = &ctl.q_free[k & 1];
-        ok = wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort) && wait_full(cnt);
+        ok = (kBf ? wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort)
+                  : wait_bar(&ctl.q_ready[k & 1], (k >> 1) & 1, &ctl.abort)) && wait_full(cnt);
         if (!ok) break;
         // the segment before has left the tensor memory (and the notes on its values)
         auto free_o = [&]() {
@@ -1236,7 +1225,8 @@ __device__ __forceinline__ void store32(bf16* out, const float (&o)[32], float i
 }
 
 template <int D, int KV>
-__device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const float2* fac, BadValues bad) {
+__device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2* stat, const float2* fac,
+                        float* q_unit, BadValues bad) {
     constexpr bool kBf = KV == kKvBf16;
     constexpr float kUp = kBf ? 0.0f : 7.0f;   // weights are 2^(x - ref + kUp)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1250,8 +1240,24 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
     unsigned blk = 0;                           // blocks before this segment
     bool ok = true;
     Walk walk(p, ctl);
-    Seg s;
-    for (int k = 0; ok && walk.next(s); ++k) {
+    Seg s, next;
+    bool more = walk.next(next);
+    // segment k's queries, `next`
+    auto prepare = [&](int k) {
+        if (!(ok = wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort))) return;
+        const int rows = next.ntok * p.G, row = rows <= kStreamRows ? lr : kStreamRows * st + lr;
+        // (of a narrow tile, the rows are its half's stream's)
+        if (row - lane < rows && (rows > kStreamRows || q_half(k, true) == st)) {
+            q_unit[(k & 3) * kTileRows + row] = q_to_f16<D>(q + st * tile_bytes<D>(), lr);
+            fence_async_shared();
+        }
+        __syncwarp();
+        // (two barriers: a stream without a block is ahead of the other by one segment at most)
+        if (lane == 0) mbar_arrive(&ctl.q_ready[k & 1]);
+    };
+    if (!kBf && more) prepare(0);
+    for (int k = 0; ok && more; ++k) {
+        s = next;
         const int nb = s.blocks();
         const int rows = s.ntok * p.G;
         const bool narrow = rows <= kStreamRows;
@@ -1285,7 +1291,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
             int v_unit = 0;
             if (!kBf) {
                 const float2 e = fac[(blk + (narrow ? st : 0) + j * step) % kFacRing];
-                if (j == 0) row_scale *= reinterpret_cast<const float*>(fac + kFacRing)[(k & 3) * kTileRows + row];
+                if (j == 0) row_scale *= q_unit[(k & 3) * kTileRows + row];
                 f = fmaxf(row_scale * e.x, 1e-37f);      // (as the launcher's, see there)
                 v_unit = __float_as_int(e.y);
                 if (j == 0) unit = v_unit;
@@ -1355,6 +1361,11 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, float2* stat, const floa
             if (!ok) break;
         }
         if (!ok) break;
+        more = walk.next(next);
+        if (!kBf && more) {
+            prepare(k + 1);
+            if (!ok) break;
+        }
 
         // ---- results ----
         // A wide tile's stream holds its rows' O. Of a narrow tile both streams hold the same
@@ -1457,6 +1468,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.q_full[i], kFeeders * 32);
             mbar_init(&ctl.q_free[i], 1);
+            mbar_init(&ctl.q_ready[i], 8);
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.p_full[i][0], 4);
             mbar_init(&ctl.p_full[i][1], 4);
@@ -1485,7 +1497,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     float2* fac = reinterpret_cast<float2*>(smem + Y::fac);
     if (warp < 8) {
         set_max_regs_inc<152>();
-        softmax<D, KV>(p, ctl, reinterpret_cast<float2*>(smem + Y::stat), fac, bad);
+        softmax<D, KV>(p, ctl, smem + Y::q, reinterpret_cast<float2*>(smem + Y::stat), fac,
+                       reinterpret_cast<float*>(fac + kFacRing), bad);
     } else if (warp < 12) {
         set_max_regs_dec<104>();
         if constexpr (kBf) load_bf16<D>(p, ctl, kv, smem + Y::kv, bad);
@@ -1493,9 +1506,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     } else {
         set_max_regs_dec<104>();
         if (warp == 12) issue_mma<D, KV>(p, ctl, q, kv, bad);
-        else if constexpr (kBf) load_q_bf16<D>(p, ctl, q);
-        else feed_codes<D, KV>(p, ctl, cc, smem + Y::q, reinterpret_cast<float*>(fac + kFacRing), smem + Y::raw,
-                               reinterpret_cast<uint2*>(smem + Y::pairs));
+        else if constexpr (kBf) load_q<D>(p, ctl, q);
+        else feed_codes<D, KV>(p, ctl, cc, q, smem + Y::raw, reinterpret_cast<uint2*>(smem + Y::pairs));
     }
     tc_fence_before();
     __syncthreads();
