@@ -133,6 +133,19 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same after a wait of half a microsecond at most.
+__device__ __forceinline__ bool mbar_wait_shortly(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(500u)
+        : "memory");
+    return ok != 0;
+}
+
 // ex2 of the special function unit: 2^-22 relative, 0 below 2^-126.
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -1011,7 +1024,7 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
     while (live || queries) {
         bool moved = false;
         if (live && (cnt < R::kTiles ||
-                     __all_sync(0xffffffffu, mbar_test(&cc.empty[cnt % R::kTiles], (cnt / R::kTiles - 1) & 1)))) {
+                     __all_sync(0xffffffffu, mbar_wait_shortly(&cc.empty[cnt % R::kTiles], (cnt / R::kTiles - 1) & 1)))) {
             const bool values = cnt & 1;
             const unsigned char* codes = static_cast<const unsigned char*>(values ? p.v : p.k) + h * R::RB +
                                          16 * (lane % R::LPR);
@@ -1049,7 +1062,7 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
             t0 = clock64();
             continue;
         }
-        __nanosleep(40);
+        if (!live) __nanosleep(100);
         if (__any_sync(0xffffffffu, ctl.abort || clock64() - t0 > 4000000000ll)) {
             if (!ctl.abort) set_timeout(p.err, &ctl.abort);
             break;
