@@ -228,14 +228,18 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
 }
 
 // A request as the tables give it: rows clamped to [0, T), no context where it
-// is out of range.
-__device__ __forceinline__ Req load_req(const ChunkParams& p, int b) {
+// is out of range (flagged, if `check`).
+__device__ __forceinline__ Req load_req(const ChunkParams& p, int b, bool check = false) {
     Req r;
-    const int a = p.q_starts[b], e = p.q_starts[b + 1];
+    const int a = p.q_starts[b], e = p.q_starts[b + 1], c = p.ctx_lens[b];
     r.row0 = min(max(a, 0), p.T);
-    r.n = max(min(e, p.T) - r.row0, 0);
-    const int c = p.ctx_lens[b];
-    r.ctx = c < 0 || c > p.max_blocks * p.page ? 0 : c;
+    r.n = max(min(max(e, 0), p.T) - r.row0, 0);      // (each end clamped: any int is safe)
+    const bool out = c < 0 || c > p.max_blocks * p.page;
+    r.ctx = out ? 0 : c;
+    if (check) {
+        if (out) set_error(p.err, kErrCtx);
+        if (a < 0 || e < a || e > p.T) set_error(p.err, kErrRow);
+    }
     return r;
 }
 
@@ -291,10 +295,11 @@ struct Walk {
         s.j0 = s.head ? 0 : (int)(u - tile) - cost;
         s.j1 = (int)min((long)nb, u1 - tile - cost);
         s.tail = s.j1 == nb;
-        u = tile + cost + s.j1;
         if (s.tail) {
-            tile = u;
+            u = tile += tile_units(r, tpt, i);
             ++i;
+        } else {
+            u = u1;
         }
         return true;
     }
@@ -363,11 +368,11 @@ __device__ __forceinline__ long cta_exclusive(long v, long* s, long& total) {
 
 // Finds this CTA's part: the requests' units added up, each thread a few; the
 // thread that holds the part's first unit (and the next part's) names the
-// request; half of the threads each then look for the tile, one tile a thread.
-// `scratch` is shared memory that nothing else uses yet.
+// request and the head; half of the threads each then look for the tile, one tile a
+// thread. `scratch` is shared memory that nothing else uses yet.
 __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* scratch) {
     struct Hit {
-        long raw, tile;       // the unit, and the first one of its head, then of its tile
+        long raw, head, tile;   // the unit, and the first one of its head, then of its tile
         Req r;
         int b, h, i;
     };
@@ -376,16 +381,12 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
     const int tpt = tile_tokens(p.G);
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    long mine = 0, last = 0;
+    long mine = 0, head = 0;
     Req r = {};
     for (int b = b0; b < b1; ++b) {
-        r = load_req(p, b);
-        mine += last = head_units(r, tpt) * p.Hkv;
-        if (blockIdx.x == 0) {
-            const int c = p.ctx_lens[b], a = p.q_starts[b], e = p.q_starts[b + 1];
-            if (c < 0 || c > p.max_blocks * p.page) set_error(p.err, kErrCtx);
-            if (a < 0 || e < a || e > p.T) set_error(p.err, kErrRow);
-        }
+        r = load_req(p, b, blockIdx.x == 0);
+        head = head_units(r, tpt);
+        mine += head * p.Hkv;
     }
     long W;
     const long before = cta_exclusive(mine, sums, W);
@@ -396,20 +397,19 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
         for (int k = 0; k < 2; ++k) {
             const long raw = sh.raw(c + k);
             if (c + k == sh.parts || raw < before || raw - before >= mine) continue;
-            long at = before, n = last;
-            int b = b1 - 1;
+            long at = before;
+            int b = b0;
             if (per > 1) {
-                for (b = b0;; ++b) {
+                for (;; ++b) {
                     r = load_req(p, b);
-                    n = head_units(r, tpt) * p.Hkv;
-                    if (raw - at < n) break;
-                    at += n;
+                    head = head_units(r, tpt);
+                    if (raw - at < head * p.Hkv) break;
+                    at += head * p.Hkv;
                 }
             }
-            const long head = head_units(r, tpt);
             const int h = (int)div_long(raw - at, head);
             hits[k].raw = raw;
-            hits[k].tile = at + h * head;
+            hits[k].head = at + h * head;
             hits[k].r = r;
             hits[k].b = b;
             hits[k].h = h;
@@ -417,22 +417,18 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
     }
     __syncthreads();
     const int k = threadIdx.x / (kThreads / 2);
-    const bool searched = c + k < sh.parts;
-    int tile = -1;
-    if (searched) {
-        const Req& rk = hits[k].r;
-        const long at = hits[k].raw - hits[k].tile;
+    if (c + k < sh.parts) {
+        Hit& x = hits[k];
+        const Req rk = x.r;
+        const long at = x.raw - x.head;
         const int nt = tiles_of(rk, tpt);
         for (int i = threadIdx.x % (kThreads / 2); i < nt; i += kThreads / 2) {
             const long u = units_before(rk, tpt, i);
-            if (u <= at && at < u + tile_units(rk, tpt, i)) tile = i;
+            if (u <= at && at < u + tile_units(rk, tpt, i)) {
+                x.i = i;
+                x.tile = x.head + u;
+            }
         }
-    }
-    __syncthreads();
-    if (tile >= 0) {
-        Hit& x = hits[k];
-        x.i = tile;
-        x.tile += units_before(x.r, tpt, tile);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -440,18 +436,16 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
         ctl.u0 = ctl.u1 = 0;
         if (c < sh.parts) {
             Hit x = hits[0];
-            const long end = x.tile + tile_units(x.r, tpt, x.i);
-            const bool narrow = is_narrow(tokens_in(x.r, tpt, x.i), tpt);
-            ctl.u0 = sh.snap(x.raw, x.tile, end, narrow);
+            const long end = x.tile + tile_units(x.r, tpt, x.i), slack = sh.slack(x.r, tpt, x.i);
+            ctl.u0 = sh.snap(x.raw, x.tile, end, slack);
             ctl.u1 = W;
             if (c + 1 < sh.parts) {
                 const Hit& y = hits[1];
-                ctl.u1 = sh.snap(y.raw, y.tile, y.tile + tile_units(y.r, tpt, y.i),
-                                 is_narrow(tokens_in(y.r, tpt, y.i), tpt));
+                ctl.u1 = sh.snap(y.raw, y.tile, y.tile + tile_units(y.r, tpt, y.i), sh.slack(y.r, tpt, y.i));
             }
             if (ctl.u0 > x.tile && ctl.u0 < end) {
                 const long keys = keys_of(x.r, tpt, x.i);
-                sh.inside(x.tile, end, narrow, c, e.kf, e.kl);
+                sh.inside(x.tile, end, slack, c, e.kf, e.kl);
                 e.inside = 1;
                 e.row0 = x.r.row0 + x.i * tpt;
                 e.ntok = tokens_in(x.r, tpt, x.i);

@@ -4,20 +4,13 @@
 // A tile is up to 256 / G consecutive tokens of one request with the G query
 // heads of one KV head: wide with more than 128 rows, otherwise narrow. Its work
 // is counted in units: a few for its queries and results and one for every block of
-// 128 keys that its last token sees (one where it sees none). Tiles are
-// numbered request by request, in a request KV head by KV head, in a head by their
-// tokens. A part is a contiguous range of units.
+// 128 keys that its last token sees (one where it sees none), or one more: whole
+// tiles are counted together, so that the units before any of them need no sum
+// over them. Tiles are numbered request by request, in a request KV head by KV
+// head, in a head by their tokens. A part is a contiguous range of units.
 #pragma once
 
 #include <stdint.h>
-
-// Functions that are called, not copied into each place: a launch runs most of
-// them a few times, each time from a cold instruction cache.
-#ifdef __CUDACC__
-#define CHUNK_CALL __host__ __device__ __noinline__ static
-#else
-#define CHUNK_CALL inline
-#endif
 
 namespace a8w8 {
 namespace chunk {
@@ -55,48 +48,27 @@ __host__ __device__ inline bool is_narrow(int tokens, int tpt) { return tokens <
 __host__ __device__ inline int cost_of(bool narrow) { return narrow ? kNarrowCost : kWideCost; }
 __host__ __device__ inline int tiles_of(const Req& r, int tpt) { return (r.n + tpt - 1) / tpt; }
 
-// sum over 0 <= k < n of floor((a k + b) / m): the whole parts of a and b taken
-// out, then the lattice points counted along the other axis (Graham, Knuth,
-// Patashnik, Concrete Mathematics, section 3.5). n at most 2^24, a and m at
-// most 256.
-CHUNK_CALL long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-    long s = 0;
-    while (n > 0) {
-        s += (long)((unsigned long)(n - 1) * n / 2) * (a / m) + (long)n * (b / m);
-        a %= m;
-        b %= m;
-        const unsigned top = a * n + b;
-        if (top < m) break;
-        n = top / m;
-        b = top - n * m;
-        const unsigned t = a;
-        a = m;
-        m = t;
-    }
-    return s;
-}
-
-// Units of a head's tiles before tile i; i is at most the number of tiles - 1,
-// so that they all hold tpt tokens and are wide.
-CHUNK_CALL long units_before(const Req& r, int tpt, int i) {
-    const int base = r.ctx - r.n;
-    // tiles whose last token sees a block at most: one unit each
-    int one = kKeys - base < tpt ? 0 : (kKeys - base) / tpt;
-    if (one > i) one = i;
-    return (long)i * kWideCost +
-           one + floor_sum(i - one, kKeys, tpt, base + (one + 1) * tpt + kKeys - 1);
+// Units of a head's tiles before tile i, all of them whole: with c the cost and b0 the
+// first token's position, tile k sees b0 + (k + 1) tpt keys, and the sum of those over
+// k < i in whole blocks and i (c + 1) are i c, the tiles' blocks and at most one more for
+// each. (Where the first tokens see nothing, b0 counts as 0: see Shares.)
+__host__ __device__ inline long units_before(const Req& r, int tpt, int i) {
+    const long b0 = r.ctx > r.n ? r.ctx - r.n : 0;
+    return (long)i * (kWideCost + 1) + (i * b0 + (long)tpt * i * (i + 1) / 2) / kKeys;
 }
 // Units of a tile, and of one KV head of a request.
-__host__ __device__ inline int tile_units(const Req& r, int tpt, int i) {
-    return cost_of(is_narrow(tokens_in(r, tpt, i), tpt)) + blocks_of(keys_of(r, tpt, i));
+__host__ __device__ inline long tile_units(const Req& r, int tpt, int i) {
+    const int tokens = r.n - i * tpt;
+    if (tokens > tpt) return units_before(r, tpt, i + 1) - units_before(r, tpt, i);
+    return cost_of(is_narrow(tokens, tpt)) + blocks_of(keys_of(r, tpt, i));
 }
-CHUNK_CALL long head_units(const Req& r, int tpt) {
+__host__ __device__ inline long head_units(const Req& r, int tpt) {
     if (r.n <= 0) return 0;
     const int last = tiles_of(r, tpt) - 1;
     return units_before(r, tpt, last) + tile_units(r, tpt, last);
 }
 
-CHUNK_CALL long div_long(long a, long b) {
+__host__ __device__ inline long div_long(long a, long b) {
     return (a | b) >> 32 ? a / b : (long)((unsigned)a / (unsigned)b);
 }
 
@@ -104,7 +76,8 @@ CHUNK_CALL long div_long(long a, long b) {
 // to the nearer end of the tile where that is at most `slack` units away, as a tile
 // that two parts hold costs both of them: an eighth of a part, kMaxSlack at most;
 // but the tile's own cost at least, so that no part begins before a tile's second
-// block.
+// block. Tiles of requests whose first tokens see nothing, where units are not
+// blocks, are not divided.
 struct Shares {
     long W, share, whole;
     int parts, rest;
@@ -116,21 +89,21 @@ struct Shares {
         share = whole / kSlackShare < kMaxSlack ? whole / kSlackShare : kMaxSlack;
     }
     __host__ __device__ long raw(int c) const { return whole * c + rest * c / (parts > 0 ? parts : 1); }
-    __host__ __device__ long slack(bool narrow) const {
-        return share > cost_of(narrow) ? share : cost_of(narrow);
+    __host__ __device__ long slack(const Req& r, int tpt, int i) const {
+        if (r.ctx < r.n) return W;
+        const int cost = cost_of(is_narrow(tokens_in(r, tpt, i), tpt));
+        return share > cost ? share : cost;
     }
-    __host__ __device__ long snap(long u, long tile, long tile_end, bool narrow) const {
-        const long s = slack(narrow);
-        if (u - tile <= s && u - tile <= tile_end - u) return tile;
-        return tile_end - u <= s ? tile_end : u;
+    __host__ __device__ static long snap(long u, long tile, long tile_end, long slack) {
+        if (u - tile <= slack && u - tile <= tile_end - u) return tile;
+        return tile_end - u <= slack ? tile_end : u;
     }
     // The parts kf .. kl that begin inside a tile (more than `slack` units from
     // both ends, as snap has it), given that part c does.
-    __host__ __device__ void inside(long tile, long tile_end, bool narrow, int c, int& kf, int& kl) const {
-        const long s = slack(narrow);
+    __host__ __device__ void inside(long tile, long tile_end, long slack, int c, int& kf, int& kl) const {
         kf = kl = c;
-        while (kf > 1 && raw(kf - 1) > tile + s) --kf;
-        while (kl + 1 < parts && raw(kl + 1) < tile_end - s) ++kl;
+        while (kf > 1 && raw(kf - 1) > tile + slack) --kf;
+        while (kl + 1 < parts && raw(kl + 1) < tile_end - slack) ++kl;
     }
 };
 
