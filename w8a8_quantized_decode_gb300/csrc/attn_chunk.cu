@@ -72,7 +72,7 @@ __host__ __device__ constexpr int raw_tiles() {
 
 struct Ctl {
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_full[2], q_free[2];                              // by the segment's parity
+    uint64_t q_first, q_full[2], q_free[2];                     // by the segment's parity
     uint64_t q_ready[2];                                        // INT8, 4-bit: made FP16
     uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];   // of stream (and half block)
     uint64_t o_free, merge, done;
@@ -345,6 +345,10 @@ __device__ __forceinline__ void set_timeout(unsigned* err, volatile int* abort) 
 // The part's units
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ void prefetch_l2(const void* g) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(g));
+}
+
 // Exclusive sum of v over the CTA's threads; `s` is one long per warp.
 __device__ __forceinline__ long cta_exclusive(long v, long* s, long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -427,6 +431,11 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
             if (u <= at && at < u + tile_units(rk, tpt, i)) {
                 x.i = i;
                 x.tile = x.head + u;
+                if (k == 0) {        // where the first keys' block id is, about
+                    const long at_key = max(at - u - cost_of(is_narrow(tokens_in(rk, tpt, i), tpt)), 0l) * kKeys;
+                    prefetch_l2(p.block_table + (size_t)x.b * p.max_blocks +
+                                min((int)((unsigned)min(at_key, 0x7FFFFFFFl) / (unsigned)p.page), p.max_blocks - 1));
+                }
             }
         }
     }
@@ -871,7 +880,8 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
 //
 // A wide tile's rows take both of the query tiles, the rows of narrow ones in turn
 // the first and the second, so that the next is loaded beside a narrow segment.
-// Only warps' rows (32) that hold some are filled.
+// Only warps' rows (32) that hold some are filled. The first segment's come by the
+// softmax's eight warps, which have nothing else to do then.
 // ---------------------------------------------------------------------------
 
 // Segment k's half of the queries, and whether it may be loaded: the last segment but
@@ -888,16 +898,17 @@ struct QueryTurn {
 };
 __device__ __forceinline__ int rows_filled(int rows) { return (rows + 31) & ~31; }
 
-// Segment k's queries by asynchronous copies, a third by each of the three warps.
-template <int D>
-__device__ __forceinline__ void copy_q(const ChunkParams& p, Ctl& ctl, const Seg& s, int k, uint32_t q) {
+// A segment's queries into tile `to` (and the next) by asynchronous copies, warp w's
+// share of kWarps.
+template <int D, int kWarps>
+__device__ __forceinline__ void copy_q(const ChunkParams& p, const Seg& s, uint32_t to, int w, uint64_t* full) {
     constexpr int CPR = D / 8, RPI = 32 / CPR;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 13;
+    const int lane = threadIdx.x & 31;
     const int c = lane % CPR, rl = lane / CPR;
     const int inv = (65536 + p.G - 1) / p.G;      // r / G = r inv >> 16 for r < 256
     const int rows = s.ntok * p.G;
-    const uint32_t to = q + q_half(k, rows <= kStreamRows) * tile_bytes<D>();
-    for (int r0 = RPI * w; r0 < rows_filled(rows); r0 += kFeeders * RPI) {
+#pragma unroll 2
+    for (int r0 = RPI * w; r0 < rows_filled(rows); r0 += kWarps * RPI) {
         const int r = r0 + rl;
         const int t = (r * inv) >> 16;
         const bool live = r < rows;
@@ -905,22 +916,48 @@ __device__ __forceinline__ void copy_q(const ChunkParams& p, Ctl& ctl, const Seg
                         (s.h * p.G + (live ? r - t * p.G : 0)) * D + 8 * c;
         cp16z(to + (r >> 7) * tile_bytes<D>() + tile_off(r & 127, c), g, live ? 16u : 0u);
     }
-    cp_async_arrive(&ctl.q_full[k & 1]);
+    cp_async_arrive(full);
+}
+
+// The segments after the first.
+struct QueryTurns {
+    Walk walk;
+    Seg s;
+    QueryTurn turn;
+    bool more;
+    __device__ __forceinline__ QueryTurns(const ChunkParams& p, const Ctl& ctl) : walk(p, ctl) {
+        turn = {-1, false, false};
+        next();
+        if (more) next();
+    }
+    __device__ __forceinline__ void next() {
+        more = walk.next(s);
+        ++turn.k;
+        turn.was = turn.narrow;
+        turn.narrow = s.ntok * walk.p.G <= kStreamRows;
+    }
+    template <int D>
+    __device__ __forceinline__ void copy(const ChunkParams& p, Ctl& ctl, uint32_t q) {
+        copy_q<D, kFeeders>(p, s, q + q_half(turn.k, turn.narrow) * tile_bytes<D>(), (threadIdx.x >> 5) - 13,
+                            &ctl.q_full[turn.k & 1]);
+        next();
+    }
+};
+// Waits for segment k's queries.
+__device__ __forceinline__ bool wait_q(Ctl& ctl, int k) {
+    return k == 0 ? wait_bar(&ctl.q_first, 0, &ctl.abort) : wait_bar(&ctl.q_full[k & 1], ((k - 1) >> 1) & 1, &ctl.abort);
 }
 
 template <int D>
 __device__ void load_q(const ChunkParams& p, Ctl& ctl, uint32_t q) {
-    Walk walk(p, ctl);
-    Seg s;
-    QueryTurn turn = {0, false, false};
-    for (; walk.next(s); ++turn.k) {
-        turn.was = turn.narrow;
-        turn.narrow = s.ntok * p.G <= kStreamRows;
+    QueryTurns next(p, ctl);
+    while (next.more) {
+        const QueryTurn& turn = next.turn;
         if (!turn.free_at_start() && !wait_bar(turn.bar(ctl), turn.parity(), &ctl.abort)) {
             if (!ctl.abort) set_timeout(p.err, &ctl.abort);
             break;
         }
-        copy_q<D>(p, ctl, s, turn.k, q);
+        next.copy<D>(p, ctl, q);
     }
     cp_async_wait_all();
 }
@@ -980,17 +1017,6 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
     const int row0 = g0 * RPI, rows = n * RPI;
     const unsigned slot_bytes = (unsigned)p.Hkv * R::RB;
 
-    Walk walk(p, ctl);
-    Seg s;
-    QueryTurn turn = {-1, false, false};
-    bool queries = false;
-    auto next_queries = [&]() {
-        queries = walk.next(s);
-        ++turn.k;
-        turn.was = turn.narrow;
-        turn.narrow = s.ntok * p.G <= kStreamRows;
-    };
-    next_queries();
     Blocks in(p, ctl);
     Look look[2];
     auto look_ahead = [&]() {            // the next block's tokens
@@ -1013,9 +1039,11 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
         look_ahead();
         step();
     }
+    QueryTurns queries(p, ctl);
+    const QueryTurn& turn = queries.turn;
     unsigned cnt = 0;
     long long t0 = clock64();
-    while (live || queries) {
+    while (live || queries.more) {
         bool moved = false;
         if (live && (cnt < R::kTiles ||
                      __all_sync(0xffffffffu, mbar_wait_shortly(&cc.empty[cnt % R::kTiles], (cnt / R::kTiles - 1) & 1)))) {
@@ -1047,9 +1075,8 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
             ++cnt;
             moved = true;
         }
-        if (queries && (turn.free_at_start() || __all_sync(0xffffffffu, mbar_test(turn.bar(ctl), turn.parity())))) {
-            copy_q<D>(p, ctl, s, turn.k, q);
-            next_queries();
+        if (queries.more && (turn.free_at_start() || __all_sync(0xffffffffu, mbar_test(turn.bar(ctl), turn.parity())))) {
+            queries.copy<D>(p, ctl, q);
             moved = true;
         }
         if (moved) {
@@ -1144,7 +1171,7 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
         const int nb = s.blocks();
         const bool narrow = s.ntok * p.G <= kStreamRows;
         uint64_t* const q_free = &ctl.q_free[k & 1];
-        ok = (kBf ? wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort)
+        ok = (kBf ? wait_q(ctl, k)
                   : wait_bar(&ctl.q_ready[k & 1], (k >> 1) & 1, &ctl.abort)) && wait_full(cnt);
         if (!ok) break;
         // the segment before has left the tensor memory (and the notes on its values)
@@ -1251,7 +1278,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
     bool more = walk.next(next);
     // segment k's queries, `next`
     auto prepare = [&](int k) {
-        if (!(ok = wait_bar(&ctl.q_full[k & 1], (k >> 1) & 1, &ctl.abort))) return;
+        if (!(ok = wait_q(ctl, k))) return;
         const int rows = next.ntok * p.G, row = rows <= kStreamRows ? lr : kStreamRows * st + lr;
         // (of a narrow tile, the rows are its half's stream's)
         if (row - lane < rows && (rows > kStreamRows || q_half(k, true) == st)) {
@@ -1262,6 +1289,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
         // (two barriers: a stream without a block is ahead of the other by one segment at most)
         if (lane == 0) mbar_arrive(&ctl.q_ready[k & 1]);
     };
+    if (more) copy_q<D, 8>(p, next, smem_u32(q), warp, &ctl.q_first);
     if (!kBf && more) prepare(0);
     for (int k = 0; ok && more; ++k) {
         s = next;
@@ -1450,6 +1478,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
         blk += nb;
     }
     if (!ok && !ctl.abort) set_timeout(p.err, &ctl.abort);
+    cp_async_wait_all();
 }
 
 // ---------------------------------------------------------------------------
@@ -1482,6 +1511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
             mbar_init(&ctl.pv_half[i], 1);
             mbar_init(&ctl.pv_done[i], 1);
         }
+        mbar_init(&ctl.q_first, 256);
         mbar_init(&ctl.o_free, 8);
         mbar_init(&ctl.merge, 8);
         mbar_init(&ctl.done, 1);
