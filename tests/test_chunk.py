@@ -66,6 +66,18 @@ def test_attention_oracle_equals_the_decode_oracle_row_by_row():
             assert (np.abs(out[starts[b] + i] - ref) <= np.abs(ref) * 2.0 ** -8 + 1e-12).all()
 
 
+def test_plan_covers_every_block_once(tmp_path):
+    """The attention's division into parts, compiled for the host (chunk_plan_check.cpp)."""
+    import os
+    import subprocess
+    exe = str(tmp_path / "check")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "chunk_plan_check.cpp")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover", "-o", exe, src],
+                   check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
 # ---------------------------------------------------------------------------
 # refusals (CPU)
 # ---------------------------------------------------------------------------
@@ -140,6 +152,17 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(a8w8.A8W8Error):
             a8w8._kv_append("paged_kv_append", qkv, None, None, torch.zeros((4, 128)), [], 2, 16, 2, 64, None, None,
                             1e-6, None, None, -1)
+
+
+@pytest.mark.parametrize("name", ["kv_append.cu", "attn_chunk.cu", "quant_i4.cuh"])
+def test_no_read_only_loads_beside_the_producer(name):
+    """These kernels start beside the one before them, which may write what they read: no load of
+    theirs goes through the read-only path."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = open(os.path.join(root, "w8a8_quantized_decode_gb300", "csrc", name)).read()
+    for word in ("__restrict__", "__ldg(", "ld_nc_v4", "ld_stream_v4", ".nc."):
+        assert word not in src, f"{name} uses {word}"
 
 
 # ---------------------------------------------------------------------------
@@ -574,6 +597,27 @@ def test_attention_on_a_given_stream(kind):
     got = _entry(kind, "attention")(*dev, 16, stream=st)
     st.synchronize()
     _check(got, want, bound, owned)
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_long_prompt(kind):
+    """4096 tokens past 300 at 40 / 8 heads of 128, in one call and in two: some rows against the
+    oracle, each as a single token with the context that it sees."""
+    import torch
+    n, prior, Hq, Hkv, D, page = 4096, 300, 40, 8, 128, 128
+    q, arrays, values, bt, ctx, starts = _case(kind, 91, [(n, n + prior)], Hq, Hkv, D, page)
+    rows = np.array([0, 1, 50, 51, 127, 128, 1000, 2047, 2048, 3333, n - 2, n - 1])
+    want, bound, _ = chunk.attention(q[rows], *values, np.repeat(bt, len(rows), 0), prior + 1 + rows,
+                                     np.arange(len(rows) + 1), page, kind=kind)
+    pick = torch.from_numpy(rows).cuda()
+    got = _run(kind, q, arrays, bt, ctx, starts, page)
+    _check(got[pick], want, bound)
+    cut = 1999
+    parts = [_run(kind, q[a:b], arrays, bt, np.array([prior + b], np.int32), np.array([0, b - a], np.int32), page)
+             for a, b in ((0, cut), (cut, n))]
+    _check(torch.cat(parts)[pick], want, bound)
+    assert a8w8.read_device_errors() == 0
 
 
 @gpu

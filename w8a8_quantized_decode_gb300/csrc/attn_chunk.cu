@@ -20,19 +20,26 @@
 //   - Softmax: a thread a row, no shuffles. Exponentials are taken against the
 //     row's last reference first and its maximum beside them; only where that
 //     grew by more than 2^8 are O and the sum rescaled and they are taken again.
-//   - P is rounded to BF16 (a BF16 cache) or FP16: 2^-8 or 2^-11 of a weight, which
-//     the plain formula does as well. Sums, maxima and O are float32.
-//   - Sixteen warps: two warpgroups of softmax, one that fetches and lays out K and V
-//     (asynchronous copies of rows by the block table; a page may end anywhere), one
-//     thread that issues products, three warps for queries.
+//   - P is rounded to BF16 (a BF16 cache) or FP16 (2^-8 or 2^-11 of a weight): what the
+//     products take; over INT8 and 4-bit rows the finer one, as K and V are FP16 there.
+//     Sums, maxima and O are float32.
+//   - Sixteen warps: two warpgroups of softmax, one that brings K and V (asynchronous
+//     copies of rows by the block table; a page may end anywhere) or makes FP16 of their
+//     codes, one thread that issues products, three warps for queries and codes.
 // The order of the sums depends on the sizes and the grid alone: the same call gives
 // the same bits.
 //
-// Measured (GB300, a graph's launch, cold L2): a prompt of 16384 tokens, 40 heads on
-// 8, D 128: 2.0 ms, 1350 TFLOP/s of 1920 that a plain product reaches; 16 single
-// tokens with up to 4095 tokens before them: 39 us; 64 requests of 4 drafts over a 4-bit cache,
-// 187 us. A stream's chain S -> softmax -> P -> O of one block (about 3700 clocks of
-// two streams, 2048 of them products) bounds the long ones, starting up the short.
+// Measured (GB300, a graph's launch; 40 heads on 8 of 128 where not said):
+//   a prompt of 16384 tokens, BF16        1.97 ms, 1395 TFLOP/s of 1920
+//   512 tokens at 16384, BF16             150 us, 1130 TFLOP/s
+//   4 prompts of 512, BF16                33 us
+//   16 single tokens past 63 to 4095      39 us, 3.5 TB/s of 6.8
+//   64 x 4 drafts past 64 to 4096, 4-bit  143 us, 1.1 TB/s
+//   16 requests of 1 to 512 tokens, INT8  214 us, 620 TFLOP/s
+// Long ones are bound by a stream's chain S -> softmax -> P -> O of a block (2900 clocks
+// for both streams' blocks, 2048 of them products); INT8 and 4-bit ones by the
+// conversion (3500 to 4400 a block); short ones by the start: 7000 clocks to find the
+// part, 8000 more to the first S (table, keys, code that no cache holds yet).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -1307,7 +1314,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
         const int mine = narrow ? (nb + 1 - st) / 2 : nb;  // blocks of this stream
         // A warp without a row of the tile has nothing to weigh: what its lanes of P hold
         // reaches no other row. It leaves its issue slots to the others (64 requests of 4
-        // drafts, 20 rows a tile: X -> Y us).
+        // drafts, 20 rows a tile: 187 -> 180 us).
         const bool idle = row - lane >= rows;
         for (int j = 0; j < mine; ++j) {
             const int key0 = (s.j0 + (narrow ? st : 0) + j * step) * kKeys;
@@ -1635,7 +1642,8 @@ cudaError_t launch(const ChunkParams& p, int grid, const Launch& L) {
     cfg.attrs = attr;
     cfg.numAttrs = L.pdl ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
-    if (cfg.gridDim.x == 1) return cudaSuccess;
+    // (no second launch for contexts of up to 256 keys: 5 tokens past 32, 9.2 -> 8.2 us)
+    if (grid == 1 || !may_divide(blocks_of(p.max_blocks * p.page))) return cudaSuccess;
     cfg.gridDim = dim3(grid - 1, (p.part_rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;

@@ -72,6 +72,12 @@ __host__ __device__ inline long div_long(long a, long b) {
     return (a | b) >> 32 ? a / b : (long)((unsigned)a / (unsigned)b);
 }
 
+// Whether a tile of contexts of up to nb blocks may be divided: it has more units
+// than both of its ends keep.
+__host__ __device__ inline bool may_divide(int nb) {
+    return kWideCost + nb + 1 > 2 * kWideSlack || kNarrowCost + nb > 2 * kNarrowSlack;
+}
+
 // How W units are shared by at most P parts: part c begins at W c / parts, moved
 // to the nearer end of the tile where that is at most `slack` units away, as a tile
 // that two parts hold costs both of them; and so that no part begins before a tile's
