@@ -23,13 +23,13 @@
 //   rotation: two products, the table's two lo parts, the sum and the interval's
 //     ends: 4 x 2^-24 (|xn c| + |xn' s|) and what is beyond first order, 4.2 taken.
 //
-// A head belongs to D / 8 lanes of 8 values; a rotation's partner value is in the
-// lane half a head away. A warp takes the heads of one token in turns, its sines
+// A head belongs to D / 8 lanes of 8 values, four of either half, so that a
+// rotation's two values are in one lane. A warp takes the heads of one token in turns, its sines
 // and cosines in registers; how many turns a warp takes depends on the number of
 // tokens (launch).
 //
-// Measured (GB300, a graph's launch): 16384 tokens of 40 / 8 heads of 128, BF16: 147 us,
-// 3.2 TB/s of 6.8 that a copy reaches; 280 instructions a turn of 256 values keep the
+// Measured (GB300, a graph's launch): 16384 tokens of 40 / 8 heads of 128, BF16: 128 us,
+// 3.7 TB/s of 6.8 that a copy reaches; some 250 instructions a turn of 256 values keep the
 // issue slots two thirds busy. One token: 2.6 us.
 #include <algorithm>
 
@@ -79,8 +79,9 @@ __device__ __forceinline__ unsigned open_of(const unsigned (&differ)[4]) {
     return open;
 }
 
-// Of the lane's 8 values x of a head those in `open` normed in pairs of floats, in
-// place of those in y. Every lane of the warp calls this.
+// Of the lane's 8 values of a head (four at w, four at w + D / 2 of the weights) those
+// in `open` normed in pairs of floats, in place of those in y. Every lane of the warp
+// calls this.
 template <int D>
 __device__ __noinline__ int4 norm_exact(int4 raw, int4 y, unsigned open, const bf16* w, float eps) {
     float x[8];
@@ -92,24 +93,22 @@ __device__ __noinline__ int4 norm_exact(int4 raw, int4 y, unsigned open, const b
 #pragma unroll 1
     for (; open; open &= open - 1) {
         const int e = __ffs(open) - 1;
-        put(y, e, norm_bf16(value(raw, e), bf2f(w[e]), inv));
+        put(y, e, norm_bf16(value(raw, e), bf2f(w[(e & 3) + (e >> 2) * (D / 2)]), inv));
     }
     return y;
 }
 
-// Of the lane's 8 values x and their partners z those in `open` rotated in pairs of
-// floats, in place of those in y. `rope` is the position's row of the table, i0 the
-// lane's first angle, upper whether it holds the head's upper half.
+// Of the lane's 8 values x those in `open` rotated in pairs of floats, in place of
+// those in y. `rope` is the lane's first angle in the position's row of the table.
 template <int D>
-__device__ __noinline__ int4 rotate_exact(int4 x, int4 z, int4 y, unsigned open, const float* rope, int i0,
-                                          bool upper) {
+__device__ __noinline__ int4 rotate_exact(int4 x, int4 y, unsigned open, const float* rope) {
 #pragma unroll 1
     for (; open; open &= open - 1) {
         const int e = __ffs(open) - 1;
-        const float* t = rope + i0 + e;
+        const float* t = rope + (e & 3);
         const f2 a = f2_mulf(f2{t[0], t[D]}, value(x, e));
-        const f2 b = f2_mulf(f2{t[D / 2], t[3 * D / 2]}, value(z, e));
-        put(y, e, f2_to_bf16(upper ? f2_add(a, b) : f2_sub(a, b)));
+        const f2 b = f2_mulf(f2{t[D / 2], t[3 * D / 2]}, value(x, e ^ 4));
+        put(y, e, f2_to_bf16(e & 4 ? f2_add(a, b) : f2_sub(a, b)));
     }
     return y;
 }
@@ -131,8 +130,7 @@ __device__ __forceinline__ unsigned bf16x2(f32x2 v) {
 // differ by the above.
 template <int D>
 __device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf)[4], float eps,
-                                       const float* rope, const f32x2 (&c)[4], const f32x2 (&s)[4], int i0,
-                                       bool upper) {
+                                       const float* rope, const f32x2 (&c)[2], const f32x2 (&s)[2]) {
     constexpr int LPR = D / 8;
     f32x2 x[4];
     unpack_pairs(raw, x);
@@ -167,18 +165,12 @@ __device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf
         if (__any_sync(0xffffffffu, open != 0u)) xn = norm_exact<D>(raw, xn, open, w, eps);
         unpack_pairs(xn, x);
     }
-    int4 other;
-    other.x = __shfl_xor_sync(0xffffffffu, xn.x, LPR / 2);
-    other.y = __shfl_xor_sync(0xffffffffu, xn.y, LPR / 2);
-    other.z = __shfl_xor_sync(0xffffffffu, xn.z, LPR / 2);
-    other.w = __shfl_xor_sync(0xffffffffu, xn.w, LPR / 2);
-    f32x2 z[4];
-    unpack_pairs(other, z);
-    const f32x2 up = pair(kRotErr, kRotErr), down = pair(-kRotErr, -kRotErr);
+    const f32x2 up = pair(kRotErr, kRotErr), down = pair(-kRotErr, -kRotErr), minus = pair(-1.0f, -1.0f);
     unsigned o[4], differ[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const f32x2 a = mul2(x[e], c[e]), b = mul2(z[e], s[e]), r = add2(a, b);
+        // x c - x' s of the lower half, x c + x' s of the upper one
+        const f32x2 a = mul2(x[e], c[e & 1]), b = mul2(x[e ^ 2], s[e & 1]), r = e < 2 ? fma2(b, minus, a) : add2(a, b);
         float a0, a1, b0, b1;
         split(a, a0, a1);
         split(b, b0, b1);
@@ -187,17 +179,23 @@ __device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf
         differ[e] = o[e] ^ bf16x2(fma2(size, down, r));
     }
     int4 y = make_int4(o[0], o[1], o[2], o[3]);
-    if ((differ[0] | differ[1]) | (differ[2] | differ[3]))
-        y = rotate_exact<D>(xn, other, y, open_of(differ), rope, i0, upper);
+    if ((differ[0] | differ[1]) | (differ[2] | differ[3])) y = rotate_exact<D>(xn, y, open_of(differ), rope);
     return y;
 }
 
-// The lane's 8 values of a row into the cache, rows of LPR lanes; nothing is written without `live`.
+// The lane's 8 values of a row, four of either half from 4 j on, into the cache, rows
+// of LPR lanes; nothing is written without `live`.
+template <int D>
+__device__ __forceinline__ void store_halves(bf16* to, int4 v) {
+    *reinterpret_cast<int2*>(to) = make_int2(v.x, v.y);
+    *reinterpret_cast<int2*>(to + D / 2) = make_int2(v.z, v.w);
+}
+
 template <int D, int KV>
 __device__ __forceinline__ void store_row(int4 v, void* rows, void* scales, size_t at, int j, bool live) {
     constexpr int LPR = D / 8;
     if (KV == kKvBf16) {
-        if (live) *reinterpret_cast<int4*>(static_cast<bf16*>(rows) + at * D + 8 * j) = v;
+        if (live) store_halves<D>(static_cast<bf16*>(rows) + at * D + 4 * j, v);
     } else if (KV == kKvI8) {
         float x[8];
         unpack8(v, x);
@@ -214,7 +212,9 @@ __device__ __forceinline__ void store_row(int4 v, void* rows, void* scales, size
             hi |= (unsigned)(quant_code(x[4 + e], sc, rc) & 0xFF) << (8 * e);
         }
         if (live) {
-            *reinterpret_cast<uint2*>(static_cast<int8_t*>(rows) + at * D + 8 * j) = make_uint2(lo, hi);
+            unsigned* to = static_cast<unsigned*>(rows) + at * (D / 4) + j;
+            to[0] = lo;
+            to[D / 8] = hi;
             if (j == 0) static_cast<float*>(scales)[at] = sc;
         }
     } else {
@@ -222,7 +222,9 @@ __device__ __forceinline__ void store_row(int4 v, void* rows, void* scales, size
         unsigned code[1];
         const unsigned meta = quant_row_i4<LPR, 1>(raw, code);
         if (live) {
-            static_cast<unsigned*>(rows)[at * LPR + j] = code[0];
+            unsigned short* to = static_cast<unsigned short*>(rows) + at * (D / 4) + j;
+            to[0] = (unsigned short)code[0];
+            to[D / 8] = (unsigned short)(code[0] >> 16);
             if (j == 0) static_cast<unsigned*>(scales)[at] = meta;
         }
     }
@@ -230,7 +232,7 @@ __device__ __forceinline__ void store_row(int4 v, void* rows, void* scales, size
 
 // Warp w takes `turns` turns of 32 / (D / 8) heads of token w / per.
 template <int D, int KV>
-__global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendParams p, int turns, int per) {
+__global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(const AppendParams p, int turns, int per) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     pdl_wait();
     pdl_trigger();
@@ -248,26 +250,20 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
     const bool token = pos >= 0 && pos < p.max_pos;
     if (!token) pos = 0;
     const bool write = token && slot >= 0 && slot < p.num_slots;
-    const bool upper = j >= LPR / 2;
-    const int i0 = 8 * (j % (LPR / 2));
-    const float* rope = p.rope + (size_t)pos * 2 * D;
+    const float* rope = p.rope + (size_t)pos * 2 * D + 4 * j;
     const int first = p.q_out ? 0 : p.Hq, all = p.Hq + 2 * p.Hkv;
     const int h0 = first + part * turns * RPW, h1 = min(all, h0 + turns * RPW);
-    f32x2 c[4], s[4];
-#pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-        const float4 a = *reinterpret_cast<const float4*>(rope + i0 + 2 * e);
-        const float4 b = *reinterpret_cast<const float4*>(rope + D / 2 + i0 + 2 * e);
-        c[e] = pair(a.x, a.y), c[e + 1] = pair(a.z, a.w);
-        s[e] = upper ? pair(b.x, b.y) : pair(-b.x, -b.y);
-        s[e + 1] = upper ? pair(b.z, b.w) : pair(-b.z, -b.w);
-    }
-    const bf16* row = p.qkv + (size_t)t * p.ld + 8 * j;
+    const float4 ca = *reinterpret_cast<const float4*>(rope);
+    const float4 sa = *reinterpret_cast<const float4*>(rope + D / 2);
+    const f32x2 c[2] = {pair(ca.x, ca.y), pair(ca.z, ca.w)}, s[2] = {pair(sa.x, sa.y), pair(sa.z, sa.w)};
+    auto halves = [](const int2& a, const int2& b) { return make_int4(a.x, a.y, b.x, b.y); };
+    const bf16* row = p.qkv + (size_t)t * p.ld + 4 * j;
     auto load = [&](int h) {
         const int at = min(h + lane / LPR, all - 1);
-        return __ldcs(reinterpret_cast<const int4*>(row + (size_t)at * D));
+        const int2* from = reinterpret_cast<const int2*>(row + (size_t)at * D);
+        return halves(__ldcs(from), __ldcs(from + D / 8));
     };
-    const bf16 *wq = p.q_norm_w ? p.q_norm_w + 8 * j : nullptr, *wk = p.k_norm_w ? p.k_norm_w + 8 * j : nullptr;
+    const bf16 *wq = p.q_norm_w ? p.q_norm_w + 4 * j : nullptr, *wk = p.k_norm_w ? p.k_norm_w + 4 * j : nullptr;
     f32x2 wf[4];
     const bf16* w = nullptr;
     int kind = -1;                       // of the heads that w belongs to: queries, keys
@@ -285,15 +281,18 @@ __global__ void __launch_bounds__(kThreads, 6) kv_append_kernel(const AppendPara
             if (mine != kind) {
                 kind = mine;
                 w = mine ? wk : wq;
-                if (w) unpack_pairs(*reinterpret_cast<const int4*>(w), wf);
+                if (w) {
+                    const int2* from = reinterpret_cast<const int2*>(w);
+                    unpack_pairs(halves(from[0], from[D / 8]), wf);
+                }
             }
-            const int4 y = rotate<D>(v, w, wf, p.eps, rope, c, s, i0, upper);
+            const int4 y = rotate<D>(v, w, wf, p.eps, rope, c, s);
             if (at < p.Hq + p.Hkv) v = y;
         }
         if (at < p.Hq) {
             if (in) {
                 if (!token) v = make_int4(0, 0, 0, 0);
-                *reinterpret_cast<int4*>(p.q_out + ((size_t)t * p.Hq + at) * D + 8 * j) = v;
+                store_halves<D>(p.q_out + ((size_t)t * p.Hq + at) * D + 4 * j, v);
             }
         }
         if (h + RPW > p.Hq) {             // some row of the turn goes to the cache
