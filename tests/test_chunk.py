@@ -511,6 +511,53 @@ def test_attention_leaves_other_rows_alone_and_gives_zeros_for_rows_before_the_c
 
 @gpu
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B", [513, 1300])
+def test_attention_of_many_requests(kind, B):
+    """More requests than threads: several a thread in the search for a part."""
+    reqs = [(i * 7 % 4, 4 + i * 37 % 290) for i in range(B)]
+    q, arrays, values, bt, ctx, starts = _case(kind, B, reqs, 4, 2, 64, 16)
+    want, bound, owned = chunk.attention(q, *values, bt, ctx, starts, 16, kind=kind)
+    _check(_run(kind, q, arrays, bt, ctx, starts, 16), want, bound, owned)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_of_nothing(kind):
+    """Requests without a row, no request, no row: out stays as it is."""
+    import torch
+    q, arrays, values, bt, ctx, starts = _case(kind, 3, [(0, 5), (0, 0), (0, 200)], 4, 2, 64, 16, behind=3)
+    out = torch.full((3, 4, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    _run(kind, q, arrays, bt, ctx, starts, 16, out=out)
+    assert (out == 2.0).all()
+    _run(kind, q, arrays, bt[:0], ctx[:0], starts[:1], 16, out=out)
+    assert (out == 2.0).all()
+    assert tuple(_run(kind, q[:0], arrays, bt, ctx, starts, 16).shape) == (0, 4, 64)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_calls_at_once(kind):
+    """On two streams, each with its own workspace, and again on one behind the other."""
+    import torch
+    cases = [_case(kind, 11, [(90, 700), (3, 1500)], 10, 2, 128, 16), _case(kind, 12, [(1, 900)] * 9, 8, 8, 128, 128)]
+    wants = [chunk.attention(c[0], *c[2], *c[3:], page, kind=kind) for c, page in zip(cases, (16, 128))]
+    devs = [[to_dev(a) for a in (c[0], *c[1], *c[3:])] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        outs = [_entry(kind, "attention")(*d, page, stream=s) for d, page, s in zip(devs, (16, 128), streams)]
+        torch.cuda.synchronize()
+        one = [_entry(kind, "attention")(*d, page) for d, page in zip(devs, (16, 128))]
+        for got in (outs, one):
+            for g, w in zip(got, wants):
+                _check(g, *w)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
 def test_attention_flags_bad_tables(kind):
     reqs = [(40, 100), (3, 60), (6, 30)]
     q, arrays, values, bt, ctx, starts = _case(kind, 41, reqs, 4, 2, 64, 16)
