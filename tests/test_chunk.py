@@ -376,6 +376,8 @@ SHAPES = [
     ([(1, c) for c in range(1, 900, 61)], 10, 5, 128, 32),
     ([(4, 200 + 40 * i) for i in range(30)], 16, 2, 128, 64),
     ([(512, 512)] * 2, 6, 2, 128, 96),
+    ([(200, 6500), (90, 300)], 5, 1, 128, 128),
+    ([(300, 7000), (256, 6200)], 2, 1, 64, 64),
 ]
 
 
@@ -490,6 +492,25 @@ def test_attention_keeps_infinities_and_nan_to_the_rows_that_see_them(kind, whic
     if which == 1 and kind == "bf16":
         assert not np.isfinite(want[20, 0, 7]) and np.isfinite(want[19]).all()
     _check(_run(kind, q, arrays, bt, ctx, starts, page), want, bound, owned)
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_tables_for_long_contexts(D):
+    """A table with room for 6144 keys and more takes the longer code over BF16: ragged requests,
+    rows that see nothing, values that are not finite, in the same bounds."""
+    reqs, Hq, Hkv, page = [(60, 90), (300, 300), (200, 700), (1, 40), (20, 20), (5, 2)], 10, 2, 16
+    q, arrays, values, bt, ctx, starts = _case("bf16", 23, reqs, Hq, Hkv, D, page, gain=3.0)
+    slot = lambda b, t: bt[b][t // page] * page + t % page  # noqa: E731
+    wide = np.pad(bt, ((0, 0), (0, 400 - bt.shape[1])))
+    for poisoned in (False, True):
+        if poisoned:
+            for b, t, h, d, x in ((0, 50, 0, 7, np.nan), (1, 20, 1, 0, np.inf), (1, 280, 0, 63, -np.inf),
+                                  (2, 600, 0, 5, np.inf), (2, 601, 0, 5, -np.inf), (4, 19, 1, 33, np.nan)):
+                _poison("bf16", arrays, values, 1, slot(b, t), h, d, x)
+        want, bound, owned = chunk.attention(q, *values, bt, ctx, starts, page)
+        _check(_run("bf16", q, arrays, wide, ctx, starts, page), want, bound, owned)
+    assert a8w8.read_device_errors() == 0
 
 
 @gpu

@@ -30,8 +30,8 @@
 // the same bits.
 //
 // Measured (GB300, a graph's launch; 40 heads on 8 of 128 where not said):
-//   a prompt of 16384 tokens, BF16        1.97 ms, 1395 TFLOP/s of 1920
-//   512 tokens at 16384, BF16             150 us, 1130 TFLOP/s
+//   a prompt of 16384 tokens, BF16        1.91 ms, 1440 TFLOP/s of 1920
+//   512 tokens at 16384, BF16             147 us, 1150 TFLOP/s
 //   4 prompts of 512, BF16                33 us
 //   16 single tokens past 63 to 4095      39 us, 3.5 TB/s of 6.8
 //   64 x 4 drafts past 64 to 4096, 4-bit  143 us, 1.1 TB/s
@@ -1265,7 +1265,8 @@ __device__ __forceinline__ void store32(bf16* out, const float (&o)[32], float i
     }
 }
 
-template <int D, int KV>
+// LONG: both halves of a block in the code, not a loop of them (see launch).
+template <int D, int KV, bool LONG>
 __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2* stat, const float2* fac,
                         float* q_unit, BadValues bad) {
     constexpr bool kBf = KV == kKvBf16;
@@ -1338,7 +1339,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
                 v_unit = __float_as_int(e.y);
                 if (j == 0) unit = v_unit;
             }
-#pragma unroll 1
+#pragma unroll (LONG ? 2 : 1)
             for (int hf = 0; hf < 2; ++hf) {
                 uint32_t v[kHalf], w[kHalf / 2];
                 tmem_ld64(ts + kHalf * hf, v);
@@ -1490,7 +1491,7 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
 
 // ---------------------------------------------------------------------------
 
-template <int D, int KV>
+template <int D, int KV, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkParams p) {
     using Y = Lay<D, KV>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -1541,7 +1542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     float2* fac = reinterpret_cast<float2*>(smem + Y::fac);
     if (warp < 8) {
         set_max_regs_inc<152>();
-        softmax<D, KV>(p, ctl, smem + Y::q, reinterpret_cast<float2*>(smem + Y::stat), fac,
+        softmax<D, KV, LONG>(p, ctl, smem + Y::q, reinterpret_cast<float2*>(smem + Y::stat), fac,
                        reinterpret_cast<float*>(fac + kFacRing), bad);
     } else if (warp < 12) {
         set_max_regs_dec<104>();
@@ -1622,9 +1623,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_chunk_join_kernel(const Chu
     }
 }
 
-template <int D, int KV>
+template <int D, int KV, bool LONG>
 cudaError_t launch(const ChunkParams& p, int grid, const Launch& L) {
-    auto kern = attn_chunk_kernel<D, KV>;
+    auto kern = attn_chunk_kernel<D, KV, LONG>;
     constexpr size_t bytes = Lay<D, KV>::total;
     static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = once_per_context(reinterpret_cast<const void*>(kern), [&] {
@@ -1658,6 +1659,23 @@ int max_parts(int T, int B, int G, int Hkv, int max_ctx) {
     return (int)std::min<long>(kMaxParts, (units + kMinUnits - 1) / kMinUnits);
 }
 
+// Over a BF16 cache, requests of half a wide tile and more on average with contexts of up
+// to so many blocks take the longer code of the softmax: a prompt of 16384 1969 -> 1912 us,
+// 512 tokens at 16384 150 -> 147, a prompt of 8192 with heads of 64 386 -> 362, 8 requests
+// of 256 to 1024 tokens past 1000 to 6000 276 -> 271. Shorter ones lose by it, as their CTAs
+// spend much of their time on code that no cache holds yet: 4 prompts of 512 33 -> 36, 16
+// requests of 1 to 256 tokens past 100 to 4000 103 -> 106; and single tokens: 64 past 1000
+// to 8000 193 -> 195.
+constexpr int kLongBlocks = 48;
+
+template <int D>
+cudaError_t launch_kind(const ChunkParams& p, int grid, const Launch& L) {
+    if (p.kv == kKvI8) return launch<D, kKvI8, false>(p, grid, L);
+    if (p.kv == kKvI4) return launch<D, kKvI4, false>(p, grid, L);
+    const bool is_long = blocks_of(p.max_blocks * p.page) >= kLongBlocks && p.T >= (long)p.B * (tile_tokens(p.G) / 2);
+    return is_long ? launch<D, kKvBf16, true>(p, grid, L) : launch<D, kKvBf16, false>(p, grid, L);
+}
+
 }  // namespace
 
 size_t attn_chunk_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_ctx) {
@@ -1676,12 +1694,8 @@ cudaError_t launch_attention_chunk(ChunkParams p, const Launch& L) {
     p.negate = p.scale_log2 < 0.0f;
     if (p.negate) p.scale_log2 = -p.scale_log2;
     if (p.scale_log2 < 1e-37f) p.scale_log2 = 1e-37f;
-    if (p.D == 128)
-        return p.kv == kKvBf16 ? launch<128, kKvBf16>(p, grid, L)
-               : p.kv == kKvI8 ? launch<128, kKvI8>(p, grid, L) : launch<128, kKvI4>(p, grid, L);
-    if (p.D == 64)
-        return p.kv == kKvBf16 ? launch<64, kKvBf16>(p, grid, L)
-               : p.kv == kKvI8 ? launch<64, kKvI8>(p, grid, L) : launch<64, kKvI4>(p, grid, L);
+    if (p.D == 128) return launch_kind<128>(p, grid, L);
+    if (p.D == 64) return launch_kind<64>(p, grid, L);
     return cudaErrorInvalidValue;
 }
 
