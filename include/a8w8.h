@@ -492,10 +492,10 @@ a8w8_status paged_chunk_attention_bf16(const a8w8_bf16* q, const a8w8_bf16* k_ca
                                        a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
 
 /* The same over the INT8 cache: K_t and V_t are codes times row scales. Arguments,
- * workspace and errors as above. The products' operands are FP16: q and K of a
- * run of 128 tokens count to 2^-28 of their largest |value| (a query head's, a
- * run's), V to 2^-28 of the largest so far in its head, INT8 values and the
- * weights besides to 2^-10 and 2^-11 of themselves. */
+ * workspace and errors as above. The products' operands are FP16: q counts to 2^-28
+ * of its head's largest |value|, K to 2^-27 of that of its run of 128 tokens, V to
+ * 2^-27 of the largest up to and with its run (of a row 127 times its scale); INT8
+ * values and the weights besides to 2^-10 and 2^-11 of themselves. */
 a8w8_status paged_chunk_attention_i8kv(const a8w8_bf16* q, const int8_t* k_codes,
                                        const int8_t* v_codes, const float* k_scale,
                                        const float* v_scale, const int32_t* block_table,
@@ -504,7 +504,8 @@ a8w8_status paged_chunk_attention_i8kv(const a8w8_bf16* q, const int8_t* k_codes
                                        int max_blocks, int num_blocks, float softmax_scale,
                                        a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
 
-/* The same over the 4-bit cache: code * s + m, rounded to FP16 once (2^-11). */
+/* The same over the 4-bit cache: code * s + m, rounded to FP16 once (2^-11, and K
+ * and V to 2^-26 of the largest as above). */
 a8w8_status paged_chunk_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
                                        const uint8_t* v_codes, const a8w8_bf16* k_meta,
                                        const a8w8_bf16* v_meta, const int32_t* block_table,

@@ -453,6 +453,29 @@ def test_attention_ranges(kind, what):
     _check(got, want, bound, owned)
 
 
+@gpu
+@pytest.mark.parametrize("kind", ["i8", "i4"])
+@pytest.mark.parametrize("step", [8, 11, 14, 16, 18, 20])
+@pytest.mark.parametrize("which", [0, 1])
+def test_small_rows_beside_large_ones(kind, step, which):
+    """The second half of each context is 2^step times the first in its keys or its values; the rows
+    of the first half see small ones only, which FP16 holds to the stated part of the large ones in
+    the same run of 128, their scales and pairs, too."""
+    reqs, Hq, Hkv, D, page = [(7, 7), (120, 120), (200, 200), (80, 90)], 10, 2, 128, 16
+    q, arrays, values, bt, ctx, starts = _case(kind, 300 + step, reqs, Hq, Hkv, D, page)
+    for b, (_, c) in enumerate(reqs):
+        t = np.arange(c // 2, c)
+        at = bt[b][t // page] * page + t % page
+        if kind == "i8":
+            arrays[2 + which][at] *= np.float32(2.0 ** step)
+        else:
+            arrays[2 + which][at] = _bf(oracle.bf16_to_f64(arrays[2 + which][at]) * 2.0 ** step)
+    values[which] = (kv_i4.dequant_rows(arrays[which], arrays[2 + which]) if kind == "i4" else
+                     arrays[which] * arrays[2 + which].astype(np.float64)[..., None])
+    want, bound, owned = chunk.attention(q, *values, bt, ctx, starts, page, kind=kind)
+    _check(_run(kind, q, arrays, bt, ctx, starts, page), want, bound, owned)
+
+
 def _poison(kind, arrays, values, which, slot, h, d, x):
     """Value x (an infinity or NaN) into row (slot, h): at dimension d (BF16), or the whole row by its
     scale or pair."""

@@ -665,10 +665,14 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
 // INT8 and 4-bit rows become FP16 on the way into the ring: value 2^-E, E a
 // whole number per block for keys (the softmax takes the power of two back with
 // the scale) and for values one that only grows through a segment (O is in units
-// of it). A block's largest |value| comes to 16 at most, and of later blocks of
-// values to 2^15: FP16 holds a value to 2^-11 of itself, or 2^-28 of the largest
-// where that is more. 4-bit (s, m) pairs are BF16 and stay exact, an INT8 row's
-// scale is rounded to FP16 (2^-11), the value once more. (As BF16 rows, scores
+// of it). A block's largest |value| comes to between 8 and 16, and of later blocks of
+// values to 2^15. A rounding to FP16 is off by 2^-11 of what it rounds, or by 2^-25
+// below the normal numbers, which is 2^-28 of the largest value. An INT8 value has two,
+// its row's scale (taken as 128 s, times code / 128) and the product: 2^-10 of
+// itself, and 2^-27 of the largest. A 4-bit value has one, the sum's: pairs are BF16 and
+// exact but below FP16's normal numbers (8 s and m; 15 codes / 8 of the one): 2^-11 of
+// itself, and 2^-26 of the largest. (With s and code as they are, small rows' scales were
+// off by 2^-21 of the block's largest value. As BF16 rows, scores
 // would be off by 2^-8 of |q| |k|, several times what the weights' rounding
 // does.)
 //
@@ -753,17 +757,18 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
         if (KV == kKvI8) return (m & 0x7F800000u) == 0x7F800000u;
         return (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u;
     };
-    // a bound on the |values| of a finite row by its pair, as a float's bits but for a power of
-    // two: s, or twice the larger of |m| and 16 s
+    // the largest |value| of a finite row by its pair, as a float's bits: 128 s (2^7 times what
+    // this gives), or the larger of |m| and |m + 15 s|
     auto size_of = [&](uint32_t m) {
         if (odd_row(m)) return 0u;
         if (KV == kKvI8) return m & 0x7FFFFFFFu;
-        const unsigned sc = (m & 0x7FFFu) << 16;
-        return max(m & 0x7FFF0000u, sc ? sc + (4u << 23) : 0u);
+        const float least = __uint_as_float(m & 0xFFFF0000u);
+        return max(m & 0x7FFF0000u,
+                   __float_as_uint(__fmaf_rn(15.0f, __uint_as_float(m << 16), least)) & 0x7FFFFFFFu);
     };
     // e with |value| <= 2^e: -100 at least, -1000 for rows of zeros alone
     auto exponent_of = [](unsigned top) {
-        return top == 0 ? -1000 : min(max((int)(top >> 23) - 126 + (KV == kKvI8 ? 7 : 1), -100), 131);
+        return top == 0 ? -1000 : min(max((int)(top >> 23) - 126 + (KV == kKvI8 ? 7 : 0), -100), 131);
     };
     // Ring tile cnt from the thread's pieces of codes (pairs `meta` of the lanes' tokens) times `up`.
     // Where piece 0's chunks go. Lanes of one store in different banks: the second half of a
@@ -787,23 +792,25 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
             unsigned char* const row = tile + i * RPI * 128;
             const uint32_t flip = RPI == 4 && (i & 1) ? 64u : 0u;      // bit 2 of the row
             if (KV == kKvI8) {
-                const __half2 sc = __float2half2_rn(__uint_as_float(m) * up);
-                const __half2 off = as_half2(0x64806480u);           // 1152
+                // 128 s and code / 128 (exact): s alone would leave FP16's normal numbers 2^7 earlier
+                const __half2 sc = __float2half2_rn(__uint_as_float(m) * (up * 128.0f));
+                const __half2 by = as_half2(0x20002000u), off = as_half2(0xC880C880u);   // 2^-7, -1152 2^-7
 #pragma unroll
                 for (int e = 0; e < CPC; ++e) {
                     uint32_t o[4];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const uint32_t u = word[2 * e + g] ^ 0x80808080u;        // 1024 + 128 + code
-                        o[2 * g] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4140)), off), sc));
-                        o[2 * g + 1] = as_u32(__hmul2(__hsub2(as_half2(__byte_perm(u, 0x64646464u, 0x4342)), off), sc));
+                        o[2 * g] = as_u32(__hmul2(__hfma2(as_half2(__byte_perm(u, 0x64646464u, 0x4140)), by, off), sc));
+                        o[2 * g + 1] = as_u32(__hmul2(__hfma2(as_half2(__byte_perm(u, 0x64646464u, 0x4342)), by, off), sc));
                     }
                     *reinterpret_cast<uint4*>(row + (to[e] ^ flip)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             } else {
-                const float sf = __uint_as_float(m << 16) * up, mf = __uint_as_float(m & 0xFFFF0000u) * up;
-                const __half2 sc = __floats2half2_rn(sf, sf * 0.0625f), mn = __float2half2_rn(mf);
-                const __half2 off = as_half2(0x64006400u);           // 1024
+                // 8 s and code / 8 (exact), as above; 8 s is 1.07 times the largest |value| at most
+                const __half2 sc = __float2half2_rn(__uint_as_float(m << 16) * (up * 8.0f));
+                const __half2 mn = __float2half2_rn(__uint_as_float(m & 0xFFFF0000u) * up);
+                const __half2 by = as_half2(0x20003000u), off = as_half2(0xC800D800u);   // (2^-3, 2^-7), -1024 of them
 #pragma unroll
                 for (int e = 0; e < CPC; ++e) {
                     uint32_t o[4];
@@ -811,7 +818,7 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
                     for (int g = 0; g < 4; ++g) {
                         // 1024 + low nibble, 1024 + 16 times the high one
                         const uint32_t u = __byte_perm(word[e], 0x64646464u, 0x4040 + 0x0101 * g) & 0x64F0640Fu;
-                        o[g] = as_u32(__hfma2(__hsub2(as_half2(u), off), sc, mn));
+                        o[g] = as_u32(__hfma2(__hfma2(as_half2(u), by, off), sc, mn));
                     }
                     *reinterpret_cast<uint4*>(row + (to[e] ^ flip)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
