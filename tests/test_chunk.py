@@ -750,6 +750,31 @@ def test_offsets_past_32_bits(kind):
     _same_rows([c[torch.from_numpy(at).long().cuda()] for c in cache], small)
 
 
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 5)])
+def test_neighbouring_narrow_tiles_keep_their_own_statistics(kind, D, G):
+    """Tiles of 128 rows and fewer, of one and two blocks of keys, several to a CTA one behind the
+    other, whose scores and values are of very different sizes: each row is joined with its own
+    tile's statistics, in every call."""
+    rng = np.random.default_rng(D)
+    reqs = [(int(rng.integers(1, 5)), int(rng.integers(5, 250))) for _ in range(100)]
+    Hkv, page = 8, 16
+    n = sum(-(-c // page) for _, c in reqs) * page + 2 * page
+    q, arrays, values, bt, ctx, starts = _case(kind, 17, reqs, Hkv * G, Hkv, D, page,
+                                               v_scale=10.0 ** rng.uniform(-3, 3, n))
+    size = np.repeat(2.0 ** rng.integers(-4, 4, len(reqs)), [m for m, _ in reqs])
+    q = _bf(oracle.bf16_to_f64(q) * size[:, None, None])
+    want, bound, owned = chunk.attention(q, *values, bt, ctx, starts, page, kind=kind)
+    a8w8.read_device_errors()
+    dev = [to_dev(a) for a in (q, *arrays, bt, ctx, starts)]
+    first = _entry(kind, "attention")(*dev, page)
+    _check(first, want, bound, owned)
+    for _ in range(100):
+        assert (_entry(kind, "attention")(*dev, page) == first).all()
+    assert a8w8.read_device_errors() == 0
+
+
 # ---------------------------------------------------------------------------
 # together (GPU)
 # ---------------------------------------------------------------------------

@@ -1424,7 +1424,11 @@ __device__ void softmax(const ChunkParams& p, Ctl& ctl, unsigned char* q, float2
         const bool none = limit < 0;
         float up = ref, all = sum, u0 = 1.0f, u1 = 0.0f;
         if (narrow) {
-            // (read until o_free: a stream with blocks comes here again only after that)
+            // The segment before may be narrow, too, and its statistics still be read: a stream's
+            // first scores do not wait for its results, so with one block a stream is here before
+            // the other has left it.
+            ok = k == 0 || wait_bar(&ctl.o_free, (k - 1) & 1, &ctl.abort);
+            if (!ok) break;
             if (st == 0 || two) {
                 stat[kStreamRows * st + lr] = make_float2(ref, sum);
                 if (!idle) ctl.v_unit[st] = unit;  // (the same in all of these)
