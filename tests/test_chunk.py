@@ -775,6 +775,37 @@ def test_neighbouring_narrow_tiles_keep_their_own_statistics(kind, D, G):
     assert a8w8.read_device_errors() == 0
 
 
+def _poison_tokens(kind, arrays, values, bt, page, tokens):
+    """(request, token, kind of value) of `tokens`: infinities and NaN there in every KV head's values."""
+    for b, t, x in tokens:
+        at = bt[b][t // page] * page + t % page
+        for h in range(values[1].shape[1]):
+            _poison(kind, arrays, values, 1, at, h, (7 * t + 3 * h) % values[1].shape[2], x)
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 5)])
+def test_values_that_are_not_finite_in_neighbouring_tiles(kind, D, G):
+    """Every tile of a CTA holds some that only part of its rows see, in rows that different warps
+    bring: no tile waits for a later one."""
+    rng = np.random.default_rng(D + 1)
+    reqs = [(n, int(rng.integers(n, 129))) for n in rng.integers(2, 60, 72).tolist()]
+    Hkv, page = 8, 16
+    q, arrays, values, bt, ctx, starts = _case(kind, 19, reqs, Hkv * G, Hkv, D, page)
+    odd = [(b, int(rng.integers(c - n + 1, c)), rng.choice([np.nan, np.inf, -np.inf]))
+           for b, (n, c) in enumerate(reqs) for _ in range(3) if b % 9]
+    _poison_tokens(kind, arrays, values, bt, page, odd)
+    want, bound, owned = chunk.attention(q, *values, bt, ctx, starts, page, kind=kind)
+    assert 0.2 < np.isfinite(want).mean() < 0.99
+    a8w8.read_device_errors()
+    dev = [to_dev(a) for a in (q, *arrays, bt, ctx, starts)]
+    for _ in range(20):
+        got = _entry(kind, "attention")(*dev, page)
+    _check(got, want, bound, owned)
+    assert a8w8.read_device_errors() == 0
+
+
 # ---------------------------------------------------------------------------
 # together (GPU)
 # ---------------------------------------------------------------------------

@@ -88,6 +88,7 @@ struct Ctl {
     long first;                    // and that tile's first unit
     int v_unit[2];                 // narrow tiles: a stream's O is in units of 2^this
     int bad_tile;                  // the segment that bad[] is about, -1 for none
+    volatile int looked[4];        // warps that bring values: the segments before this are looked over
     uint32_t tmem;
     volatile int abort, never;     // never: always 0
 };
@@ -498,19 +499,29 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
 // token) are looked over as they are loaded: an infinity or NaN becomes zero and
 // is noted by its dimension as the first token that has a NaN, plus or minus
 // infinity there (ten bits each, counted from `base`); the rows that see it get
-// it back at the end. One segment at a time holds the notes.
+// it back at the end. One segment at a time holds the notes, in their order: the warps
+// that look do not wait for one another, and a segment ends only when all of its values
+// have come, so an earlier one must never find the notes held by a later one.
 constexpr uint32_t kNoBad = 0x3FFFFFFFu;
 struct BadValues {
     uint32_t* words;      // [D]
     Ctl& ctl;
+    unsigned* err;
     __device__ __forceinline__ static int base(const Seg& s) { return (s.pos0 + 1) & ~(kKeys - 1); }
     // kind 0: NaN, 1: infinity, 2: minus infinity
     __device__ __noinline__ void note(int seg, int token, int d, int kind) {
         const uint64_t t0 = globaltimer_ns();
         for (;;) {
-            const int owner = atomicCAS(&ctl.bad_tile, -1, seg);
-            if (owner == -1 || owner == seg) break;
-            if (ctl.abort || globaltimer_ns() - t0 > 2000000000ull) return;   // a wait that gives up elsewhere
+            if (min(min(ctl.looked[0], ctl.looked[1]), min(ctl.looked[2], ctl.looked[3])) >= seg) {
+                __threadfence_block();
+                const int owner = atomicCAS(&ctl.bad_tile, -1, seg);
+                if (owner == -1 || owner == seg) break;
+            }
+            if (ctl.abort) return;
+            if (globaltimer_ns() - t0 > 2000000000ull) {
+                set_timeout(err, &ctl.abort);
+                return;
+            }
         }
         uint32_t old = words[d], was;
         do {
@@ -520,6 +531,12 @@ struct BadValues {
             const uint32_t now = (was & ~(1023u << (10 * kind))) | ((uint32_t)token << (10 * kind));
             old = atomicCAS(&words[d], was, now);
         } while (old != was);
+    }
+    // By warp w of those that bring values: what it does next is segment seg's.
+    __device__ __forceinline__ void come_to(int seg, int w) const {
+        __threadfence_block();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ctl.looked[w] = seg;
     }
     __device__ __forceinline__ bool any(int seg) const {
         return *reinterpret_cast<volatile int*>(&ctl.bad_tile) == seg;
@@ -643,6 +660,7 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
                     cp_async_wait_group<1>();
                     look_over();
                 }
+                if (v == 0 && j == s.j0) bad.come_to(s.k, w);     // (before this segment's first values)
                 const int lo = s.pos0 + 1 - j * kKeys, hi = s.kend - j * kKeys;
                 if (v == 1 && lo < kKeys && hi > max(lo, 0)) {
                     look.st = st;
@@ -864,6 +882,7 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
         else if (e > ev + 11) ev = e;
         if (threadIdx.x % 128 == 0)
             fac[blk % kFacRing] = make_float2(pow2(min(ek - 4, 127)), __int_as_float(min(ev - 4, 127)));
+        if (x.first) bad.come_to(x.s.k, w);
         uint32_t pair_of = m.x, vmine = m.y;
         float up = pow2(max(4 - ek, -126));
 #pragma unroll 1
@@ -1536,6 +1555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         mbar_init(&ctl.done, 1);
         ctl.abort = ctl.never = 0;
         ctl.bad_tile = -1;
+        for (int i = 0; i < 4; ++i) ctl.looked[i] = 0;
         mbar_init_fence();
     }
     if (warp == 12) tmem_alloc(&ctl.tmem, kTmemCols);
@@ -1549,7 +1569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
     // Registers: a launch gives every thread 128; their sum over the four groups of
     // four warps stays 512.
     constexpr bool kBf = KV == kKvBf16;
-    const BadValues bad = {reinterpret_cast<uint32_t*>(smem + Y::bad), ctl};
+    const BadValues bad = {reinterpret_cast<uint32_t*>(smem + Y::bad), ctl, p.err};
     float2* fac = reinterpret_cast<float2*>(smem + Y::fac);
     if (warp < 8) {
         set_max_regs_inc<152>();
