@@ -778,9 +778,10 @@ def test_neighbouring_narrow_tiles_keep_their_own_statistics(kind, D, G):
 def _poison_tokens(kind, arrays, values, bt, page, tokens):
     """(request, token, kind of value) of `tokens`: infinities and NaN there in every KV head's values."""
     for b, t, x in tokens:
-        at = bt[b][t // page] * page + t % page
+        at = slice(bt[b][t // page] * page + t % page, None)
+        a, v = [c[at][:1] for c in arrays], [c[at][:1] for c in values]      # (views of the one slot)
         for h in range(values[1].shape[1]):
-            _poison(kind, arrays, values, 1, at, h, (7 * t + 3 * h) % values[1].shape[2], x)
+            _poison(kind, a, v, 1, 0, h, (7 * t + 3 * h) % values[1].shape[2], x)
 
 
 @gpu
@@ -800,6 +801,30 @@ def test_values_that_are_not_finite_in_neighbouring_tiles(kind, D, G):
     assert 0.2 < np.isfinite(want).mean() < 0.99
     a8w8.read_device_errors()
     dev = [to_dev(a) for a in (q, *arrays, bt, ctx, starts)]
+    for _ in range(20):
+        got = _entry(kind, "attention")(*dev, page)
+    _check(got, want, bound, owned)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,prior,G,D", [(8, 122, 2, 128), (4, 126, 5, 64), (60, 100, 2, 64), (3, 126, 4, 128),
+                                         (30, 230, 1, 128)])
+def test_values_that_are_not_finite_in_narrow_tiles_across_a_block(kind, n, prior, G, D):
+    """Neighbouring tiles of two and three blocks of keys whose first block with unseen tokens holds
+    such values, in every KV head: what a tile notes of them waits for the last one's notes to be
+    read, and for nothing behind it."""
+    B, Hkv, page = 48, 8, 16
+    ctx = n + prior
+    q, arrays, values, bt, ctxs, starts = _case(kind, 29, [(n, ctx)] * B, Hkv * G, Hkv, D, page)
+    last = prior + 1 | 1                    # in the block of the first unseen token, behind it
+    odd = [(b, t, x) for b in range(B) if b % 8 for t, x in ((last, np.nan if b % 2 else np.inf), (ctx - 1, -np.inf))]
+    _poison_tokens(kind, arrays, values, bt, page, odd)
+    want, bound, owned = chunk.attention(q, *values, bt, ctxs, starts, page, kind=kind)
+    assert prior < last < ctx and 0.1 < np.isfinite(want).mean() < 1
+    a8w8.read_device_errors()
+    dev = [to_dev(a) for a in (q, *arrays, bt, ctxs, starts)]
     for _ in range(20):
         got = _entry(kind, "attention")(*dev, page)
     _check(got, want, bound, owned)
