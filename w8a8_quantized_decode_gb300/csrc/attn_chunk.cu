@@ -88,7 +88,6 @@ struct Ctl {
     long first;                    // and that tile's first unit
     int v_unit[2];                 // narrow tiles: a stream's O is in units of 2^this
     int bad_tile;                  // the segment that bad[] is about, -1 for none
-    volatile int looked[4];        // warps that bring values: the segments before this are looked over
     uint32_t tmem;
     volatile int abort, never;     // never: always 0
 };
@@ -499,21 +498,22 @@ __device__ __forceinline__ void find_part(const ChunkParams& p, Ctl& ctl, void* 
 // token) are looked over as they are loaded: an infinity or NaN becomes zero and
 // is noted by its dimension as the first token that has a NaN, plus or minus
 // infinity there (ten bits each, counted from `base`); the rows that see it get
-// it back at the end. One segment at a time holds the notes, in their order: the warps
-// that look do not wait for one another, and a segment ends only when all of its values
-// have come, so an earlier one must never find the notes held by a later one.
+// it back at the end. One segment at a time holds the notes, in their order: a segment ends
+// only when all of its values have come, so an earlier one must never find the notes
+// held by a later one.
 constexpr uint32_t kNoBad = 0x3FFFFFFFu;
 struct BadValues {
     uint32_t* words;      // [D]
     Ctl& ctl;
     unsigned* err;
     __device__ __forceinline__ static int base(const Seg& s) { return (s.pos0 + 1) & ~(kKeys - 1); }
-    // kind 0: NaN, 1: infinity, 2: minus infinity
-    __device__ __noinline__ void note(int seg, int token, int d, int kind) {
+    // kind 0: NaN, 1: infinity, 2: minus infinity. `before`: the barrier (and the phase) by
+    // which all have looked over the segments before, null where that is known.
+    __device__ __noinline__ void note(int seg, int token, int d, int kind, uint64_t* before = nullptr,
+                                      unsigned parity = 0) {
         const uint64_t t0 = globaltimer_ns();
         for (;;) {
-            if (min(min(ctl.looked[0], ctl.looked[1]), min(ctl.looked[2], ctl.looked[3])) >= seg) {
-                __threadfence_block();
+            if (!before || mbar_test(before, parity)) {
                 const int owner = atomicCAS(&ctl.bad_tile, -1, seg);
                 if (owner == -1 || owner == seg) break;
             }
@@ -531,12 +531,6 @@ struct BadValues {
             const uint32_t now = (was & ~(1023u << (10 * kind))) | ((uint32_t)token << (10 * kind));
             old = atomicCAS(&words[d], was, now);
         } while (old != was);
-    }
-    // By warp w of those that bring values: what it does next is segment seg's.
-    __device__ __forceinline__ void come_to(int seg, int w) const {
-        __threadfence_block();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) ctl.looked[w] = seg;
     }
     __device__ __forceinline__ bool any(int seg) const {
         return *reinterpret_cast<volatile int*>(&ctl.bad_tile) == seg;
@@ -602,8 +596,13 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
     Seg s;
     bool ok = true;
     // a tile of values that is still to be looked over: its ring tile, segment, rows
-    // [lo, hi) and the first row's token from BadValues::base
-    struct { int st, seg, lo, hi, tok; } look = {-1, 0, 0, 0, 0};
+    // [lo, hi), the first row's token from BadValues::base, its number and that of its
+    // segment's first tile
+    struct { int st, seg, lo, hi, tok; unsigned at, first; } look = {-1, 0, 0, 0, 0, 0, 0};
+    // The warps do not wait for one another here. All have looked over the segments before
+    // when the tile before this segment has come. From kSt tiles behind it on that is so,
+    // as its place in the ring was free again; up to there its barrier cannot be past the
+    // phase behind it, which needs this warp.
     auto look_over = [&]() {
         unsigned char* tile = kvp + look.st * tile_bytes<D>();
 #pragma unroll 1
@@ -619,7 +618,10 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
             for (int e = 0; e < 8; ++e) {
                 const uint32_t h = (u[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
                 if ((h & 0x7F80u) != 0x7F80u) continue;
-                bad.note(look.seg, look.tok + row, 8 * c + e, h & 0x7Fu ? 0 : h & 0x8000u ? 2 : 1);
+                const unsigned prev = look.first - 1;
+                const bool ask = look.first && look.at - prev < kSt;
+                bad.note(look.seg, look.tok + row, 8 * c + e, h & 0x7Fu ? 0 : h & 0x8000u ? 2 : 1,
+                         ask ? &ctl.kv_full[prev % kSt] : nullptr, (prev / kSt) & 1);
                 u[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
             }
             v = make_uint4(u[0], u[1], u[2], u[3]);
@@ -629,6 +631,7 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
         look.st = -1;
     };
     while (ok && walk.next(s)) {
+        const unsigned first = cnt;
         Look next = look_up(p, s.b, s.kend, s.j0 * kKeys + 32 * w + lane);
         for (int j = s.j0; ok && j < s.j1; ++j) {
             const int slot = slot_of(p, next);
@@ -660,7 +663,6 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
                     cp_async_wait_group<1>();
                     look_over();
                 }
-                if (v == 0 && j == s.j0) bad.come_to(s.k, w);     // (before this segment's first values)
                 const int lo = s.pos0 + 1 - j * kKeys, hi = s.kend - j * kKeys;
                 if (v == 1 && lo < kKeys && hi > max(lo, 0)) {
                     look.st = st;
@@ -668,6 +670,8 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
                     look.lo = lo;
                     look.hi = hi;
                     look.tok = j * kKeys - BadValues::base(s);
+                    look.at = cnt;
+                    look.first = first;
                 } else {
                     cp_async_arrive(&ctl.kv_full[st]);
                 }
@@ -697,7 +701,7 @@ __device__ void load_bf16(const ChunkParams& p, Ctl& ctl, uint32_t kv, unsigned 
 // The codes and the pairs come by asynchronous copies into rings of their own
 // (feed_codes). The four converting warps wait for one another once a block, for
 // the largest pair of their quarters (each reading all pairs instead took 3000
-// clocks of a block's 7900).
+// clocks of a block's 7900), so that all have looked over the blocks before.
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 // The power of two 2^e, e in [-126, 127].
@@ -882,7 +886,6 @@ __device__ void convert_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, unsi
         else if (e > ev + 11) ev = e;
         if (threadIdx.x % 128 == 0)
             fac[blk % kFacRing] = make_float2(pow2(min(ek - 4, 127)), __int_as_float(min(ev - 4, 127)));
-        if (x.first) bad.come_to(x.s.k, w);
         uint32_t pair_of = m.x, vmine = m.y;
         float up = pow2(max(4 - ek, -126));
 #pragma unroll 1
@@ -1559,7 +1562,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const ChunkPara
         mbar_init(&ctl.done, 1);
         ctl.abort = ctl.never = 0;
         ctl.bad_tile = -1;
-        for (int i = 0; i < 4; ++i) ctl.looked[i] = 0;
         mbar_init_fence();
     }
     if (warp == 12) tmem_alloc(&ctl.tmem, kTmemCols);
