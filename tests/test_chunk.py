@@ -260,6 +260,77 @@ def test_append_many_rows_have_the_exact_values_rounding(D):
     _same_rows([q] + cache, [wq, wk, wv])
 
 
+FAR = [
+    # (name, exponents of the rows' values, of the weights (None: no norm), eps, position)
+    ("norm of large heads", 70, 0, 1e-6, 5), ("norm of the largest heads", 125, 0, 1e-6, 5),
+    ("norm of heads of all sizes", (-60, 120), 0, 1e-6, 5), ("norm of tiny heads, no eps", -100, 0, 0.0, 5),
+    ("norm of tiny heads, tiny eps", -90, 0, 1e-36, 5), ("large weights", 55, 100, 1e-6, 5),
+    ("the largest weights", 0, 126, 1e-6, 5), ("tiny weights", 0, -90, 1e-6, 5),
+    ("large eps", 0, 0, 1e30, 5), ("sums past the largest", 126.5, None, 1e-6, 5)]
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name,size,wsize,eps,at", FAR, ids=[f[0] for f in FAR])
+def test_append_of_far_values(kind, D, name, size, wsize, eps, at):
+    """Heads whose squares, products with the weight or rotations leave float32's range have the exact
+    values' roundings as others (below 2^-100 to the last bit: such values count as equal here)."""
+    T, Hq, Hkv = 9, 3, 2
+    rng = np.random.default_rng(D)
+    shape = (T, (Hq + 2 * Hkv) * D)
+    e = rng.integers(*size, shape) if isinstance(size, tuple) else size
+    qkv = rng.normal(size=shape) * 2.0 ** e
+    qkv[:, (Hq + Hkv) * D:] = rng.normal(size=(T, Hkv * D))
+    qkv = _bf(np.clip(qkv, -3e38, 3e38))
+    w = None if wsize is None else _bf(np.clip(rng.normal(1, 0.1, D) * 2.0 ** wsize, -3e38, 3e38))
+    pos = np.full(T, at, np.int32)
+    slots = np.arange(T, dtype=np.int32)
+    host = _empty_cache(kind, T, Hkv, D)
+    dev = [to_dev(a) for a in host]
+    rope = a8w8.a8w8_rope_table(16, D, THETA)
+    dw = None if w is None else to_dev(w)
+    q = _entry(kind, "append")(to_dev(qkv), to_dev(pos), to_dev(slots), rope, *dev, 1, q_norm_w=dw, k_norm_w=dw,
+                               eps=eps)
+    with np.errstate(all="ignore"):
+        wq, wk, wv, live = chunk.append(qkv, Hq, Hkv, D, pos, 16, THETA, w, w, eps)
+    rows, exact = [(q, wq)], []
+    if kind == "bf16":
+        rows += zip(dev, (wk, wv))
+    elif np.isfinite(oracle.bf16_to_f64(wk)).all():
+        _fill(kind, host, wk, wv, slots, live)
+        exact = [dev, host]
+    for g, x in rows:
+        g, x = oracle.bf16_to_f64(to_host(g)), oracle.bf16_to_f64(x)
+        same = (g == x) | (np.isnan(g) & np.isnan(x)) | (np.maximum(np.abs(g), np.abs(x)) < 2.0 ** -100)
+        assert same.all(), (g[~same][:4], x[~same][:4])
+    _same_rows(*exact or ([], []))
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("at", [0, 5])
+def test_append_of_infinities_and_nan(D, norm, at):
+    """An infinity or NaN in a head is where the formulas have it: the other values of its pair by the
+    rotation alone; of a normed head itself, beside zeros, and all of them with a NaN."""
+    T, Hq, Hkv = 6, 3, 2
+    qkv = synth.bf16_normal(D, (T, (Hq + 2 * Hkv) * D))
+    for t, d, x in ((0, 3, np.inf), (1, D + 40, -np.inf), (2, Hq * D + D // 2, np.inf), (3, Hq * D + 1, np.nan),
+                    (4, 0, np.inf), (4, D // 2, np.inf), (5, 7, np.inf), (5, 8, np.nan)):
+        qkv[t, d] = _bf(x)
+    w = to_dev(_bf(np.random.default_rng(D).normal(1, 0.1, D))) if norm else None
+    pos, slots = np.full(T, at, np.int32), np.arange(T, dtype=np.int32)
+    cache = [to_dev(a) for a in _empty_cache("bf16", T, Hkv, D)]
+    rope = a8w8.a8w8_rope_table(16, D, THETA)
+    q = a8w8.paged_kv_append(to_dev(qkv), to_dev(pos), to_dev(slots), rope, *cache, 1, q_norm_w=w, k_norm_w=w)
+    hw = None if w is None else to_host(w)
+    with np.errstate(all="ignore"):
+        wq, wk, wv, _ = chunk.append(qkv, Hq, Hkv, D, pos, 16, THETA, hw, hw, 1e-6)
+    assert not np.isfinite(oracle.bf16_to_f64(wq)).all() and not np.isfinite(oracle.bf16_to_f64(wk)).all()
+    _same_rows([q] + cache, [wq, wk, wv])
+
+
 @gpu
 def test_append_equals_the_layers_own_rows():
     """The decode layer's taps of its rotated queries and keys, and the cache it wrote, bit for bit."""

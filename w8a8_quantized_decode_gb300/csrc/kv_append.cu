@@ -98,6 +98,41 @@ __device__ __noinline__ int4 norm_exact(int4 raw, int4 y, unsigned open, const b
     return y;
 }
 
+// An overflow of pairs of floats is NaN: r, or where it is not finite the float's value.
+__device__ __forceinline__ bf16 finite_or(bf16 r, float plain) {
+    return (__bfloat16_as_ushort(r) & 0x7F80u) == 0x7F80u ? f2bf(plain) : r;
+}
+
+// The same for heads whose squares, or products with a weight, leave float32's range: the
+// head and eps in units that bring the largest |x| to about 1 and eps to 4 at most.
+// Beside an infinity, every finite value norms to zero.
+template <int D>
+__device__ __noinline__ int4 norm_far(int4 raw, int4 y, unsigned open, const bf16* w, float eps) {
+    float x[8];
+    unpack8(raw, x);
+    unsigned top = 0u;                   // the largest |x|, as bits: NaN is above infinity
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int unit = (int)(top >> 23) - 126;
+    if (eps > 0.0f) unit = max(unit, ((int)(__float_as_uint(eps) >> 23) - 127) >> 1);
+    const float up = __uint_as_float((unsigned)(127 - min(max(unit, -126), 126)) << 23);
+    f2 ss = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f2_acc(ss, __fmul_rn(__fmul_rn(x[e], up), __fmul_rn(x[e], up)));
+    f2 inv = rms_inv(row_sum_f2<D / 8>(ss), D, __fmul_rn(__fmul_rn(eps, up), up));
+    if (top == 0x7F800000u) inv = f2{0.0f, 0.0f};
+#pragma unroll 1
+    for (; open; open &= open - 1) {
+        const int e = __ffs(open) - 1;
+        const f2 v = f2_mulf(inv, __fmul_rn(value(raw, e), up));
+        const float we = bf2f(w[(e & 3) + (e >> 2) * (D / 2)]);
+        put(y, e, finite_or(f2_to_bf16(f2_mulf(v, we)), __fmul_rn(v.hi, we)));
+    }
+    return y;
+}
+
 // Of the lane's 8 values x those in `open` rotated in pairs of floats, in place of
 // those in y. `rope` is the lane's first angle in the position's row of the table.
 template <int D>
@@ -106,9 +141,10 @@ __device__ __noinline__ int4 rotate_exact(int4 x, int4 y, unsigned open, const f
     for (; open; open &= open - 1) {
         const int e = __ffs(open) - 1;
         const float* t = rope + (e & 3);
-        const f2 a = f2_mulf(f2{t[0], t[D]}, value(x, e));
-        const f2 b = f2_mulf(f2{t[D / 2], t[3 * D / 2]}, value(x, e ^ 4));
-        put(y, e, f2_to_bf16(e & 4 ? f2_add(a, b) : f2_sub(a, b)));
+        const float xa = value(x, e), xb = value(x, e ^ 4);
+        const f2 a = f2_mulf(f2{t[0], t[D]}, xa), b = f2_mulf(f2{t[D / 2], t[3 * D / 2]}, xb);
+        put(y, e, finite_or(f2_to_bf16(e & 4 ? f2_add(a, b) : f2_sub(a, b)),
+                            e & 4 ? t[0] * xa + t[D / 2] * xb : t[0] * xa - t[D / 2] * xb));
     }
     return y;
 }
@@ -119,17 +155,24 @@ __device__ __forceinline__ void unpack_pairs(const int4& v, f32x2 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
 }
+// Whether some |weight| is 2^59 or more: of a head whose sum of squares is finite, |x|
+// is below 2^64.
+__device__ __forceinline__ bool far_weights(const int4& w) {
+    const unsigned a = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    return max(a >> 16, a & 0xFFFFu) >= (127u + 59u) << 7;
+}
 __device__ __forceinline__ unsigned bf16x2(f32x2 v) {
     float a, b;
     split(v, a, b);
     return as_u32(__floats2bfloat162_rn(a, b));
 }
 
-// The lane's 8 values of a head, normed (with w) and rotated: in float32, both ends
-// of the interval that holds the exact value rounded to BF16, and where those
-// differ by the above.
+// The lane's 8 values of a head, normed (with w, where the mean square is from 10^-12 to
+// `limit` by this) and rotated: in float32, both ends of the interval that holds the
+// exact value rounded to BF16, and where those differ by the above.
 template <int D>
-__device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf)[4], float eps,
+__device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf)[4], float limit, float eps,
                                        const float* rope, const f32x2 (&c)[2], const f32x2 (&s)[2]) {
     constexpr int LPR = D / 8;
     f32x2 x[4];
@@ -143,6 +186,7 @@ __device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float square = __fmaf_rn(ss, 1.0f / D, eps), inv = __frsqrt_rn(square);
         unsigned open = 0u;
+        const bool in = square > 1e-12f && square < limit;
         if (w) {
             const float lo = inv * (1.0f - kNormErr), hi = inv * (1.0f + kNormErr);
             const f32x2 lo2 = pair(lo, lo), hi2 = pair(hi, hi);
@@ -158,11 +202,13 @@ __device__ __forceinline__ int4 rotate(int4 raw, const bf16* w, const f32x2 (&wf
                 differ[e] = o[e] ^ bf16x2(mul2(t, hi2));
             }
             xn = make_int4(o[0], o[1], o[2], o[3]);
-            // (products out of the normal numbers' range have other errors)
-            if ((small < 1e-17f && ss != 0.0f) || !(square > 1e-30f && square < 3e38f)) open = 0xFFu;
+            // (products out of the normal numbers' range have other errors; zeros among them,
+            // which are exact, come here too)
+            if ((small < 1e-17f && ss != 0.0f) || !in) open = 0xFFu;
             else if ((differ[0] | differ[1]) | (differ[2] | differ[3])) open = open_of(differ);
         }
-        if (__any_sync(0xffffffffu, open != 0u)) xn = norm_exact<D>(raw, xn, open, w, eps);
+        if (__any_sync(0xffffffffu, open != 0u))
+            xn = __all_sync(0xffffffffu, in) ? norm_exact<D>(raw, xn, open, w, eps) : norm_far<D>(raw, xn, open, w, eps);
         unpack_pairs(xn, x);
     }
     const f32x2 up = pair(kRotErr, kRotErr), down = pair(-kRotErr, -kRotErr), minus = pair(-1.0f, -1.0f);
@@ -266,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(const AppendPara
     const bf16 *wq = p.q_norm_w ? p.q_norm_w + 4 * j : nullptr, *wk = p.k_norm_w ? p.k_norm_w + 4 * j : nullptr;
     f32x2 wf[4];
     const bf16* w = nullptr;
+    float limit = 3e38f;                 // of the mean square, 0 for far weights
     int kind = -1;                       // of the heads that w belongs to: queries, keys
     int4 next = load(h0);
 #pragma unroll 1
@@ -283,10 +330,12 @@ __global__ void __launch_bounds__(kThreads, 7) kv_append_kernel(const AppendPara
                 w = mine ? wk : wq;
                 if (w) {
                     const int2* from = reinterpret_cast<const int2*>(w);
-                    unpack_pairs(halves(from[0], from[D / 8]), wf);
+                    const int4 packed = halves(from[0], from[D / 8]);
+                    unpack_pairs(packed, wf);
+                    limit = far_weights(packed) ? 0.0f : 3e38f;
                 }
             }
-            const int4 y = rotate<D>(v, w, wf, p.eps, rope, c, s);
+            const int4 y = rotate<D>(v, w, wf, limit, p.eps, rope, c, s);
             if (at < p.Hq + p.Hkv) v = y;
         }
         if (at < p.Hq) {
