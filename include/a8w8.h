@@ -432,8 +432,8 @@ size_t a8w8_attention_i4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_
  *   xn = bf16_rne( x / sqrt(mean(x^2) + eps) * w ),
  * and rotated (rotate-half, table of a8w8_rope_table with max_pos rows),
  *   y = bf16_rne( rotation of xn ),
- * each rounding that of the exact value, as the layers have it. The queries go
- * to q_rot ([T, Hq, D]; nullable: they are left out), keys and values to
+ * each rounding that of the exact value (below 2^-100 the last bit may differ). The
+ * queries go to q_rot ([T, Hq, D]; nullable: they are left out), keys and values to
  * slot_mapping[t] of the cache (paged_kv_write's). positions[t] < 0 is a padded
  * row: zeros in q_rot, nothing in the cache; so is positions[t] >= max_pos, which
  * flags A8W8_DEVERR_POS. slot_mapping[t] < 0 leaves the cache alone; a slot >=
