@@ -154,6 +154,21 @@ def test_binding_refuses_wrong_tensors():
                             1e-6, None, None, -1)
 
 
+def test_binding_refuses_heads_of_another_size_and_rows_too_far_apart():
+    import torch
+    for dtype in (torch.bfloat16, torch.int8):      # queries of 64 over a cache of 128: whole pages all the same
+        z = torch.zeros((32, 2, 128), dtype=dtype)
+        with pytest.raises(a8w8.A8W8Error, match=r"\[slots, 2, 64\]"):
+            a8w8._cache_rows((z, z), dtype, 2, 64, 16, "x", -1)
+        with pytest.raises(a8w8.A8W8Error, match=r"\[slots, 2, 128\]"):
+            a8w8._cache_rows((z, z.view(64, 2, 64)), dtype, 2, 128, 16, "x", -1)
+    far = torch.empty_strided((2, 6 * 64), (2 ** 32 + 6 * 64, 1), dtype=torch.bfloat16, device="meta")
+    assert far.stride(0) % 2 ** 32 == 6 * 64                 # what a 32-bit stride would pass for
+    with pytest.raises(a8w8.A8W8Error, match="apart"):
+        a8w8._kv_append("paged_kv_append", far, None, None, torch.zeros((4, 128)), [], 2, 16, 2, 64, None, None,
+                        1e-6, None, None, far.get_device())
+
+
 @pytest.mark.parametrize("name", ["kv_append.cu", "attn_chunk.cu", "quant_i4.cuh"])
 def test_no_read_only_loads_beside_the_producer(name):
     """These kernels start beside the one before them, which may write what they read: no load of

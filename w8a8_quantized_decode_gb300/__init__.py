@@ -706,7 +706,8 @@ def chunk_attention_workspace_bytes(T, B, Hq, Hkv, D, max_ctx) -> int:
 def _cache_rows(data, dtype, Hkv, D, page_size, what, dev):
     """Pointers and page count of K and V rows [slots, Hkv, D] in whole pages."""
     n = data[0].numel()
-    if Hkv <= 0 or D <= 0 or page_size <= 0 or n % (Hkv * D * page_size) or data[1].numel() != n:
+    if Hkv <= 0 or D <= 0 or page_size <= 0 or n % (Hkv * D * page_size) or data[1].numel() != n or \
+            any(t.shape[-1] != D for t in data):
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: caches [slots, {Hkv}, {D}] of whole pages of "
                         f"{page_size} tokens expected")
     return [_typed(t, dtype, what, dev) for t in data], n // (Hkv * D * page_size)
@@ -747,6 +748,8 @@ def _kv_append(what, qkv, positions, slot_mapping, rope, ptrs, num_blocks, page_
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: rows of {cols} elements are not Hq + 2 x {Hkv} "
                         f"heads of {D}")
     ld = qkv.stride(0) if T > 1 else cols
+    if ld >= 2 ** 31:
+        raise A8W8Error(ERR_UNSUPPORTED_SHAPE, f"{what}: rows {ld} elements apart, 2^31 - 1 at most")
     if rope.dim() != 2 or rope.shape[1] != 2 * D:
         raise A8W8Error(ERR_INVALID_ARG, f"{what}: the rope table is [max_pos, {2 * D}]")
     if q_out is None:
