@@ -798,6 +798,45 @@ def test_attention_long_prompt(kind):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_prompt_of_8192_tokens(D):
+    """A BF16 prompt long enough for the longer code, whole: some rows against the oracle."""
+    import torch
+    n, Hq, Hkv, page = 8192, 40, 8, 128
+    q, arrays, values, bt, ctx, starts = _case("bf16", 92, [(n, n)], Hq, Hkv, D, page)
+    rows = np.array([0, 1, 51, 127, 128, 4095, 4096, 6143, n - 2, n - 1])
+    want, bound, _ = chunk.attention(q[rows], *values, np.repeat(bt, len(rows), 0), 1 + rows,
+                                     np.arange(len(rows) + 1), page)
+    got = _run("bf16", q, arrays, bt, ctx, starts, page)
+    _check(got[torch.from_numpy(rows).cuda()], want, bound)
+    assert a8w8.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_of_a_long_chunk(kind):
+    """8192 tokens of 40 / 8 heads, a warp all heads of a token: some rows bit for bit, pages in any
+    order."""
+    import torch
+    T, Hq, Hkv, D, page, first = 8192, 40, 8, 128, 128, 1234
+    rng = np.random.default_rng(93)
+    qkv = synth.bf16_normal(93, (T, (Hq + 2 * Hkv) * D), std=2.0)
+    slots = (rng.permutation(T // page)[:, None] * page + np.arange(page)).reshape(-1).astype(np.int32)
+    pos = np.arange(first, first + T, dtype=np.int32)
+    w = _bf(rng.normal(1, 0.2, D))
+    dev = [to_dev(a) for a in _empty_cache(kind, T, Hkv, D)]
+    rope = a8w8.a8w8_rope_table(first + T, D, THETA)
+    q = _entry(kind, "append")(to_dev(qkv), to_dev(pos), to_dev(slots), rope, *dev, page, q_norm_w=to_dev(w),
+                               k_norm_w=to_dev(w))
+    rows = np.concatenate(([0, 1, T - 1], rng.permutation(T)[:60]))
+    wq, wk, wv, live = chunk.append(qkv[rows], Hq, Hkv, D, pos[rows], first + T, THETA, w, w)
+    small = _empty_cache(kind, len(rows), Hkv, D)
+    _fill(kind, small, wk, wv, np.arange(len(rows)), live)
+    at = torch.from_numpy(slots[rows]).long().cuda()
+    _same_rows([q[torch.from_numpy(rows).cuda()]] + [c[at] for c in dev], [wq] + small)
+
+
+@gpu
 @pytest.mark.slow
 @pytest.mark.parametrize("kind", KINDS)
 def test_offsets_past_32_bits(kind):
