@@ -474,7 +474,8 @@ a8w8_status paged_kv_append_i4(const a8w8_bf16* qkv, int T, int Hq, int Hkv, int
  * q_starts[B] on belong to no request, and their rows of out stay as they are.
  * Products are exact, sums float32; the weights are rounded to BF16 (2^-8) before
  * the product with V, out to BF16 once. A value that is infinite or NaN reaches
- * the rows that see its token, no others; a NaN score makes its row NaN.
+ * the rows that see its token, no others (an infinity as NaN where its weight rounds
+ * to zero); a NaN score makes its row NaN.
  * ws: a8w8_chunk_attention_workspace_bytes of the same T, B, Hq, Hkv, D and
  * max_blocks * page_size; its contents need no initialisation, and calls that
  * share it must not overlap on the GPU. On the device: a context outside [0,
@@ -505,7 +506,8 @@ a8w8_status paged_chunk_attention_i8kv(const a8w8_bf16* q, const int8_t* k_codes
                                        a8w8_bf16* out, void* ws, size_t ws_bytes, void* stream);
 
 /* The same over the 4-bit cache: code * s + m, rounded to FP16 once (2^-11, and K
- * and V to 2^-26 of the largest as above). */
+ * and V to 2^-26 of the largest as above). A batch of single tokens alone is faster by
+ * paged_decode_attention_i4kv. */
 a8w8_status paged_chunk_attention_i4kv(const a8w8_bf16* q, const uint8_t* k_codes,
                                        const uint8_t* v_codes, const a8w8_bf16* k_meta,
                                        const a8w8_bf16* v_meta, const int32_t* block_table,

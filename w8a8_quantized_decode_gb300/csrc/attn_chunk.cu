@@ -30,12 +30,13 @@
 // the same bits.
 //
 // Measured (GB300, a graph's launch; 40 heads on 8 of 128 where not said):
-//   a prompt of 16384 tokens, BF16        1.91 ms, 1440 TFLOP/s of 1920
-//   512 tokens at 16384, BF16             147 us, 1150 TFLOP/s
-//   4 prompts of 512, BF16                33 us
+//   a prompt of 16384 tokens, BF16        1.93 ms, 1420 TFLOP/s of 1920
+//   the same, INT8 and 4-bit              2.75 and 2.59 ms, 1000 and 1060 TFLOP/s
+//   512 tokens at 16384, BF16             152 us, 1110 TFLOP/s
+//   4 prompts of 512, BF16                34 us
 //   16 single tokens past 63 to 4095      39 us, 3.5 TB/s of 6.8
-//   64 x 4 drafts past 64 to 4096, 4-bit  143 us, 1.1 TB/s
-//   16 requests of 1 to 512 tokens, INT8  214 us, 620 TFLOP/s
+//   64 x 4 drafts past 64 to 4096, 4-bit  147 us, 1.0 TB/s
+//   16 requests of 1 to 512 tokens, INT8  215 us, 620 TFLOP/s
 // Long ones are bound by a stream's chain S -> softmax -> P -> O of a block (2900 clocks
 // for both streams' blocks, 2048 of them products); INT8 and 4-bit ones by the
 // conversion (3500 to 4400 a block); short ones by the start: 7000 clocks to find the
@@ -1132,8 +1133,12 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
 // Matrix products: one warp, of which one thread issues them
 //
 // Scores of a block overwrite the weights of the stream's block before, which
-// the product issued just before reads: products of one thread go through the
-// SM's tensor pipe in the order of their issue. A commit covers all products
+// the product issued just before reads. Nothing but the order of issue is between the
+// two: this assumes that the products of one thread go through the SM's tensor pipe
+// in that order. What the PTX ISA promises of it is about products of the same
+// accumulator and shape; here the accumulators differ (O and S), and for D = 64 the
+// shapes, too (N = 64 and 128). It has held in every run; to wait for the product
+// with V instead would leave the pipe idle twice a block. A commit covers all products
 // before it, so that of a block's scores tells the softmax that the product with
 // V before them is done, too.
 // True in one thread of the (converged) warp. Under this predicate the compiler
@@ -1680,7 +1685,8 @@ cudaError_t launch(const ChunkParams& p, int grid, const Launch& L) {
     cfg.attrs = attr;
     cfg.numAttrs = L.pdl ? 1 : 0;
     if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
-    // (no second launch for contexts of up to 256 keys: 5 tokens past 32, 9.2 -> 8.2 us)
+    // (no second launch for tables of up to 256 keys: 5 tokens past 32, 9.2 -> 8.2 us; with a
+    // wider table they keep it, as the host does not know the contexts)
     if (grid == 1 || !may_divide(blocks_of(p.max_blocks * p.page))) return cudaSuccess;
     cfg.gridDim = dim3(grid - 1, (p.part_rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
@@ -1696,13 +1702,14 @@ int max_parts(int T, int B, int G, int Hkv, int max_ctx) {
     return (int)std::min<long>(kMaxParts, (units + kMinUnits - 1) / kMinUnits);
 }
 
-// Over a BF16 cache, requests of half a wide tile and more on average with contexts of up
-// to so many blocks take the longer code of the softmax: a prompt of 16384 1969 -> 1912 us,
+// Over a BF16 cache, requests of half a wide tile and more on average with a table for so
+// many blocks of keys and more take the longer code of the softmax: a prompt of 16384 1969 -> 1912 us,
 // 512 tokens at 16384 150 -> 147, a prompt of 8192 with heads of 64 386 -> 362, 8 requests
 // of 256 to 1024 tokens past 1000 to 6000 276 -> 271. Shorter ones lose by it, as their CTAs
 // spend much of their time on code that no cache holds yet: 4 prompts of 512 33 -> 36, 16
 // requests of 1 to 256 tokens past 100 to 4000 103 -> 106; and single tokens: 64 past 1000
-// to 8000 193 -> 195.
+// to 8000 193 -> 195. The table's width stands for the contexts, which only the device knows:
+// 4 prompts of 512 with a table for 16384 keys take 37.5 instead of 33.5.
 constexpr int kLongBlocks = 48;
 
 template <int D>

@@ -6,9 +6,9 @@
 //   xn = bf16( x w / sqrt(mean x^2 + eps) ),
 //   y_i = bf16( xn_i c_i - xn_{i+D/2} s_i ), y_{i+D/2} = bf16( xn_{i+D/2} c_i + xn_i s_i ),
 // c + i s = e^{i p theta^{-2i/D}} from the table of hi + lo float pairs, each
-// rounding that of the exact value (as the layers' norm_rope_head). Keys and
-// values then are stored as they are, or quantised by the row (quant.cu,
-// kv_i4.cu).
+// rounding that of the exact value (as the layers' norm_rope_head has it for squares
+// in float32's range). Keys and values then are stored as they are, or quantised by
+// the row (quant.cu, kv_i4.cu).
 //
 // What bounds it: HBM, 2 (Hq + 2 Hkv) D bytes of a token in, 2 Hq D and the
 // cache's row out. What stands against it is arithmetic: in pairs of floats
@@ -28,9 +28,10 @@
 // and cosines in registers; how many turns a warp takes depends on the number of
 // tokens (launch).
 //
-// Measured (GB300, a graph's launch): 16384 tokens of 40 / 8 heads of 128, BF16: 128 us,
-// 3.7 TB/s of 6.8 that a copy reaches; some 250 instructions a turn of 256 values keep the
-// issue slots two thirds busy. One token: 2.6 us.
+// Measured (GB300, a graph's launch): 16384 tokens of 40 / 8 heads of 128, BF16: 130 us,
+// 3.7 TB/s of 6.8 that a copy reaches (INT8 154, 4-bit 144); some 250 instructions a turn of
+// 256 values keep the issue slots 70 % busy. 64 tokens: 4.7 us, one: 2.6. A zero takes its
+// lane's eight values past the float32 form: with one in most heads the 16384 tokens take 436 us.
 #include <algorithm>
 
 #include "kernels.cuh"
