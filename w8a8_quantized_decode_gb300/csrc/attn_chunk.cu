@@ -1238,13 +1238,12 @@ __device__ void issue_mma(const ChunkParams& p, Ctl& ctl, uint32_t q, uint32_t k
             // block j goes to stream j % 2. Block 1's keys come behind the look over block 0's
             // values, which waits for the last segment's notes to be cleared: where there are
             // any (they are complete, with that segment's last values), that comes first.
-            const bool noted = k > 0 && bad.any(k - 1);
-            for (int j = 0; ok && j < min(2, nb); ++j) {
-                if (j == 1 && noted) ok = free_o();
-                ok = ok && wait_full(cnt + 2 * j);
-                if (ok) qk(j, q_half(k, true), cnt + 2 * j, true, j + 1 == nb ? q_free : nullptr);
+            const int m = min(2, nb), at = k > 0 && nb > 1 && bad.any(k - 1) ? 1 : m;
+            for (int j = 0; ok && j <= m; ++j) {
+                if (j == at) ok = free_o();
+                if (j == m || !(ok = ok && wait_full(cnt + 2 * j))) break;
+                qk(j, q_half(k, true), cnt + 2 * j, true, j + 1 == nb ? q_free : nullptr);
             }
-            ok = ok && (noted && nb > 1 || free_o());
             for (int j = 0; ok && j < nb; ++j) {
                 const unsigned tv = cnt + 2 * j + 1, tk = tv + 3;
                 const bool more = j + 2 < nb;
