@@ -35,8 +35,8 @@
 //   512 tokens at 16384, BF16             152 us, 1110 TFLOP/s
 //   4 prompts of 512, BF16                34 us
 //   16 single tokens past 63 to 4095      39 us, 3.5 TB/s of 6.8
-//   64 x 4 drafts past 64 to 4096, 4-bit  147 us, 1.0 TB/s
-//   16 requests of 1 to 512 tokens, INT8  215 us, 620 TFLOP/s
+//   64 x 4 drafts past 64 to 4096, 4-bit  146 us, 1.0 TB/s
+//   16 requests of 1 to 512 tokens, INT8  214 us, 620 TFLOP/s
 // Long ones are bound by a stream's chain S -> softmax -> P -> O of a block (2900 clocks
 // for both streams' blocks, 2048 of them products); INT8 and 4-bit ones by the
 // conversion (3500 to 4400 a block); short ones by the start: 7000 clocks to find the
@@ -1137,8 +1137,9 @@ __device__ void feed_codes(const ChunkParams& p, Ctl& ctl, CodesCtl& cc, uint32_
 // two: this assumes that the products of one thread go through the SM's tensor pipe
 // in that order. What the PTX ISA promises of it is about products of the same
 // accumulator and shape; here the accumulators differ (O and S), and for D = 64 the
-// shapes, too (N = 64 and 128). It has held in every run; to wait for the product
-// with V instead would leave the pipe idle twice a block. A commit covers all products
+// shapes, too (N = 64 and 128). It has held in every run; a wait for the product with V
+// before each S instead costs 2 to 7 % (a prompt of 16384 1933 -> 2019 us, 16 mixed
+// requests, INT8, 214 -> 226, 4 prompts of 512 35.4 -> 36.2). A commit covers all products
 // before it, so that of a block's scores tells the softmax that the product with
 // V before them is done, too.
 // True in one thread of the (converged) warp. Under this predicate the compiler
